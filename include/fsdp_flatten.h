@@ -58,7 +58,7 @@ extern "C" {
 #define FSDP_API
 #endif
 
-#define FSDP_ABI_VERSION 3
+#define FSDP_ABI_VERSION 4
 #define FSDP_ALL_RANKS (-1)
 #define FSDP_MAX_NDIM 8
 
@@ -463,6 +463,207 @@ FSDP_API fsdp_status fsdp_grad_sqnorm(const fsdp_unit* unit, int32_t k, const fl
  */
 FSDP_API fsdp_status fsdp_grad_sqnorm_noalloc(const fsdp_unit* unit, int32_t k, const float* grad,
                                               double* out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Layer operators: what a transformer block computes around its matrix
+ * products between the copy-out and the gradient reduction, with the
+ * activations the backward pass needs saved in 8 bits.  The norms' weights and
+ * the biases are parameters of the unit; their gradients come out in the form
+ * fsdp_grad_accumulate's accumulator (fp32, added in place at
+ * fsdp_unit_param_offset) or the copy-in (bf16) takes.
+ *
+ * Activations are rows x cols matrices (rows: tokens), bf16 or fp32, row i
+ * starting at data + i * pitch elements.  Rows may start at any element.  An
+ * input's pitch may be any value >= 0 (0: every row is the same one); an
+ * output's is at least cols when there is more than one row.  What lies in an
+ * output between a row's end and the next row's start, and behind the last
+ * row, stays as it was.  Arithmetic is fp32; a result is rounded once, to
+ * nearest even, when it is stored.  Results do not depend on the device's load:
+ * every sum has a fixed order that the sizes alone set (rows and columns; for
+ * one matrix the same whatever its pitch and address).
+ * No operand may overlap an output.  The current device must be the one the
+ * buffers and the stream belong to.
+ * rows == 0 or cols == 0: nothing is read or written, except that with rows ==
+ * 0 the gradients of weight and bias are sums of nothing (0 is written, or
+ * nothing added).
+ * ------------------------------------------------------------------------ */
+
+typedef enum { FSDP_BF16 = 1, FSDP_F32 = 2 } fsdp_dtype;
+
+/* How an 8-bit activation checkpoint holds a row: groups of FSDP_CKPT_GROUP
+ * consecutive columns (the row's last group may be shorter) share one scale, a
+ * power of two 2^s held as the byte s + 127; an element is a code times its
+ * group's scale.  s is the smallest power at which the group's largest
+ * magnitude, rounded to nearest even, is a code:
+ *   FSDP_CKPT_E4M3 : codes are 8-bit floats (sign, 4 exponent bits of bias 7, 3
+ *     mantissa bits; largest 448, no infinity); |x| / 2^s <= 464, s >= -124.
+ *     Off by at most 2^-4 of the element's own size (half of 2^(s-9) below
+ *     2^(s-6)): for groups with outliers.
+ *   FSDP_CKPT_INT8 : codes are integers -127..127 in two's complement;
+ *     |x| / 2^s < 127.5, s >= -127.  Off by at most half of 2^s, 1/128 of
+ *     the group's largest magnitude: for groups of similar magnitudes.
+ * Rounding is to nearest, ties to even.  Every value a code stands for is a
+ * bf16 number, so reading back is exact in bf16 and fp32 (one exception: an
+ * element that rounds to 2^128 reads back as infinity).  A group
+ * that holds an infinity or a NaN gets the scale byte 255 and reads back as NaN
+ * throughout. */
+typedef enum { FSDP_CKPT_E4M3 = 1, FSDP_CKPT_INT8 = 2 } fsdp_ckpt_format;
+#define FSDP_CKPT_GROUP 32
+
+typedef enum {
+    FSDP_NORM_LAYER = 1,   /* (x - mean) * rstd * weight + bias, rstd = 1/sqrt(var + eps)  */
+    FSDP_NORM_RMS = 2      /* x * rstd * weight (+ bias), rstd = 1/sqrt(mean(x^2) + eps)   */
+} fsdp_norm_kind;
+
+typedef enum {
+    FSDP_ACT_RELU = 1,
+    FSDP_ACT_GELU = 2,       /* x Phi(x); Phi to an absolute 1e-7                           */
+    FSDP_ACT_GELU_TANH = 3,  /* x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2             */
+    FSDP_ACT_SILU = 4        /* x / (1 + e^-x)                                              */
+} fsdp_act_kind;
+
+/* One activation matrix; data NULL: not given. */
+typedef struct {
+    void* data;
+    int64_t pitch;         /* elements from one row's start to the next one's   */
+} fsdp_rows;
+
+/* An 8-bit activation checkpoint of a rows x cols matrix. */
+typedef struct {
+    uint8_t* codes;        /* device pointer, cols bytes a row                    */
+    uint8_t* scales;       /* device pointer, ceil(cols / FSDP_CKPT_GROUP) a row  */
+    int64_t code_pitch;    /* bytes from one row's codes to the next one's        */
+    int64_t scale_pitch;
+    int32_t format;        /* an fsdp_ckpt_format                                 */
+    int32_t reserved;      /* ignored; set it to 0                                */
+} fsdp_ckpt;
+
+typedef struct {
+    int64_t rows, cols;    /* cols < 2^31                                         */
+    int32_t dtype;         /* of the activations and their gradients              */
+    int32_t param_dtype;   /* norms: of weight and bias                           */
+    int32_t grad_dtype;    /* backward: of dweight and dbias                      */
+    int32_t accumulate;    /* backward, non-zero: add to what dweight and dbias
+                              hold (in fp32, rounded once)                        */
+    int32_t kind;          /* an fsdp_norm_kind, or an fsdp_act_kind              */
+    float eps;             /* norm forward: finite, >= 0                          */
+} fsdp_layer_cfg;
+
+typedef struct {
+    fsdp_rows x;
+    fsdp_rows residual;    /* optional: the norm is of x + residual, rounded to dtype       */
+    fsdp_rows sum;         /* optional, with residual: that sum, stored                     */
+    fsdp_rows y;
+    const void* weight;    /* cols elements of param_dtype                                  */
+    const void* bias;      /* optional                                                      */
+    float* mean;           /* rows floats (FSDP_NORM_LAYER; else ignored, may be NULL)      */
+    float* rstd;           /* rows floats                                                   */
+    const fsdp_ckpt* ckpt; /* optional: receives the norm's input in 8 bits                 */
+} fsdp_norm_fwd;
+
+typedef struct {
+    fsdp_rows dy;
+    fsdp_rows x;           /* the norm's input, or NULL where ckpt holds it                 */
+    fsdp_rows dres;        /* optional: added to dx (the residual stream's gradient)        */
+    fsdp_rows dx;
+    fsdp_rows y;           /* optional: receives the norm's output again                    */
+    const fsdp_ckpt* ckpt; /* the norm's input in 8 bits, or NULL                           */
+    const void* weight;
+    const void* bias;      /* optional, read for y only                                     */
+    const float* mean;     /* as the forward pass wrote them                                */
+    const float* rstd;
+    void* dweight;         /* optional: cols elements of grad_dtype                         */
+    void* dbias;           /* optional                                                      */
+    float* workspace;      /* device pointer, 16-byte aligned                               */
+    int64_t workspace_len; /* floats, at least fsdp_norm_workspace                          */
+} fsdp_norm_bwd;
+
+typedef struct {
+    fsdp_rows x;
+    fsdp_rows y;
+    const fsdp_ckpt* ckpt; /* optional: receives x in 8 bits                                */
+} fsdp_act_fwd;
+
+typedef struct {
+    fsdp_rows dy;
+    fsdp_rows x;           /* the activation's input, or NULL where ckpt holds it           */
+    fsdp_rows dx;
+    fsdp_rows y;           /* optional: receives the activation's output again              */
+    const fsdp_ckpt* ckpt;
+    void* dbias;           /* optional: cols elements of grad_dtype                         */
+    float* workspace;      /* device pointer, 16-byte aligned; unused without dbias         */
+    int64_t workspace_len; /* floats, at least fsdp_act_workspace                           */
+} fsdp_act_bwd;
+
+/*
+ * Save rows x cols activations in 8 bits (see fsdp_ckpt_format).
+ *   x : the activations, of `dtype`.   ckpt : host pointer, read during the call.
+ * Errors: FSDP_E_ARG (NULL ckpt; with elements, a NULL buffer), FSDP_E_RANGE
+ * (rows or cols negative, cols >= 2^31, dtype, format, a pitch), FSDP_E_ALIGN (x
+ * not aligned to its element size), FSDP_E_OVERFLOW (a buffer's extent beyond
+ * int64), FSDP_E_HIP.
+ */
+FSDP_API fsdp_status fsdp_ckpt_pack(int64_t rows, int64_t cols, int32_t dtype, fsdp_rows x,
+                                    const fsdp_ckpt* ckpt, void* stream);
+
+/* The values a checkpoint holds, as bf16 or fp32.  Errors as fsdp_ckpt_pack. */
+FSDP_API fsdp_status fsdp_ckpt_unpack(int64_t rows, int64_t cols, int32_t dtype,
+                                      const fsdp_ckpt* ckpt, fsdp_rows x, void* stream);
+
+/*
+ * LayerNorm or RMSNorm of every row, with the statistics its backward pass
+ * needs, optionally after a residual add and with an 8-bit checkpoint of the
+ * norm's input.  The variance is summed over (x - mean)^2.
+ * Errors: FSDP_E_ARG (NULL cfg or io; with elements, a NULL x, y, weight or rstd,
+ * a NULL mean with FSDP_NORM_LAYER, a sum without a residual, a ckpt with a NULL
+ * buffer), FSDP_E_RANGE (sizes, dtypes, kind, eps, a pitch, the ckpt's format),
+ * FSDP_E_ALIGN, FSDP_E_OVERFLOW, FSDP_E_HIP.
+ */
+FSDP_API fsdp_status fsdp_norm_forward(const fsdp_layer_cfg* cfg, const fsdp_norm_fwd* io,
+                                       void* stream);
+
+/* Floats of workspace fsdp_norm_backward needs for these sizes.  Host only. */
+FSDP_API fsdp_status fsdp_norm_workspace(int64_t rows, int64_t cols, int64_t* n_floats);
+
+/*
+ * Backward pass of fsdp_norm_forward, from the norm's input or its 8-bit
+ * checkpoint.  With xh = (x - mean) * rstd (mean 0 for FSDP_NORM_RMS) and
+ * g = dy * weight:
+ *   dx      = rstd * (g - mean(g) - xh * mean(g * xh)) + dres   (RMS: no mean(g))
+ *   dweight = (accumulate ? dweight : 0) + sum over rows of dy * xh
+ *   dbias   = (accumulate ? dbias : 0) + sum over rows of dy
+ *   y       = xh * weight + bias
+ * Every partial sum read was written by the same call: the workspace needs no
+ * clearing, and calls that share one must be ordered (on one stream, or in one
+ * graph).
+ * Errors: FSDP_E_ARG (as fsdp_norm_forward; with elements, a NULL dy, dx,
+ * weight, rstd or workspace, a NULL mean with FSDP_NORM_LAYER, both or neither
+ * of x and ckpt), FSDP_E_RANGE (also workspace_len), FSDP_E_ALIGN,
+ * FSDP_E_OVERFLOW, FSDP_E_HIP.
+ */
+FSDP_API fsdp_status fsdp_norm_backward(const fsdp_layer_cfg* cfg, const fsdp_norm_bwd* io,
+                                        void* stream);
+
+/*
+ * An MLP's activation, y = f(x), optionally with an 8-bit checkpoint of x.
+ * Errors as fsdp_norm_forward.
+ */
+FSDP_API fsdp_status fsdp_act_forward(const fsdp_layer_cfg* cfg, const fsdp_act_fwd* io,
+                                      void* stream);
+
+/* Floats of workspace fsdp_act_backward needs for dbias.  Host only. */
+FSDP_API fsdp_status fsdp_act_workspace(int64_t rows, int64_t cols, int64_t* n_floats);
+
+/*
+ * Backward pass of fsdp_act_forward, from its input or the 8-bit checkpoint:
+ *   dx    = dy * f'(x)         (f' of ReLU at 0 is 0)
+ *   dbias = (accumulate ? dbias : 0) + sum over rows of dx before its rounding,
+ *           the gradient of a bias that was added to make x
+ *   y     = f(x)
+ * Errors as fsdp_norm_backward (the workspace only with a dbias).
+ */
+FSDP_API fsdp_status fsdp_act_backward(const fsdp_layer_cfg* cfg, const fsdp_act_bwd* io,
+                                       void* stream);
 
 #ifdef __cplusplus
 }

@@ -16,7 +16,7 @@ FSDP_FLAT = 1
 FSDP_ROWS = 2
 FSDP_ALL_RANKS = -1
 FSDP_MAX_NDIM = 8
-ABI_VERSION = 3  # FSDP_ABI_VERSION of include/fsdp_flatten.h this binding marshals for
+ABI_VERSION = 4  # FSDP_ABI_VERSION of include/fsdp_flatten.h this binding marshals for
 
 STATUS_NAMES = {0: "FSDP_OK", 1: "FSDP_E_ARG", 2: "FSDP_E_RANGE", 3: "FSDP_E_ALIGN",
                 4: "FSDP_E_OVERFLOW", 5: "FSDP_E_NOMEM", 6: "FSDP_E_HIP",
@@ -468,4 +468,8 @@ ABI_FUNCTIONS = ["fsdp_abi_version", "fsdp_last_error", "fsdp_status_string", "f
                  "fsdp_flatten_shard_bf16", "fsdp_grad_reduce_shard_ex", "fsdp_grad_reduce_workspace",
                  "fsdp_grad_accumulate",
                  "fsdp_grad_unscale", "fsdp_grad_sqnorm_workspace", "fsdp_grad_sqnorm",
-                 "fsdp_grad_sqnorm_noalloc"]
+                 "fsdp_grad_sqnorm_noalloc",
+                 # the layer operators, bound in layer.py
+                 "fsdp_ckpt_pack", "fsdp_ckpt_unpack", "fsdp_norm_forward", "fsdp_norm_workspace",
+                 "fsdp_norm_backward", "fsdp_act_forward", "fsdp_act_workspace",
+                 "fsdp_act_backward"]

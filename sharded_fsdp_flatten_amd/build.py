@@ -32,7 +32,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libfsdpflat.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 
-SOURCES = ["kernels.hip", "plan.cpp", "fsdp_abi.cpp"]
+SOURCES = ["kernels.hip", "layer.hip", "plan.cpp", "fsdp_abi.cpp"]
 PROBE_LIB_PATH = os.path.join(HERE, "libfsdpprobe.so")
 PROBE_SOURCES = ["probes.hip"]
 

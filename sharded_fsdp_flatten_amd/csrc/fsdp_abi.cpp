@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "kernels.h"
+#include "layer.h"
 #include "plan.h"
 
 struct fsdp_unit {
@@ -158,6 +159,102 @@ std::vector<int64_t> param_numels(const fsdp::UnitPlan& u) {
     for (const auto& p : u.params) n.push_back(p.numel);
     return n;
 }
+
+// ---- layer operators ----
+
+fsdp_status check_extent(int64_t rows, int64_t cols) {
+    if (rows < 0) return fail(FSDP_E_RANGE, "rows must not be negative");
+    if (cols < 0 || cols > INT32_MAX) return fail(FSDP_E_RANGE, "cols must be in [0, 2^31)");
+    return FSDP_OK;
+}
+
+fsdp_status check_dtype(int32_t dtype, const char* name) {
+    if (dtype != FSDP_BF16 && dtype != FSDP_F32)
+        return fail(FSDP_E_RANGE, std::string(name) + " must be FSDP_BF16 or FSDP_F32");
+    return FSDP_OK;
+}
+
+size_t elem_size(int32_t dtype) { return dtype == FSDP_BF16 ? 2 : 4; }
+
+// rows x cols elements of `elem` bytes, rows `pitch` apart (`out`: rows must not overlap).
+fsdp_status check_rows(const void* p, int64_t pitch, int64_t rows, int64_t cols, size_t elem,
+                       bool out, const char* name) {
+    if (rows == 0 || cols == 0) return FSDP_OK;
+    fsdp_status s = check_buf(p, 1, elem, name);
+    if (s != FSDP_OK) return s;
+    if (pitch < 0) return fail(FSDP_E_RANGE, std::string(name) + "'s pitch is negative");
+    if (out && rows > 1 && pitch < cols)
+        return fail(FSDP_E_RANGE, std::string(name) + "'s pitch is below its columns");
+    int64_t n;
+    if (__builtin_mul_overflow(rows - 1, pitch, &n) || __builtin_add_overflow(n, cols, &n) ||
+        __builtin_mul_overflow(n, static_cast<int64_t>(elem), &n))
+        return fail(FSDP_E_OVERFLOW, std::string(name) + "'s extent overflows int64");
+    return FSDP_OK;
+}
+
+// A checkpoint's buffers, as the kernels take them.
+fsdp_status check_ckpt(const fsdp_ckpt* q, int64_t rows, int64_t cols, bool out, fsdp::CkptRows* to) {
+    if (q->format != FSDP_CKPT_E4M3 && q->format != FSDP_CKPT_INT8)
+        return fail(FSDP_E_RANGE, "ckpt's format must be FSDP_CKPT_E4M3 or FSDP_CKPT_INT8");
+    fsdp_status s;
+    const int64_t groups = (cols + FSDP_CKPT_GROUP - 1) / FSDP_CKPT_GROUP;
+    if ((s = check_rows(q->codes, q->code_pitch, rows, cols, 1, out, "ckpt's codes")) != FSDP_OK ||
+        (s = check_rows(q->scales, q->scale_pitch, rows, groups, 1, out, "ckpt's scales")) != FSDP_OK)
+        return s;
+    *to = {q->codes, q->scales, q->code_pitch, q->scale_pitch, q->format == FSDP_CKPT_INT8};
+    return FSDP_OK;
+}
+
+fsdp_status check_norm(const fsdp_layer_cfg* c) {
+    fsdp_status s;
+    if ((s = check_extent(c->rows, c->cols)) != FSDP_OK || (s = check_dtype(c->dtype, "dtype")) != FSDP_OK ||
+        (s = check_dtype(c->param_dtype, "param_dtype")) != FSDP_OK)
+        return s;
+    if (c->kind != FSDP_NORM_LAYER && c->kind != FSDP_NORM_RMS)
+        return fail(FSDP_E_RANGE, "kind must be FSDP_NORM_LAYER or FSDP_NORM_RMS");
+    return FSDP_OK;
+}
+
+fsdp_status check_act(const fsdp_layer_cfg* c) {
+    fsdp_status s;
+    if ((s = check_extent(c->rows, c->cols)) != FSDP_OK || (s = check_dtype(c->dtype, "dtype")) != FSDP_OK)
+        return s;
+    if (c->kind < FSDP_ACT_RELU || c->kind > FSDP_ACT_SILU)
+        return fail(FSDP_E_RANGE, "kind must be an fsdp_act_kind");
+    return FSDP_OK;
+}
+
+// The input of a backward pass: a tensor or a checkpoint of it.
+fsdp_status check_input(const fsdp_layer_cfg* c, const fsdp_rows& x, const fsdp_ckpt* ckpt,
+                        fsdp::CkptRows* to) {
+    if (c->rows == 0 || c->cols == 0) return FSDP_OK;
+    if ((x.data != nullptr) == (ckpt != nullptr))
+        return fail(FSDP_E_ARG, x.data ? "x and ckpt are both given" : "neither x nor ckpt is given");
+    if (ckpt) return check_ckpt(ckpt, c->rows, c->cols, false, to);
+    return check_rows(x.data, x.pitch, c->rows, c->cols, elem_size(c->dtype), false, "x");
+}
+
+fsdp_status check_workspace(const float* ws, int64_t len, int64_t need) {
+    if (need < 0) return fail(FSDP_E_OVERFLOW, "the workspace's size overflows int64");
+    if (need == 0) return FSDP_OK;
+    if (!ws) return fail(FSDP_E_ARG, "workspace is NULL; " + std::to_string(need) + " floats are needed");
+    if (!aligned_to(ws, 16)) return fail(FSDP_E_ALIGN, "workspace is not 16-byte aligned");
+    if (len < need)
+        return fail(FSDP_E_RANGE, "workspace holds " + std::to_string(len) + " floats; " +
+                                      std::to_string(need) + " are needed");
+    return FSDP_OK;
+}
+
+// dweight or dbias: cols elements of grad_dtype, or NULL.
+fsdp_status check_grad(const fsdp_layer_cfg* c, void* p, const char* name, fsdp::ColOut* to) {
+    *to = {p, c->grad_dtype == FSDP_BF16, c->accumulate != 0};
+    if (!p) return FSDP_OK;
+    const fsdp_status s = check_dtype(c->grad_dtype, "grad_dtype");
+    return s != FSDP_OK ? s : check_buf(p, 1, elem_size(c->grad_dtype), name);
+}
+
+fsdp::RowsIn in(const fsdp_rows& r) { return {r.data, r.pitch}; }
+fsdp::RowsOut out(const fsdp_rows& r) { return {r.data, r.pitch}; }
 
 }  // namespace
 
@@ -532,6 +629,213 @@ fsdp_status fsdp_grad_sqnorm_noalloc(const fsdp_unit* unit, int32_t k, const flo
         e = fsdp::launch_grad_sqnorm(grad, runs, partial, out, static_cast<hipStream_t>(stream));
         if (e != hipSuccess) return hip_fail(e, "fsdp_grad_sqnorm_noalloc launch");
         return ok();
+    });
+}
+
+fsdp_status fsdp_ckpt_pack(int64_t rows, int64_t cols, int32_t dtype, fsdp_rows x,
+                           const fsdp_ckpt* ckpt, void* stream) {
+    return guarded("fsdp_ckpt_pack", [&]() -> fsdp_status {
+        if (!ckpt) return fail(FSDP_E_ARG, "ckpt is NULL");
+        fsdp::ActFwd a{};
+        fsdp_status s;
+        if ((s = check_extent(rows, cols)) != FSDP_OK || (s = check_dtype(dtype, "dtype")) != FSDP_OK ||
+            (s = check_rows(x.data, x.pitch, rows, cols, elem_size(dtype), false, "x")) != FSDP_OK ||
+            (s = check_ckpt(ckpt, rows, cols, true, &a.ckpt)) != FSDP_OK)
+            return s;
+        if (rows == 0 || cols == 0) return ok();
+        a.rows = rows;
+        a.cols = cols;
+        a.bf16 = dtype == FSDP_BF16;
+        a.x = in(x);
+        const hipError_t e = fsdp::launch_act_forward(a, static_cast<hipStream_t>(stream));
+        return e != hipSuccess ? hip_fail(e, "fsdp_ckpt_pack launch") : ok();
+    });
+}
+
+fsdp_status fsdp_ckpt_unpack(int64_t rows, int64_t cols, int32_t dtype, const fsdp_ckpt* ckpt,
+                             fsdp_rows x, void* stream) {
+    return guarded("fsdp_ckpt_unpack", [&]() -> fsdp_status {
+        if (!ckpt) return fail(FSDP_E_ARG, "ckpt is NULL");
+        fsdp::CkptRows q{};
+        fsdp_status s;
+        if ((s = check_extent(rows, cols)) != FSDP_OK || (s = check_dtype(dtype, "dtype")) != FSDP_OK ||
+            (s = check_ckpt(ckpt, rows, cols, false, &q)) != FSDP_OK ||
+            (s = check_rows(x.data, x.pitch, rows, cols, elem_size(dtype), true, "x")) != FSDP_OK)
+            return s;
+        if (rows == 0 || cols == 0) return ok();
+        const hipError_t e = fsdp::launch_unpack(rows, cols, dtype == FSDP_BF16, q, out(x),
+                                                 static_cast<hipStream_t>(stream));
+        return e != hipSuccess ? hip_fail(e, "fsdp_ckpt_unpack launch") : ok();
+    });
+}
+
+fsdp_status fsdp_norm_forward(const fsdp_layer_cfg* cfg, const fsdp_norm_fwd* io, void* stream) {
+    return guarded("fsdp_norm_forward", [&]() -> fsdp_status {
+        if (!cfg || !io) return fail(FSDP_E_ARG, cfg ? "io is NULL" : "cfg is NULL");
+        fsdp_status s;
+        if ((s = check_norm(cfg)) != FSDP_OK) return s;
+        if (!std::isfinite(cfg->eps) || cfg->eps < 0.0f)
+            return fail(FSDP_E_RANGE, "eps must be finite and not negative");
+        const int64_t R = cfg->rows, C = cfg->cols;
+        const size_t e = elem_size(cfg->dtype), pe = elem_size(cfg->param_dtype);
+        const bool layer = cfg->kind == FSDP_NORM_LAYER;
+        if (io->sum.data && !io->residual.data) return fail(FSDP_E_ARG, "sum without a residual");
+        fsdp::NormFwd a{};
+        if ((s = check_rows(io->x.data, io->x.pitch, R, C, e, false, "x")) != FSDP_OK ||
+            (s = check_rows(io->y.data, io->y.pitch, R, C, e, true, "y")) != FSDP_OK ||
+            (io->residual.data &&
+             (s = check_rows(io->residual.data, io->residual.pitch, R, C, e, false, "residual")) != FSDP_OK) ||
+            (io->sum.data && (s = check_rows(io->sum.data, io->sum.pitch, R, C, e, true, "sum")) != FSDP_OK) ||
+            (io->ckpt && (s = check_ckpt(io->ckpt, R, C, true, &a.ckpt)) != FSDP_OK))
+            return s;
+        const int64_t any = R > 0 && C > 0;
+        if ((s = check_buf(io->weight, any, pe, "weight")) != FSDP_OK ||
+            (s = check_buf(io->bias, any && io->bias, pe, "bias")) != FSDP_OK ||
+            (s = check_buf(io->mean, any && layer, sizeof(float), "mean")) != FSDP_OK ||
+            (s = check_buf(io->rstd, any, sizeof(float), "rstd")) != FSDP_OK)
+            return s;
+        if (!any) return ok();
+        a.rows = R;
+        a.cols = C;
+        a.bf16 = cfg->dtype == FSDP_BF16;
+        a.param_bf16 = cfg->param_dtype == FSDP_BF16;
+        a.rms = !layer;
+        a.eps = cfg->eps;
+        a.x = in(io->x);
+        a.residual = in(io->residual);
+        a.sum = out(io->sum);
+        a.y = out(io->y);
+        a.weight = io->weight;
+        a.bias = io->bias;
+        a.mean = layer ? io->mean : nullptr;
+        a.rstd = io->rstd;
+        const hipError_t err = fsdp::launch_norm_forward(a, static_cast<hipStream_t>(stream));
+        return err != hipSuccess ? hip_fail(err, "fsdp_norm_forward launch") : ok();
+    });
+}
+
+fsdp_status fsdp_norm_workspace(int64_t rows, int64_t cols, int64_t* n_floats) {
+    return guarded("fsdp_norm_workspace", [&]() -> fsdp_status {
+        if (!n_floats) return fail(FSDP_E_ARG, "n_floats is NULL");
+        const fsdp_status s = check_extent(rows, cols);
+        if (s != FSDP_OK) return s;
+        const int64_t n = fsdp::norm_workspace_floats(rows, cols);
+        if (n < 0) return fail(FSDP_E_OVERFLOW, "the workspace's size overflows int64");
+        *n_floats = n;
+        return ok();
+    });
+}
+
+fsdp_status fsdp_norm_backward(const fsdp_layer_cfg* cfg, const fsdp_norm_bwd* io, void* stream) {
+    return guarded("fsdp_norm_backward", [&]() -> fsdp_status {
+        if (!cfg || !io) return fail(FSDP_E_ARG, cfg ? "io is NULL" : "cfg is NULL");
+        fsdp_status s;
+        if ((s = check_norm(cfg)) != FSDP_OK) return s;
+        const int64_t R = cfg->rows, C = cfg->cols;
+        const size_t e = elem_size(cfg->dtype), pe = elem_size(cfg->param_dtype);
+        const bool layer = cfg->kind == FSDP_NORM_LAYER;
+        fsdp::NormBwd a{};
+        if ((s = check_rows(io->dy.data, io->dy.pitch, R, C, e, false, "dy")) != FSDP_OK ||
+            (s = check_input(cfg, io->x, io->ckpt, &a.ckpt)) != FSDP_OK ||
+            (io->dres.data && (s = check_rows(io->dres.data, io->dres.pitch, R, C, e, false, "dres")) != FSDP_OK) ||
+            (s = check_rows(io->dx.data, io->dx.pitch, R, C, e, true, "dx")) != FSDP_OK ||
+            (io->y.data && (s = check_rows(io->y.data, io->y.pitch, R, C, e, true, "y")) != FSDP_OK))
+            return s;
+        const int64_t any = R > 0 && C > 0;
+        if ((s = check_buf(io->weight, any, pe, "weight")) != FSDP_OK ||
+            (s = check_buf(io->bias, any && io->bias, pe, "bias")) != FSDP_OK ||
+            (s = check_buf(io->mean, any && layer, sizeof(float), "mean")) != FSDP_OK ||
+            (s = check_buf(io->rstd, any, sizeof(float), "rstd")) != FSDP_OK ||
+            (s = check_grad(cfg, io->dweight, "dweight", &a.dweight)) != FSDP_OK ||
+            (s = check_grad(cfg, io->dbias, "dbias", &a.dbias)) != FSDP_OK ||
+            (s = check_workspace(io->workspace, io->workspace_len, fsdp::norm_workspace_floats(R, C))) != FSDP_OK)
+            return s;
+        if (C == 0) return ok();
+        a.rows = R;
+        a.cols = C;
+        a.bf16 = cfg->dtype == FSDP_BF16;
+        a.param_bf16 = cfg->param_dtype == FSDP_BF16;
+        a.rms = !layer;
+        a.dy = in(io->dy);
+        a.x = in(io->x);
+        a.dres = in(io->dres);
+        a.dx = out(io->dx);
+        a.y = out(io->y);
+        a.weight = io->weight;
+        a.bias = io->bias;
+        a.mean = layer ? io->mean : nullptr;
+        a.rstd = io->rstd;
+        a.workspace = io->workspace;
+        const hipError_t err = fsdp::launch_norm_backward(a, static_cast<hipStream_t>(stream));
+        return err != hipSuccess ? hip_fail(err, "fsdp_norm_backward launch") : ok();
+    });
+}
+
+fsdp_status fsdp_act_forward(const fsdp_layer_cfg* cfg, const fsdp_act_fwd* io, void* stream) {
+    return guarded("fsdp_act_forward", [&]() -> fsdp_status {
+        if (!cfg || !io) return fail(FSDP_E_ARG, cfg ? "io is NULL" : "cfg is NULL");
+        fsdp_status s;
+        if ((s = check_act(cfg)) != FSDP_OK) return s;
+        const int64_t R = cfg->rows, C = cfg->cols;
+        const size_t e = elem_size(cfg->dtype);
+        fsdp::ActFwd a{};
+        if ((s = check_rows(io->x.data, io->x.pitch, R, C, e, false, "x")) != FSDP_OK ||
+            (s = check_rows(io->y.data, io->y.pitch, R, C, e, true, "y")) != FSDP_OK ||
+            (io->ckpt && (s = check_ckpt(io->ckpt, R, C, true, &a.ckpt)) != FSDP_OK))
+            return s;
+        if (R == 0 || C == 0) return ok();
+        a.rows = R;
+        a.cols = C;
+        a.bf16 = cfg->dtype == FSDP_BF16;
+        a.f = cfg->kind;
+        a.x = in(io->x);
+        a.y = out(io->y);
+        const hipError_t err = fsdp::launch_act_forward(a, static_cast<hipStream_t>(stream));
+        return err != hipSuccess ? hip_fail(err, "fsdp_act_forward launch") : ok();
+    });
+}
+
+fsdp_status fsdp_act_workspace(int64_t rows, int64_t cols, int64_t* n_floats) {
+    return guarded("fsdp_act_workspace", [&]() -> fsdp_status {
+        if (!n_floats) return fail(FSDP_E_ARG, "n_floats is NULL");
+        const fsdp_status s = check_extent(rows, cols);
+        if (s != FSDP_OK) return s;
+        const int64_t n = fsdp::act_workspace_floats(rows, cols);
+        if (n < 0) return fail(FSDP_E_OVERFLOW, "the workspace's size overflows int64");
+        *n_floats = n;
+        return ok();
+    });
+}
+
+fsdp_status fsdp_act_backward(const fsdp_layer_cfg* cfg, const fsdp_act_bwd* io, void* stream) {
+    return guarded("fsdp_act_backward", [&]() -> fsdp_status {
+        if (!cfg || !io) return fail(FSDP_E_ARG, cfg ? "io is NULL" : "cfg is NULL");
+        fsdp_status s;
+        if ((s = check_act(cfg)) != FSDP_OK) return s;
+        const int64_t R = cfg->rows, C = cfg->cols;
+        const size_t e = elem_size(cfg->dtype);
+        fsdp::ActBwd a{};
+        if ((s = check_rows(io->dy.data, io->dy.pitch, R, C, e, false, "dy")) != FSDP_OK ||
+            (s = check_input(cfg, io->x, io->ckpt, &a.ckpt)) != FSDP_OK ||
+            (s = check_rows(io->dx.data, io->dx.pitch, R, C, e, true, "dx")) != FSDP_OK ||
+            (io->y.data && (s = check_rows(io->y.data, io->y.pitch, R, C, e, true, "y")) != FSDP_OK) ||
+            (s = check_grad(cfg, io->dbias, "dbias", &a.dbias)) != FSDP_OK)
+            return s;
+        if (io->dbias && (s = check_workspace(io->workspace, io->workspace_len,
+                                              fsdp::act_workspace_floats(R, C))) != FSDP_OK)
+            return s;
+        if (C == 0) return ok();
+        a.rows = R;
+        a.cols = C;
+        a.bf16 = cfg->dtype == FSDP_BF16;
+        a.f = cfg->kind;
+        a.dy = in(io->dy);
+        a.x = in(io->x);
+        a.dx = out(io->dx);
+        a.y = out(io->y);
+        a.workspace = io->workspace;
+        const hipError_t err = fsdp::launch_act_backward(a, static_cast<hipStream_t>(stream));
+        return err != hipSuccess ? hip_fail(err, "fsdp_act_backward launch") : ok();
     });
 }
 
