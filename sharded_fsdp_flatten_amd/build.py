@@ -21,9 +21,11 @@ A flag that matters for speed only:
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -32,7 +34,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libfsdpflat.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 
-SOURCES = ["kernels.hip", "layer.hip", "plan.cpp", "fsdp_abi.cpp"]
+SOURCES = ["kernels.hip", "layer.hip", "norm_backward_bf16.hip", "norm_backward_f32.hip",
+           "plan.cpp", "fsdp_abi.cpp"]
 PROBE_LIB_PATH = os.path.join(HERE, "libfsdpprobe.so")
 PROBE_SOURCES = ["probes.hip"]
 
@@ -43,7 +46,6 @@ FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-ffp-contract=off",
     "-fno-fast-math",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -54,16 +56,25 @@ FLAGS = [
 ]
 
 
-def _link(sources, path, verbose):
-    tmp = path + ".tmp%d" % os.getpid()
-    cmd = [HIPCC, *FLAGS, "-I", INCLUDE, "-I", CSRC,
-           *[os.path.join(CSRC, s) for s in sources], "-o", tmp]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     proc = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     if proc.returncode != 0:
         sys.stderr.write(proc.stdout)
-        raise RuntimeError("hipcc failed to build %s" % os.path.basename(path))
+        raise RuntimeError("hipcc failed: %s" % " ".join(cmd[-3:]))
+
+
+def _link(sources, path, verbose):
+    """Compile the sources side by side and link them into the shared library at `path`."""
+    tmp = path + ".tmp%d" % os.getpid()
+    with tempfile.TemporaryDirectory() as d:
+        objects = [os.path.join(d, s + ".o") for s in sources]
+        compile_one = lambda so: _run([HIPCC, *FLAGS, "-I", INCLUDE, "-I", CSRC, "-c",  # noqa: E731
+                                       os.path.join(CSRC, so[0]), "-o", so[1]], verbose)
+        with concurrent.futures.ThreadPoolExecutor(max_workers=8) as pool:
+            list(pool.map(compile_one, zip(sources, objects)))
+        _run([HIPCC, *FLAGS, "-shared", *objects, "-o", tmp], verbose)
     os.replace(tmp, path)
 
 

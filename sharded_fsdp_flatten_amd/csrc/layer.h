@@ -86,4 +86,14 @@ hipError_t launch_act_backward(const ActBwd& a, hipStream_t stream);
 hipError_t launch_norm_forward(const NormFwd& a, hipStream_t stream);
 hipError_t launch_norm_backward(const NormBwd& a, hipStream_t stream);
 
+// The kernels of the norms' backward pass that hold a row in registers, `threads` of them with
+// `vectors` vectors of 4 columns each: they write the input's gradient and, for every workgroup, a
+// partial row (2 x cols floats) of the weight's and the bias's.
+struct BwdShape {
+    int threads, vectors;
+};
+BwdShape norm_bwd_shape(int64_t cols);
+void launch_norm_bwd_rows_bf16(const NormBwd& a, float* partial, uint32_t blocks, hipStream_t stream);
+void launch_norm_bwd_rows_f32(const NormBwd& a, float* partial, uint32_t blocks, hipStream_t stream);
+
 }  // namespace fsdp

@@ -14,6 +14,7 @@
 #include <cstdint>
 
 #include "layer.h"
+#include "layer_dev.h"
 
 // Nothing here is compared bit for bit with separately rounded steps (scaling by powers of two
 // is exact either way), so multiply-adds may be fused.
@@ -21,279 +22,6 @@
 
 namespace fsdp {
 namespace {
-
-constexpr int kV = 8;           // columns of a lane's vector
-constexpr int kThreads = 256;   // workgroup of the kernels that walk tiles
-
-typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-typedef float f4 __attribute__((ext_vector_type(4)));
-typedef float f2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
-// the same at any element's alignment
-typedef uint32_t u4e __attribute__((ext_vector_type(4), aligned(2)));
-typedef uint32_t u2e __attribute__((ext_vector_type(2), aligned(1)));
-typedef float f4e __attribute__((ext_vector_type(4), aligned(4)));
-
-// ---------------------------------------------------------------------------
-// vectors of 8 columns: raw registers, and their values
-// ---------------------------------------------------------------------------
-template <typename T> struct Vec;
-template <> struct Vec<uint16_t> {
-    u4 r;
-    __device__ void load(const uint16_t* p) { r = __builtin_nontemporal_load((const u4e*)p); }
-    __device__ void load_part(const uint16_t* p, int n) {
-        r = u4{0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int j = 0; j < kV; ++j)
-            if (j < n) r[j >> 1] |= uint32_t{p[j]} << (16 * (j & 1));
-    }
-    __device__ void zero() { r = u4{0u, 0u, 0u, 0u}; }
-    __device__ void get(float* v) const {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __builtin_bit_cast(float, r[j] << 16);
-            v[2 * j + 1] = __builtin_bit_cast(float, r[j] & 0xFFFF0000u);
-        }
-    }
-    // round to nearest even, NaN kept NaN (v_cvt_pk_bf16_f32)
-    __device__ void set(const float* v) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            r[j] = __builtin_bit_cast(uint32_t,
-                                      __builtin_convertvector((f2{v[2 * j], v[2 * j + 1]}), bf2));
-    }
-    __device__ void store(uint16_t* p) const { __builtin_nontemporal_store(r, (u4e*)p); }
-    __device__ void store_part(uint16_t* p, int n) const {
-#pragma unroll
-        for (int j = 0; j < kV; ++j)
-            if (j < n) p[j] = static_cast<uint16_t>(r[j >> 1] >> (16 * (j & 1)));
-    }
-};
-template <> struct Vec<float> {
-    f4 r[2];
-    __device__ void load(const float* p) {
-        r[0] = __builtin_nontemporal_load((const f4e*)p);
-        r[1] = __builtin_nontemporal_load((const f4e*)(p + 4));
-    }
-    __device__ void load_part(const float* p, int n) {
-        zero();
-#pragma unroll
-        for (int j = 0; j < kV; ++j)
-            if (j < n) r[j >> 2][j & 3] = p[j];
-    }
-    __device__ void zero() { r[0] = r[1] = f4{0.0f, 0.0f, 0.0f, 0.0f}; }
-    __device__ void get(float* v) const {
-#pragma unroll
-        for (int j = 0; j < kV; ++j) v[j] = r[j >> 2][j & 3];
-    }
-    __device__ void set(const float* v) {
-#pragma unroll
-        for (int j = 0; j < kV; ++j) r[j >> 2][j & 3] = v[j];
-    }
-    __device__ void store(float* p) const {
-        __builtin_nontemporal_store(r[0], (f4e*)p);
-        __builtin_nontemporal_store(r[1], (f4e*)(p + 4));
-    }
-    __device__ void store_part(float* p, int n) const {
-#pragma unroll
-        for (int j = 0; j < kV; ++j)
-            if (j < n) p[j] = r[j >> 2][j & 3];
-    }
-};
-
-// n: columns of this vector inside the row (8 or more: whole; 0 or less: none).
-template <typename T>
-__device__ __forceinline__ void vload(Vec<T>& v, const T* p, int n) {
-    if (n >= kV) v.load(p);
-    else if (n > 0) v.load_part(p, n);
-    else v.zero();
-}
-template <typename T>
-__device__ __forceinline__ void vstore(const Vec<T>& v, T* p, int n) {
-    if (n >= kV) v.store(p);
-    else if (n > 0) v.store_part(p, n);
-}
-template <typename T>
-__device__ __forceinline__ void put8(T* p, const float* f, int n) {
-    Vec<T> v;
-    v.set(f);
-    vstore(v, p, n);
-}
-// 8 values of a parameter (weight, bias): cached loads, every row reads them again.
-__device__ __forceinline__ void param8(const void* w, bool bf16, int64_t c, int n, float* v) {
-#pragma unroll
-    for (int j = 0; j < kV; ++j) v[j] = 0.0f;
-    if (n <= 0) return;
-    if (bf16) {
-        const uint16_t* p = static_cast<const uint16_t*>(w) + c;
-        if (n >= kV) {
-            Vec<uint16_t> t;
-            t.r = *(const u4e*)p;
-            t.get(v);
-        } else {
-            for (int j = 0; j < kV; ++j)
-                if (j < n) v[j] = __builtin_bit_cast(float, uint32_t{p[j]} << 16);
-        }
-    } else {
-        const float* p = static_cast<const float*>(w) + c;
-        if (n >= kV) {
-            const f4 a = *(const f4e*)p, b = *(const f4e*)(p + 4);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) { v[j] = a[j]; v[4 + j] = b[j]; }
-        } else {
-            for (int j = 0; j < kV; ++j)
-                if (j < n) v[j] = p[j];
-        }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// 8-bit groups
-// ---------------------------------------------------------------------------
-// A group's scale is 2^s, held as the byte s + 127.  s is the smallest power at which the
-// group's largest magnitude still rounds to a value the codes have: e4m3 up to 464 (448 is
-// the largest code; 464, halfway to the next step, goes to the even one below), integers below
-// 127.5.  With the magnitude 1.m x 2^e that is s = e - 8, one more where 1.m > 464/256, or
-// s = e - 6, one more where 1.m >= 127.5/64; never below -124 (e4m3: its smallest step is then
-// bf16's smallest) or -127 (integers, the byte's end).  Dividing by a power of two is exact, so
-// a code is off by at most half its step, and every value a code stands for is a bf16 number.
-// Byte 255: the group held an infinity or a NaN, and reads back as NaN throughout.
-__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits, bool int8) {
-    const uint32_t e = amax_bits >> 23, m = amax_bits & 0x7FFFFFu;
-    if (e == 255u) return 255u;
-    const int s = int8 ? static_cast<int>(e) - 6 + (m >= 0x7F0000u) : static_cast<int>(e) - 8 + (m > 0x680000u);
-    return static_cast<uint32_t>(max(s, int8 ? 0 : 3));
-}
-__device__ __forceinline__ float scale_value(uint32_t b) {
-    uint32_t bits = b << 23;
-    if (b == 0u) bits = 0x00400000u;   // 2^-127, a subnormal
-    if (b == 255u) bits = 0x7FC00000u;
-    return __builtin_bit_cast(float, bits);
-}
-template <int kCtrl>
-__device__ __forceinline__ uint32_t dpp(uint32_t x) {
-    return __builtin_amdgcn_update_dpp(0u, x, kCtrl, 0xF, 0xF, true);
-}
-constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E;   // quad_perm [1,0,3,2], [2,3,0,1]
-constexpr int kHalfMirror = 0x141, kMirror = 0x140;
-
-// Codes of 8 columns whose group is the calling lane's quad; every lane of the quad calls it.
-__device__ __forceinline__ u2 encode8(const float* v, bool int8, uint32_t* byte) {
-    uint32_t a = 0;
-#pragma unroll
-    for (int j = 0; j < kV; ++j) a = max(a, __builtin_bit_cast(uint32_t, v[j]) & 0x7FFFFFFFu);
-    a = max(a, dpp<kQuadXor1>(a));
-    a = max(a, dpp<kQuadXor2>(a));
-    const uint32_t b = scale_byte(a, int8);
-    *byte = b;
-    u2 q = {0u, 0u};
-    if (b == 255u) return q;
-    const float inv = __builtin_bit_cast(float, (254u - b) << 23);   // 2^-s, a normal number
-    if (int8) {
-        // 1.5 x 2^23 + x 2^-s rounds to the nearest integer, ties to even, and its low byte is
-        // that integer in two's complement
-        uint32_t t[kV];
-#pragma unroll
-        for (int j = 0; j < kV; ++j)
-            t[j] = __builtin_bit_cast(uint32_t, __builtin_fmaf(v[j], inv, 12582912.0f));
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t lo = __builtin_amdgcn_perm(t[4 * h + 1], t[4 * h], 0x0C0C0400u);
-            const uint32_t hi = __builtin_amdgcn_perm(t[4 * h + 3], t[4 * h + 2], 0x04000C0Cu);
-            q[h] = lo | hi;
-        }
-    } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            int w = 0;
-            w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h] * inv, v[4 * h + 1] * inv, w, false);
-            w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2] * inv, v[4 * h + 3] * inv, w, true);
-            q[h] = static_cast<uint32_t>(w);
-        }
-    }
-    return q;
-}
-__device__ __forceinline__ void decode8(u2 q, uint32_t byte, bool int8, float* v) {
-    const float s = scale_value(byte);
-    if (int8) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t u = q[h] ^ 0x80808080u;   // offset by 128
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[4 * h + j] = (static_cast<float>((u >> (8 * j)) & 0xFFu) - 128.0f) * s;
-        }
-    } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q[h]), false);
-            const f2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q[h]), true);
-            v[4 * h] = a[0] * s;
-            v[4 * h + 1] = a[1] * s;
-            v[4 * h + 2] = b[0] * s;
-            v[4 * h + 3] = b[1] * s;
-        }
-    }
-}
-__device__ __forceinline__ u2 code_load(const uint8_t* p, int n) {
-    if (n >= kV) return __builtin_nontemporal_load((const u2e*)p);
-    u2 q = {0u, 0u};
-#pragma unroll
-    for (int j = 0; j < kV; ++j)
-        if (j < n) q[j >> 2] |= uint32_t{p[j]} << (8 * (j & 3));
-    return q;
-}
-__device__ __forceinline__ void code_store(uint8_t* p, u2 q, int n) {
-    if (n >= kV) {
-        __builtin_nontemporal_store(q, (u2e*)p);
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < kV; ++j)
-        if (j < n) p[j] = static_cast<uint8_t>(q[j >> 2] >> (8 * (j & 3)));
-}
-// Codes and scale of the vector at column c (n of its columns inside the row) of a row.
-__device__ __forceinline__ void pack8(const CkptRows& q, int64_t row, int64_t c, int n,
-                                      const float* v) {
-    uint32_t byte;
-    const u2 code = encode8(v, q.int8 != 0, &byte);
-    code_store(q.codes + row * q.code_pitch + c, code, n);
-    if (n > 0 && (threadIdx.x & 3) == 0)
-        q.scales[row * q.scale_pitch + c / kCkptGroup] = static_cast<uint8_t>(byte);
-}
-
-// ---------------------------------------------------------------------------
-// sums over a wave and a workgroup
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ float wave_sum(float x) {
-    const auto add = [](float a, uint32_t b) { return a + __builtin_bit_cast(float, b); };
-    const auto bits = [](float a) { return __builtin_bit_cast(uint32_t, a); };
-    x = add(x, dpp<kQuadXor1>(bits(x)));
-    x = add(x, dpp<kQuadXor2>(bits(x)));
-    x = add(x, dpp<kHalfMirror>(bits(x)));
-    x = add(x, dpp<kMirror>(bits(x)));
-    const auto r = __builtin_amdgcn_permlane16_swap(bits(x), bits(x), false, false);
-    x = __builtin_bit_cast(float, static_cast<uint32_t>(r[0])) +
-        __builtin_bit_cast(float, static_cast<uint32_t>(r[1]));
-    const auto t = __builtin_amdgcn_permlane32_swap(bits(x), bits(x), false, false);
-    return __builtin_bit_cast(float, static_cast<uint32_t>(t[0])) +
-           __builtin_bit_cast(float, static_cast<uint32_t>(t[1]));
-}
-// Sum over the workgroup, the same in every thread.  `lds` holds one float per wave and is
-// free again only after the next barrier.
-template <int kT>
-__device__ __forceinline__ float group_sum(float x, float* lds) {
-    x = wave_sum(x);
-    if constexpr (kT > 64) {
-        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
-        __syncthreads();
-        x = lds[0];
-#pragma unroll
-        for (int i = 1; i < kT / 64; ++i) x += lds[i];
-    }
-    return x;
-}
 
 // ---------------------------------------------------------------------------
 // activations
@@ -318,14 +46,14 @@ __device__ __forceinline__ void activate(float h, float* y, float* d) {
         *y = h * s;
         *d = s * (1.0f + h * (1.0f - s));
     } else if constexpr (kF == kGeluTanh) {
-        // (1 + tanh u) / 2 = 1 / (1 + e^-2u), u = sqrt(2/pi) (h + 0.044715 h^3)
-        constexpr float a = 0.79788456080286536f, c = 0.044715f;
+        // (1 + tanh u) / 2 = 1 / (1 + e^-2u), u = sqrt(2/pi) (h + 0.044715 h^3).
         // h^2 is capped where the logistic function is flat, so that no product overflows to 0 x inf;
         // a NaN comes through h
+        constexpr float a = 0.79788456080286536f, c = 0.044715f, l = -2.0f * a * 1.44269504088896341f;
         const float h2 = __builtin_fminf(h * h, 1000.0f);
-        const float s = __builtin_amdgcn_rcpf(1.0f + fast_exp(-2.0f * a * h * (1.0f + c * h2)));
+        const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(h * (l + l * c * h2)));
         *y = h * s;
-        *d = s + (s * (1.0f - s) * h) * (2.0f * a + 6.0f * a * c * h2);
+        *d = s + *y * (1.0f - s) * (2.0f * a + 6.0f * a * c * h2);
     } else {
         // Phi(h) by Hastings' rational form of erfc (Abramowitz and Stegun 7.1.26, absolute error
         // 1.5e-7): erfc(z) = t (a1 + t (a2 + ...)) e^-z^2, t = 1 / (1 + p z), z = |h| / sqrt 2;
@@ -351,13 +79,13 @@ struct Tiles {
     uint32_t across;  // tiles across a row
     int64_t down;     // tiles down the rows
 };
-Tiles plan_tiles(int64_t rows, int64_t cols) {
+Tiles plan_tiles(int64_t rows, int64_t cols, int widest = 8) {
     const int64_t nv = (cols + kCkptGroup - 1) / kCkptGroup * (kCkptGroup / kV);
     int best = 2;
     while (best < 5 && (int64_t{1} << best) < nv) ++best;
     if (best == 5) {
-        // of 32, 64, 128 and 256 vectors the width that leaves the fewest lanes idle
-        for (int k = 6; k <= 8; ++k) {
+        // of 32, 64, ... vectors the width that leaves the fewest lanes idle
+        for (int k = 6; k <= widest; ++k) {
             const auto padded = [&](int b) { return (((nv - 1) >> b) + 1) << b; };
             if (padded(k) <= padded(best)) best = k;
         }
@@ -370,10 +98,22 @@ Tiles plan_tiles(int64_t rows, int64_t cols) {
     return t;
 }
 
+// The dispatcher deals workgroups to the eight XCDs in turn.  This hands each of them runs of
+// `run` consecutive tiles instead (a bijection of the whole groups of 8 run; what is left over, and
+// run == 0, stays as dealt), so that an XCD reads and writes longer stretches of memory.
+__device__ __forceinline__ uint32_t xcd_order(uint32_t b, uint32_t blocks, uint32_t run) {
+    const uint32_t span = 8u * run;
+    if (b >= blocks / max(span, 1u) * span) return b;
+    const uint32_t r = b % span;
+    return b - r + (r & 7u) * run + (r >> 3);
+}
+uint32_t xcd_run(uint32_t blocks) { return blocks >= 4096u ? 64u : 0u; }
+
 // y = f(x) and the checkpoint of x, one tile per workgroup.
 template <typename T, int kF>
-__global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActFwd a, int k, uint32_t across) {
-    const uint32_t down = blockIdx.x / across, tile = blockIdx.x - down * across;
+__global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActFwd a, int k, uint32_t across, uint32_t run) {
+    const uint32_t block = xcd_order(blockIdx.x, gridDim.x, run);
+    const uint32_t down = block / across, tile = block - down * across;
     const int64_t row = static_cast<int64_t>(down) * (kThreads >> k) + (threadIdx.x >> k);
     if (row >= a.rows) return;  // whole quads leave together (k >= 2)
     const int64_t c = ((static_cast<int64_t>(tile) << k) + (threadIdx.x & ((1 << k) - 1))) * kV;
@@ -393,8 +133,9 @@ __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActFwd a, int k, uint
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-unpack_kernel(int64_t rows, int64_t cols, CkptRows q, RowsOut x, int k, uint32_t across) {
-    const uint32_t down = blockIdx.x / across, tile = blockIdx.x - down * across;
+unpack_kernel(int64_t rows, int64_t cols, CkptRows q, RowsOut x, int k, uint32_t across, uint32_t run) {
+    const uint32_t block = xcd_order(blockIdx.x, gridDim.x, run);
+    const uint32_t down = block / across, tile = block - down * across;
     const int64_t row = static_cast<int64_t>(down) * (kThreads >> k) + (threadIdx.x >> k);
     if (row >= rows) return;
     const int64_t c = ((static_cast<int64_t>(tile) << k) + (threadIdx.x & ((1 << k) - 1))) * kV;
@@ -411,45 +152,79 @@ unpack_kernel(int64_t rows, int64_t cols, CkptRows q, RowsOut x, int k, uint32_t
 // ---------------------------------------------------------------------------
 // The lanes of a tile's rows add their 8 columns in LDS, row by row; the first row's lanes
 // write the workgroup's partial sums.  Called by every thread.
+template <int kT>
 __device__ __forceinline__ void tile_partial(const float* s, float* lds, int k, float* out, int n) {
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kV; ++j) lds[j * kThreads + threadIdx.x] = s[j];
+    for (int j = 0; j < kV; ++j) lds[j * kT + threadIdx.x] = s[j];
+    __syncthreads();
+    // every thread adds up columns of its own
+    for (int i = threadIdx.x; i < (kV << k); i += kT) {
+        const int j = i >> k, l = i & ((1 << k) - 1);
+        float t = lds[j * kT + l];
+        for (int r = 1; r < (kT >> k); ++r) t += lds[j * kT + l + (r << k)];
+        lds[j * kT + l] = t;   // of this column no other thread reads
+    }
     __syncthreads();
     if (threadIdx.x >> k) return;
-#pragma unroll
-    for (int j = 0; j < kV; ++j) {
-        float t = lds[j * kThreads + threadIdx.x];
-        for (int r = 1; r < (kThreads >> k); ++r) t += lds[j * kThreads + threadIdx.x + (r << k)];
-        if (j < n) out[j] = t;
+    if (n == kV) {
+        *(f4e*)out = f4{lds[threadIdx.x], lds[kT + threadIdx.x], lds[2 * kT + threadIdx.x], lds[3 * kT + threadIdx.x]};
+        *(f4e*)(out + 4) = f4{lds[4 * kT + threadIdx.x], lds[5 * kT + threadIdx.x], lds[6 * kT + threadIdx.x], lds[7 * kT + threadIdx.x]};
+        return;
     }
+#pragma unroll
+    for (int j = 0; j < kV; ++j)
+        if (j < n) out[j] = lds[j * kT + threadIdx.x];
 }
 
-constexpr int kSumCols = 64, kSumSlices = 16;   // sum kernel: columns and slices of a workgroup
-// out[c] (+)= sum over g of partial[g][c]: each slice sums its part of the partial rows, then the
-// slices are added in order.
-__global__ void __launch_bounds__(kSumCols / 4 * kSumSlices)
+// A workgroup of 16 waves sums 32 columns (one 128-byte line of a partial row): 8 lanes of 4
+// columns, 128 slices of the partial rows, so that a thousand partial rows are 8 loads in flight a
+// thread.  Each slice adds its rows in order, then the slices of a wave and the waves add up in a
+// fixed tree.
+constexpr int kSumCols = 32;
+template <int kSumThreads>
+__global__ void __launch_bounds__(kSumThreads)
 col_sum_kernel(const float* partial, int64_t G, int64_t pitch, int64_t cols, ColOut o0, ColOut o1) {
-    __shared__ f4 lds[kSumSlices][kSumCols / 4];
+    constexpr int kSumSlices = kSumThreads / (kSumCols / 4);
+    __shared__ f4 lds[kSumThreads / 64][kSumCols / 4];
     const ColOut o = blockIdx.y ? o1 : o0;
     const float* p = partial + (blockIdx.y ? cols : 0);
     const int lane = threadIdx.x % (kSumCols / 4), slice = threadIdx.x / (kSumCols / 4);
     const int64_t c = static_cast<int64_t>(blockIdx.x) * kSumCols + 4 * lane;
     const int n = static_cast<int>(min(cols - c, int64_t{4}));
     f4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t g = slice; g < G; g += kSumSlices) {
-        const float* q = p + g * pitch + c;
-        if (n == 4) {
-            s += *(const f4e*)q;
-        } else {
-            for (int j = 0; j < 4; ++j)
-                if (j < n) s[j] += q[j];
+    constexpr int kAhead = 8;
+    for (int64_t g = slice; g < G; g += kAhead * kSumSlices) {
+        f4 v[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int64_t r = g + i * kSumSlices;
+            v[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (r < G) {
+                const float* q = p + r * pitch + c;
+                if (n == 4) {
+                    v[i] = *(const f4e*)q;
+                } else {
+                    for (int j = 0; j < 4; ++j)
+                        if (j < n) v[i][j] = q[j];
+                }
+            }
         }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) s += v[i];
     }
-    lds[slice][lane] = s;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        // lanes 8, 16 and 32 apart hold the wave's other slices
+        float x = s[j];
+        x += __builtin_bit_cast(float, dpp<kRowRor8>(__builtin_bit_cast(uint32_t, x)));
+        s[j] = sum_rows(x);
+    }
+    if ((threadIdx.x & 63) < kSumCols / 4) lds[threadIdx.x >> 6][lane] = s;
     __syncthreads();
     if (slice || n <= 0) return;
-    for (int i = 1; i < kSumSlices; ++i) s += lds[i][lane];
+#pragma unroll
+    for (int i = 1; i < kSumThreads / 64; ++i) s += lds[i][lane];
     for (int j = 0; j < 4; ++j) {
         if (j >= n) break;
         if (o.bf16) {
@@ -464,6 +239,7 @@ col_sum_kernel(const float* partial, int64_t G, int64_t pitch, int64_t cols, Col
         }
     }
 }
+constexpr int64_t kSumFew = 256;
 hipError_t launch_col_sum(const float* partial, int64_t G, int64_t pitch, int64_t cols,
                           const ColOut& o0, const ColOut& o1, hipStream_t stream) {
     if (!o0.p && !o1.p) return hipSuccess;
@@ -476,11 +252,95 @@ hipError_t launch_col_sum(const float* partial, int64_t G, int64_t pitch, int64_
         b.p = nullptr;
         p += cols;
     }
-    col_sum_kernel<<<dim3(static_cast<uint32_t>(blocks), b.p ? 2 : 1), kSumCols / 4 * kSumSlices, 0, stream>>>(
-        p, G, pitch, cols, a, b);
+    const dim3 grid(static_cast<uint32_t>(blocks), b.p ? 2 : 1);
+    if (G <= kSumFew) col_sum_kernel<256><<<grid, 256, 0, stream>>>(p, G, pitch, cols, a, b);
+    else col_sum_kernel<1024><<<grid, 1024, 0, stream>>>(p, G, pitch, cols, a, b);
     return hipGetLastError();
 }
 
+// What a lane reads of one row for the activation's backward pass.
+template <typename T, bool kCkpt>
+struct ActRow {
+    Vec<T> dy, x;
+    u2 q;
+    uint32_t byte;
+    __device__ __forceinline__ void load(const ActBwd& a, int64_t row, int64_t c, int64_t group) {
+        dy.load(static_cast<const T*>(a.dy.p) + row * a.dy.pitch + c);
+        if constexpr (kCkpt) {
+            q = __builtin_nontemporal_load((const u2e*)(a.ckpt.codes + row * a.ckpt.code_pitch + c));
+            byte = a.ckpt.scales[row * a.ckpt.scale_pitch + group];
+        } else {
+            x.load(static_cast<const T*>(a.x.p) + row * a.x.pitch + c);
+        }
+    }
+    // row of fewer than 8 columns
+    __device__ __forceinline__ void load_part(const ActBwd& a, int64_t row, int n) {
+        dy.load_part(static_cast<const T*>(a.dy.p) + row * a.dy.pitch, n);
+        if constexpr (kCkpt) {
+            q = code_load(a.ckpt.codes + row * a.ckpt.code_pitch, n);
+            byte = a.ckpt.scales[row * a.ckpt.scale_pitch];
+        } else {
+            x.load_part(static_cast<const T*>(a.x.p) + row * a.x.pitch, n);
+        }
+    }
+    __device__ __forceinline__ void drop(int k) {
+        dy.drop(k);
+        if constexpr (kCkpt) q = __builtin_bit_cast(u2, __builtin_bit_cast(uint64_t, q) >> (8 * k));
+        else x.drop(k);
+    }
+};
+
+// dx = dy f'(h), optionally y = f(h) again, and the column sums of dx before its rounding.  A
+// workgroup takes one block of 2^k vectors across and kActThreads >> k lanes of kActRows rows
+// each, all of whose loads are in flight at once, and ends: its lanes' sums add up in LDS to one
+// partial row.  The vector that the row's end cuts is read from the row's last 8 columns (kNarrow:
+// there are none); rows past the last read it once more, so that no branch stands between loads.
+constexpr int kActThreads = 1024, kActRows = 1;
+constexpr int kActWidest = 6;   // log2 of a block's vectors across, at most
+template <typename T, int kF, bool kCkpt, bool kNarrow>
+__global__ void __launch_bounds__(kActThreads)
+act_bwd_kernel(ActBwd a, int k, uint32_t across) {
+    __shared__ float lds[kV * kActThreads];
+    const uint32_t down = blockIdx.x / across, tile = blockIdx.x - down * across;
+    const int64_t c = ((static_cast<int64_t>(tile) << k) + (threadIdx.x & ((1 << k) - 1))) * kV;
+    const int n = static_cast<int>(max(min(a.cols - c, int64_t{kV}), int64_t{0}));
+    const int64_t at = n > 0 ? min(c, a.cols - kV) : 0, group = n > 0 ? c / kCkptGroup : 0;
+    const int skip = n > 0 ? static_cast<int>(c - at) : 0;
+    const int high = kActThreads >> k;
+    const int64_t row = static_cast<int64_t>(down) * kActRows * high + (threadIdx.x >> k), last = a.rows - 1;
+    ActRow<T, kCkpt> in[kActRows];
+#pragma unroll
+    for (int u = 0; u < kActRows; ++u) {
+        const int64_t r = min(row + u * high, last);
+        if constexpr (kNarrow) in[u].load_part(a, r, n);
+        else in[u].load(a, r, at, group);
+    }
+    float s[kV] = {};
+#pragma unroll
+    for (int u = 0; u < kActRows; ++u) {
+        const int64_t r = row + u * high;
+        if (r > last || n == 0) continue;
+        if (!kNarrow && skip) in[u].drop(skip);
+        float h[kV], g[kV], y[kV];
+        if constexpr (kCkpt) decode8(in[u].q, in[u].byte, a.ckpt.int8 != 0, h);
+        else in[u].x.get(h);
+        in[u].dy.get(g);
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            float d;
+            activate<kF>(h[j], &y[j], &d);
+            g[j] *= d;
+            s[j] += g[j];
+        }
+        put8(static_cast<T*>(a.dx.p) + r * a.dx.pitch + c, g, n);
+        if (a.y.p) put8(static_cast<T*>(a.y.p) + r * a.y.pitch + c, y, n);
+    }
+    if (a.dbias.p) tile_partial<kActThreads>(s, lds, k, a.workspace + static_cast<int64_t>(down) * a.cols + c, n);
+}
+
+// ---------------------------------------------------------------------------
+// norms, rows of any length: one workgroup per row, the row read again for each pass over it
+// ---------------------------------------------------------------------------
 // How a backward pass that walks tiles cuts its rows: `chunks` runs of tiles down, about eight
 // workgroups per CU, each run long enough that its partial sums stay small against its rows.
 struct Walk {
@@ -497,48 +357,6 @@ Walk plan_walk(int64_t rows, int64_t cols) {
     return w;
 }
 
-// dx = dy f'(h), optionally y = f(h) again, and the column sums of dx before its rounding.
-template <typename T, int kF, bool kCkpt>
-__global__ void __launch_bounds__(kThreads)
-act_bwd_kernel(ActBwd a, int k, uint32_t across, int64_t per) {
-    __shared__ float lds[kV * kThreads];
-    const uint32_t chunk = blockIdx.x / across, tile = blockIdx.x - chunk * across;
-    const int64_t c = ((static_cast<int64_t>(tile) << k) + (threadIdx.x & ((1 << k) - 1))) * kV;
-    const int n = static_cast<int>(max(min(a.cols - c, int64_t{kV}), int64_t{0}));
-    const int high = kThreads >> k;
-    const int64_t r0 = chunk * per * high;
-    const int64_t r1 = min(a.rows, r0 + per * high);
-    float s[kV] = {};
-    for (int64_t row = r0 + (threadIdx.x >> k); row < r1; row += high) {
-        if (n == 0) break;
-        Vec<T> dy;
-        vload(dy, static_cast<const T*>(a.dy.p) + row * a.dy.pitch + c, n);
-        float h[kV], g[kV], y[kV];
-        if constexpr (kCkpt) {
-            decode8(code_load(a.ckpt.codes + row * a.ckpt.code_pitch + c, n),
-                    a.ckpt.scales[row * a.ckpt.scale_pitch + c / kCkptGroup], a.ckpt.int8 != 0, h);
-        } else {
-            Vec<T> x;
-            vload(x, static_cast<const T*>(a.x.p) + row * a.x.pitch + c, n);
-            x.get(h);
-        }
-        dy.get(g);
-#pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            float d;
-            activate<kF>(h[j], &y[j], &d);
-            g[j] *= d;
-            s[j] += g[j];
-        }
-        put8(static_cast<T*>(a.dx.p) + row * a.dx.pitch + c, g, n);
-        if (a.y.p) put8(static_cast<T*>(a.y.p) + row * a.y.pitch + c, y, n);
-    }
-    if (a.dbias.p) tile_partial(s, lds, k, a.workspace + chunk * a.cols + c, n);
-}
-
-// ---------------------------------------------------------------------------
-// norms, rows of any length: one workgroup per row, the row read again for each pass over it
-// ---------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(kThreads) norm_fwd_long_kernel(NormFwd a) {
     __shared__ float lds[2][kThreads / 64];
@@ -691,8 +509,125 @@ norm_bwd_tile_kernel(NormBwd a, const float* stat, float* partial, int k, uint32
         if (a.y.p) put8(static_cast<T*>(a.y.p) + row * a.y.pitch + c, x, n);
     }
     float* out = partial + chunk * 2 * a.cols + c;
-    if (a.dweight.p) tile_partial(sw, lds, k, out, n);
-    if (a.dbias.p) tile_partial(sb, lds, k, out + a.cols, n);
+    if (a.dweight.p) tile_partial<kThreads>(sw, lds, k, out, n);
+    if (a.dbias.p) tile_partial<kThreads>(sb, lds, k, out + a.cols, n);
+}
+
+// ---------------------------------------------------------------------------
+// norms, a row in registers: kT threads (a wave, or a whole workgroup) own a row, kN vectors each
+// ---------------------------------------------------------------------------
+// Thread t of a row owns vectors t, t + kT, ...; with kWhole every vector is whole or outside.
+template <int kT> constexpr int group_threads() { return kT == 64 ? kThreads : kT; }
+
+template <bool kWhole, typename T>
+__device__ __forceinline__ void rload(Vec<T>& v, const T* p, int n) {
+    if constexpr (kWhole) {
+        if (n > 0) v.load(p);
+        else v.zero();
+    } else {
+        vload(v, p, n);
+    }
+}
+template <bool kWhole, typename T>
+__device__ __forceinline__ void rput(T* p, const float* f, int n) {
+    Vec<T> v;
+    v.set(f);
+    if constexpr (kWhole) {
+        if (n > 0) v.store(p);
+    } else {
+        vstore(v, p, n);
+    }
+}
+
+template <typename T, int kT, int kN, bool kWhole>
+__global__ void __launch_bounds__(group_threads<kT>()) norm_fwd_kernel(NormFwd a) {
+    constexpr int kRows = group_threads<kT>() / kT;
+    __shared__ float lds[2][kT / 64];
+    const int t = threadIdx.x % kT;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + (kRows > 1 ? threadIdx.x / kT : 0);
+    if (kRows > 1 && row >= a.rows) return;
+    const int cols = static_cast<int>(a.cols);
+    float v[kN][kV];
+    {
+        Vec<T> x[kN];
+        const T* xp = static_cast<const T*>(a.x.p) + row * a.x.pitch;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int c = (t + i * kT) * kV;
+            rload<kWhole>(x[i], xp + c, cols - c);
+        }
+        if (a.residual.p) {
+            Vec<T> r[kN];
+            const T* rp = static_cast<const T*>(a.residual.p) + row * a.residual.pitch;
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const int c = (t + i * kT) * kV;
+                rload<kWhole>(r[i], rp + c, cols - c);
+            }
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                float u[kV], w[kV];
+                x[i].get(u);
+                r[i].get(w);
+#pragma unroll
+                for (int j = 0; j < kV; ++j) u[j] += w[j];
+                x[i].set(u);
+            }
+            if (a.sum.p) {
+                T* sp = static_cast<T*>(a.sum.p) + row * a.sum.pitch;
+#pragma unroll
+                for (int i = 0; i < kN; ++i) {
+                    const int c = (t + i * kT) * kV;
+                    vstore(x[i], sp + c, cols - c);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kN; ++i) x[i].get(v[i]);
+    }
+    const float inv = 1.0f / static_cast<float>(cols);
+    float mean = 0.0f;
+    if (!a.rms) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+#pragma unroll
+            for (int j = 0; j < kV; ++j) s += v[i][j];
+        mean = group_sum<kT>(s, lds[0]) * inv;
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const int n = cols - (t + i * kT) * kV;
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            const float d = v[i][j] - mean;
+            if (kWhole ? n > 0 : n > j) s += d * d;
+        }
+    }
+    const float rstd = 1.0f / __builtin_sqrtf(group_sum<kT>(s, lds[1]) * inv + a.eps);
+    if (t == 0) {
+        if (a.mean) a.mean[row] = mean;
+        a.rstd[row] = rstd;
+    }
+    if (a.ckpt.codes) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int c = (t + i * kT) * kV;
+            pack8(a.ckpt, row, c, cols - c, v[i]);
+        }
+    }
+    T* yp = static_cast<T*>(a.y.p) + row * a.y.pitch;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const int c = (t + i * kT) * kV;
+        float w[kV], b[kV] = {};
+        param8(a.weight, a.param_bf16, c, cols - c, w);
+        if (a.bias) param8(a.bias, a.param_bf16, c, cols - c, b);
+#pragma unroll
+        for (int j = 0; j < kV; ++j) v[i][j] = (v[i][j] - mean) * rstd * w[j] + b[j];
+        rput<kWhole>(yp + c, v[i], cols - c);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -741,32 +676,105 @@ hipError_t act_forward_t(const ActFwd& a, hipStream_t stream) {
         b.y = skip(a.y, r, a.bf16);
         b.ckpt = skip(a.ckpt, r);
         switch (a.f) {
-            case kNone: act_fwd_kernel<T, kNone><<<blocks, kThreads, 0, stream>>>(b, k, across); break;
-            case kRelu: act_fwd_kernel<T, kRelu><<<blocks, kThreads, 0, stream>>>(b, k, across); break;
-            case kGelu: act_fwd_kernel<T, kGelu><<<blocks, kThreads, 0, stream>>>(b, k, across); break;
-            case kGeluTanh: act_fwd_kernel<T, kGeluTanh><<<blocks, kThreads, 0, stream>>>(b, k, across); break;
-            default: act_fwd_kernel<T, kSilu><<<blocks, kThreads, 0, stream>>>(b, k, across); break;
+            case kNone: act_fwd_kernel<T, kNone><<<blocks, kThreads, 0, stream>>>(b, k, across, xcd_run(blocks)); break;
+            case kRelu: act_fwd_kernel<T, kRelu><<<blocks, kThreads, 0, stream>>>(b, k, across, xcd_run(blocks)); break;
+            case kGelu: act_fwd_kernel<T, kGelu><<<blocks, kThreads, 0, stream>>>(b, k, across, xcd_run(blocks)); break;
+            case kGeluTanh: act_fwd_kernel<T, kGeluTanh><<<blocks, kThreads, 0, stream>>>(b, k, across, xcd_run(blocks)); break;
+            default: act_fwd_kernel<T, kSilu><<<blocks, kThreads, 0, stream>>>(b, k, across, xcd_run(blocks)); break;
         }
     });
 }
 
+// The blocks of the activation's backward pass: `t.down` partial rows.
+Tiles act_tiles(int64_t rows, int64_t cols) {
+    Tiles t = plan_tiles(rows, cols, kActWidest);
+    const int64_t high = static_cast<int64_t>(kActThreads >> t.k) * kActRows;
+    t.down = (rows + high - 1) / high;
+    return t;
+}
+template <typename T, int kF, bool kCkpt>
+void act_backward_f(const ActBwd& a, const Tiles& t, hipStream_t stream) {
+    const uint32_t blocks = static_cast<uint32_t>(t.down * t.across);
+    if (a.cols < kV) act_bwd_kernel<T, kF, kCkpt, true><<<blocks, kActThreads, 0, stream>>>(a, t.k, t.across);
+    else act_bwd_kernel<T, kF, kCkpt, false><<<blocks, kActThreads, 0, stream>>>(a, t.k, t.across);
+}
 template <typename T, bool kCkpt>
-void act_backward_t(const ActBwd& a, const Walk& w, hipStream_t stream) {
-    const uint32_t blocks = static_cast<uint32_t>(w.chunks * w.t.across);
+void act_backward_t(const ActBwd& a, const Tiles& w, hipStream_t stream) {
     switch (a.f) {
-        case kRelu: act_bwd_kernel<T, kRelu, kCkpt><<<blocks, kThreads, 0, stream>>>(a, w.t.k, w.t.across, w.per); break;
-        case kGelu: act_bwd_kernel<T, kGelu, kCkpt><<<blocks, kThreads, 0, stream>>>(a, w.t.k, w.t.across, w.per); break;
-        case kGeluTanh: act_bwd_kernel<T, kGeluTanh, kCkpt><<<blocks, kThreads, 0, stream>>>(a, w.t.k, w.t.across, w.per); break;
-        default: act_bwd_kernel<T, kSilu, kCkpt><<<blocks, kThreads, 0, stream>>>(a, w.t.k, w.t.across, w.per); break;
+        case kRelu: return act_backward_f<T, kRelu, kCkpt>(a, w, stream);
+        case kGelu: return act_backward_f<T, kGelu, kCkpt>(a, w, stream);
+        case kGeluTanh: return act_backward_f<T, kGeluTanh, kCkpt>(a, w, stream);
+        default: return act_backward_f<T, kSilu, kCkpt>(a, w, stream);
+    }
+}
+
+// Rows longer than this take the kernels that read a row again for each pass.
+constexpr int64_t kMaxRowCols = 16384;
+
+// Threads of a row and vectors of a thread for the kernels that hold a row in registers.
+struct RowShape {
+    int threads, vectors;
+};
+RowShape fwd_shape(int64_t cols) {
+    const int64_t nv = (cols + kV - 1) / kV;
+    if (nv <= 256) return {64, static_cast<int>((nv + 63) / 64)};
+    const int n = static_cast<int>((nv + 255) / 256);
+    return {256, n <= 2 ? 2 : n <= 4 ? 4 : n <= 6 ? 6 : 8};
+}
+// Whether the backward pass holds a row of these columns in registers.
+bool bwd_in_registers(int64_t cols) { return cols >= 4 && cols <= kMaxRowCols; }
+// Workgroups of the backward pass over rows in registers: each writes a partial row.
+int64_t bwd_groups(int64_t rows, int64_t cols) {
+    const BwdShape s = norm_bwd_shape(cols);
+    const int64_t high = std::max(1, 512 / s.threads);
+    const int64_t most = s.threads == 1024 ? 256 : 512;
+    const int64_t each = (rows + high - 1) / high;
+    return std::min(most, std::max(std::min<int64_t>(each, 64), (each + 3) / 4));
+}
+
+template <typename T, int kT, int kN>
+void norm_fwd_run(const NormFwd& a, hipStream_t stream) {
+    constexpr int kRows = group_threads<kT>() / kT;
+    const uint32_t blocks = static_cast<uint32_t>((a.rows + kRows - 1) / kRows);
+    if (a.cols % kV == 0) norm_fwd_kernel<T, kT, kN, true><<<blocks, group_threads<kT>(), 0, stream>>>(a);
+    else norm_fwd_kernel<T, kT, kN, false><<<blocks, group_threads<kT>(), 0, stream>>>(a);
+}
+template <typename T>
+void norm_forward_t(const NormFwd& a, hipStream_t stream) {
+    if (a.cols > kMaxRowCols) {
+        norm_fwd_long_kernel<T><<<static_cast<uint32_t>(a.rows), kThreads, 0, stream>>>(a);
+        return;
+    }
+    const RowShape s = fwd_shape(a.cols);
+    if (s.threads == 64) {
+        switch (s.vectors) {
+            case 1: return norm_fwd_run<T, 64, 1>(a, stream);
+            case 2: return norm_fwd_run<T, 64, 2>(a, stream);
+            case 3: return norm_fwd_run<T, 64, 3>(a, stream);
+            default: return norm_fwd_run<T, 64, 4>(a, stream);
+        }
+    }
+    switch (s.vectors) {
+        case 2: return norm_fwd_run<T, 256, 2>(a, stream);
+        case 4: return norm_fwd_run<T, 256, 4>(a, stream);
+        case 6: return norm_fwd_run<T, 256, 6>(a, stream);
+        default: return norm_fwd_run<T, 256, 8>(a, stream);
     }
 }
 
 template <typename T, bool kCkpt>
 hipError_t norm_backward_t(const NormBwd& a, hipStream_t stream) {
-    const Walk w = plan_walk(a.rows, a.cols);
-    float* stat = a.workspace;
-    float* partial = a.workspace + (2 * a.rows + 3) / 4 * 4;
-    if (a.rows > 0) {
+    float* partial = a.workspace;
+    int64_t G = 0;
+    if (a.rows > 0 && bwd_in_registers(a.cols)) {
+        G = bwd_groups(a.rows, a.cols);
+        if (a.bf16) launch_norm_bwd_rows_bf16(a, partial, static_cast<uint32_t>(G), stream);
+        else launch_norm_bwd_rows_f32(a, partial, static_cast<uint32_t>(G), stream);
+    } else if (a.rows > 0) {
+        const Walk w = plan_walk(a.rows, a.cols);
+        G = w.chunks;
+        float* stat = a.workspace;
+        partial = a.workspace + (2 * a.rows + 3) / 4 * 4;
         for (int64_t r = 0; r < a.rows; r += kMaxBlocks) {
             NormBwd b = a;
             b.dy = skip(a.dy, r, a.bf16);
@@ -778,16 +786,25 @@ hipError_t norm_backward_t(const NormBwd& a, hipStream_t stream) {
         }
         norm_bwd_tile_kernel<T, kCkpt><<<static_cast<uint32_t>(w.chunks * w.t.across), kThreads, 0, stream>>>(
             a, stat, partial, w.t.k, w.t.across, w.per);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
     }
-    return launch_col_sum(partial, w.chunks, 2 * a.cols, a.cols, a.dweight, a.dbias, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    return launch_col_sum(partial, G, 2 * a.cols, a.cols, a.dweight, a.dbias, stream);
 }
 
 }  // namespace
 
+BwdShape norm_bwd_shape(int64_t cols) {
+    const int64_t nq = (cols + 3) / 4;
+    if (nq <= 64) return {64, 1};
+    for (int threads = 64; threads < 1024; threads *= 2)
+        if (nq <= 3 * threads) return {threads, static_cast<int>((nq + threads - 1) / threads)};
+    return {1024, static_cast<int>((nq + 1023) / 1024)};
+}
+
 int64_t norm_workspace_floats(int64_t rows, int64_t cols) {
     if (rows == 0 || cols == 0) return 0;
+    if (bwd_in_registers(cols)) return 2 * bwd_groups(rows, cols) * cols;
     int64_t n, r;
     if (__builtin_mul_overflow(2 * plan_walk(rows, cols).chunks, cols, &n)) return -1;
     if (__builtin_mul_overflow(rows, int64_t{2}, &r) || __builtin_add_overflow(r, 3, &r) ||
@@ -798,7 +815,7 @@ int64_t norm_workspace_floats(int64_t rows, int64_t cols) {
 int64_t act_workspace_floats(int64_t rows, int64_t cols) {
     if (rows == 0 || cols == 0) return 0;
     int64_t n;
-    return __builtin_mul_overflow(plan_walk(rows, cols).chunks, cols, &n) ? -1 : n;
+    return __builtin_mul_overflow(act_tiles(rows, cols).down, cols, &n) ? -1 : n;
 }
 
 hipError_t launch_act_forward(const ActFwd& a, hipStream_t stream) {
@@ -809,26 +826,39 @@ hipError_t launch_unpack(int64_t rows, int64_t cols, bool bf16, const CkptRows& 
                          hipStream_t stream) {
     return for_tiles(rows, cols, [&](int64_t r, int64_t n, uint32_t across, int k, uint32_t blocks) {
         if (bf16)
-            unpack_kernel<uint16_t><<<blocks, kThreads, 0, stream>>>(n, cols, skip(q, r), skip(x, r, true), k, across);
+            unpack_kernel<uint16_t><<<blocks, kThreads, 0, stream>>>(n, cols, skip(q, r), skip(x, r, true), k, across, xcd_run(blocks));
         else
-            unpack_kernel<float><<<blocks, kThreads, 0, stream>>>(n, cols, skip(q, r), skip(x, r, false), k, across);
+            unpack_kernel<float><<<blocks, kThreads, 0, stream>>>(n, cols, skip(q, r), skip(x, r, false), k, across, xcd_run(blocks));
     });
 }
 
 hipError_t launch_act_backward(const ActBwd& a, hipStream_t stream) {
-    const Walk w = plan_walk(a.rows, a.cols);
-    if (a.rows > 0) {
+    const Tiles t = act_tiles(a.rows, a.cols);
+    // runs of rows, as in the forward pass; each run's partial rows follow those before
+    const int64_t high = static_cast<int64_t>(kActThreads >> t.k) * kActRows;
+    const int64_t run = std::max<int64_t>(1, kMaxBlocks / 2 / t.across) * high;
+    for (int64_t r = 0; r < a.rows; r += run) {
+        ActBwd b = a;
+        b.rows = std::min(run, a.rows - r);
+        b.dy = skip(a.dy, r, a.bf16);
+        b.x = skip(a.x, r, a.bf16);
+        b.ckpt = skip(a.ckpt, r);
+        b.dx = skip(a.dx, r, a.bf16);
+        b.y = skip(a.y, r, a.bf16);
+        if (a.dbias.p) b.workspace = a.workspace + r / high * a.cols;
+        Tiles u = t;
+        u.down = (b.rows + high - 1) / high;
         if (a.bf16) {
-            if (a.ckpt.codes) act_backward_t<uint16_t, true>(a, w, stream);
-            else act_backward_t<uint16_t, false>(a, w, stream);
+            if (a.ckpt.codes) act_backward_t<uint16_t, true>(b, u, stream);
+            else act_backward_t<uint16_t, false>(b, u, stream);
         } else {
-            if (a.ckpt.codes) act_backward_t<float, true>(a, w, stream);
-            else act_backward_t<float, false>(a, w, stream);
+            if (a.ckpt.codes) act_backward_t<float, true>(b, u, stream);
+            else act_backward_t<float, false>(b, u, stream);
         }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    return launch_col_sum(a.workspace, w.chunks, a.cols, a.cols, a.dbias, ColOut{nullptr, 0, 0}, stream);
+    return launch_col_sum(a.workspace, t.down, a.cols, a.cols, a.dbias, ColOut{nullptr, 0, 0}, stream);
 }
 
 hipError_t launch_norm_forward(const NormFwd& a, hipStream_t stream) {
@@ -842,8 +872,8 @@ hipError_t launch_norm_forward(const NormFwd& a, hipStream_t stream) {
         b.ckpt = skip(a.ckpt, r);
         if (a.mean) b.mean = a.mean + r;
         b.rstd = a.rstd + r;
-        if (a.bf16) norm_fwd_long_kernel<uint16_t><<<static_cast<uint32_t>(b.rows), kThreads, 0, stream>>>(b);
-        else norm_fwd_long_kernel<float><<<static_cast<uint32_t>(b.rows), kThreads, 0, stream>>>(b);
+        if (a.bf16) norm_forward_t<uint16_t>(b, stream);
+        else norm_forward_t<float>(b, stream);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

@@ -1,0 +1,358 @@
+// norm_backward.h -- the norms' backward pass for rows that fit in registers; compiled for each
+// activation type in norm_backward_bf16.hip and norm_backward_f32.hip.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "layer.h"
+#include "layer_dev.h"
+
+#pragma clang fp contract(fast)
+
+namespace fsdp {
+namespace {
+
+// Vectors of 4 columns: the column sums, a row's values and the next row's loads are all in
+// registers, and narrower vectors leave fewer of them unused.
+constexpr int kQ = 4;
+typedef uint32_t u1e __attribute__((aligned(1)));
+typedef uint32_t u2h __attribute__((ext_vector_type(2), aligned(2)));
+template <typename T> struct Quad;
+template <> struct Quad<uint16_t> {
+    u2 r;
+    __device__ void load(const uint16_t* p) { r = __builtin_nontemporal_load((const u2h*)p); }
+    // drops the first k elements, zeros behind the last
+    __device__ void drop(int k) {
+        r = __builtin_bit_cast(u2, __builtin_bit_cast(uint64_t, r) >> (16 * k));
+    }
+    __device__ void get(float* v) const {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            v[2 * j] = __builtin_bit_cast(float, r[j] << 16);
+            v[2 * j + 1] = __builtin_bit_cast(float, r[j] & 0xFFFF0000u);
+        }
+    }
+    __device__ static void put(uint16_t* p, const float* v, int n) {
+        u2 r;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            r[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v[2 * j], v[2 * j + 1]}), bf2));
+        if (n >= kQ) {
+            __builtin_nontemporal_store(r, (u2h*)p);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < kQ; ++j)
+            if (j < n) p[j] = static_cast<uint16_t>(r[j >> 1] >> (16 * (j & 1)));
+    }
+};
+template <> struct Quad<float> {
+    f4 r;
+    __device__ void load(const float* p) { r = __builtin_nontemporal_load((const f4e*)p); }
+    __device__ void drop(int k) {
+        if (k & 1) r = f4{r[1], r[2], r[3], 0.0f};
+        if (k & 2) r = f4{r[2], r[3], 0.0f, 0.0f};
+    }
+    __device__ void get(float* v) const {
+#pragma unroll
+        for (int j = 0; j < kQ; ++j) v[j] = r[j];
+    }
+    __device__ static void put(float* p, const float* v, int n) {
+        if (n >= kQ) {
+            __builtin_nontemporal_store(f4{v[0], v[1], v[2], v[3]}, (f4e*)p);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < kQ; ++j)
+            if (j < n) p[j] = v[j];
+    }
+};
+// 4 values of a parameter, 0 outside its n.
+__device__ __forceinline__ f4 param4(const void* w, bool bf16, int64_t c, int n) {
+    f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (bf16) {
+        const uint16_t* p = static_cast<const uint16_t*>(w) + c;
+        if (n >= kQ) {
+            const u2 r = *(const u2h*)p;
+            v = f4{__builtin_bit_cast(float, r[0] << 16), __builtin_bit_cast(float, r[0] & 0xFFFF0000u),
+                   __builtin_bit_cast(float, r[1] << 16), __builtin_bit_cast(float, r[1] & 0xFFFF0000u)};
+        } else {
+            for (int j = 0; j < n; ++j) v[j] = __builtin_bit_cast(float, uint32_t{p[j]} << 16);
+        }
+    } else {
+        const float* p = static_cast<const float*>(w) + c;
+        if (n >= kQ) v = *(const f4e*)p;
+        else
+            for (int j = 0; j < n; ++j) v[j] = p[j];
+    }
+    return v;
+}
+template <bool kInt8>
+__device__ __forceinline__ void decode4(uint32_t q, uint32_t byte, float* v) {
+    const float s = scale_value(byte);
+    if constexpr (kInt8) {
+        const uint32_t u = q ^ 0x80808080u;   // offset by 128
+#pragma unroll
+        for (int j = 0; j < kQ; ++j) v[j] = (static_cast<float>((u >> (8 * j)) & 0xFFu) - 128.0f) * s;
+    } else {
+        const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q), false);
+        const f2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q), true);
+        v[0] = a[0] * s;
+        v[1] = a[1] * s;
+        v[2] = b[0] * s;
+        v[3] = b[1] * s;
+    }
+}
+
+// Partial sums, which the next kernel reads.
+__device__ __forceinline__ void keep(float* p, const float* v, int n) {
+    if (n >= kQ) {
+        *(f4e*)p = f4{v[0], v[1], v[2], v[3]};
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < kQ; ++j)
+        if (j < n) p[j] = v[j];
+}
+
+// Where the input comes from.
+enum { kTensor = 0, kE4m3 = 1, kInt8 = 2 };
+
+// What a row's backward pass reads, in flight.
+template <typename T, int kSrc, bool kRes, int kN>
+struct BwdRow {
+    Quad<T> dy[kN], x[kSrc == kTensor ? kN : 1], r[kRes ? kN : 1];
+    uint32_t q[kSrc == kTensor ? 1 : kN], byte[kSrc == kTensor ? 1 : kN];
+    float mean, rstd;
+    // at[i]: the column that vector i is read from, group[i]: its scale.  A row past the last
+    // is not branched around, which would have the compiler wait for loads that it cannot count:
+    // the last row's first columns are read instead, by all lanes at once.
+    __device__ __forceinline__ void load(const NormBwd& a, int64_t row, const int* at, const int* group) {
+        const int mask = row < a.rows ? -1 : 0;
+        row = row < a.rows ? row : a.rows - 1;
+        const T* dp = static_cast<const T*>(a.dy.p) + row * a.dy.pitch;
+        const T* xp = static_cast<const T*>(a.x.p) + row * a.x.pitch;
+        const T* rp = static_cast<const T*>(a.dres.p) + row * a.dres.pitch;
+        const uint8_t* qp = a.ckpt.codes + row * a.ckpt.code_pitch;
+        const uint8_t* sp = a.ckpt.scales + row * a.ckpt.scale_pitch;
+        rstd = a.rstd[row];
+        mean = a.rms ? 0.0f : a.mean[row];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int c = at[i] & mask;
+            dy[i].load(dp + c);
+            if constexpr (kSrc != kTensor) {
+                q[i] = __builtin_nontemporal_load((const u1e*)(qp + c));
+                byte[i] = sp[group[i] & mask];
+            } else {
+                x[i].load(xp + c);
+            }
+            if constexpr (kRes) r[i].load(rp + c);
+        }
+    }
+    __device__ __forceinline__ void drop(int i, int k) {
+        dy[i].drop(k);
+        if constexpr (kSrc != kTensor) q[i] >>= 8 * k;
+        else x[i].drop(k);
+        if constexpr (kRes) r[i].drop(k);
+    }
+    __device__ __forceinline__ void input(int i, float* v) const {
+        if constexpr (kSrc == kTensor) x[i].get(v);
+        else decode4<kSrc == kInt8>(q[i], byte[i], v);
+    }
+};
+
+// A workgroup is 8 waves, or the 16 of a row that takes as many.
+template <int kT> constexpr int bwd_threads() { return kT < 512 ? 512 : kT; }
+
+// Row groups of kT threads, kN vectors a thread, take rows g, g + groups, ... with the next row's
+// loads in flight, and keep the column sums of all their rows in registers; a workgroup adds up
+// its groups' sums and writes one partial row of each.  Weight and bias lie in LDS: read as
+// memory, they would make a row wait for the next one's loads, which return in order.  kWhole:
+// the columns are a multiple of 4; else the vector that the row's end cuts is read from the row's
+// last 4 columns.  A vector outside the row reads its first columns, which a weight of 0 and no
+// stores make harmless.
+template <typename T, int kSrc, bool kRes, int kT, int kN, bool kWhole>
+__global__ void __launch_bounds__(bwd_threads<kT>()) norm_bwd_kernel(NormBwd a, float* partial) {
+    constexpr int kW = bwd_threads<kT>(), kRows = kW / kT;
+    __shared__ f4 lw[kT * kN], lb[kT * kN];
+    __shared__ float lds[2][2 * (kW / 64)];
+    const int t = threadIdx.x % kT;
+    const int mine = kRows > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / kT) : 0;
+    const int64_t groups = static_cast<int64_t>(gridDim.x) * kRows;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + mine;
+    const int cols = static_cast<int>(a.cols);
+    const float inv = 1.0f / static_cast<float>(cols);
+    const bool again = a.y.p != nullptr;
+    int at[kN], group[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const int c = (t + i * kT) * kQ;
+        at[i] = c < cols ? (kWhole ? c : min(c, cols - kQ)) : 0;
+        group[i] = c < cols ? c / kCkptGroup : 0;
+    }
+    typedef BwdRow<T, kSrc, kRes, kN> Row;
+    Row even, odd;
+    even.load(a, row, at, group);
+    for (int v = threadIdx.x; v < kT * kN; v += kW) {
+        lw[v] = param4(a.weight, a.param_bf16, v * kQ, cols - v * kQ);
+        if (again && a.bias) lb[v] = param4(a.bias, a.param_bf16, v * kQ, cols - v * kQ);
+        else lb[v] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    __syncthreads();
+    float sw[kN][kQ] = {}, sb[kN][kQ] = {};
+
+    // One row of each group; `half` alternates, for a row's sums must not overwrite those that a
+    // slower wave still reads for the row before.
+    const auto step = [&](Row& now, int half) __attribute__((always_inline)) {
+        const bool live = row < a.rows;   // groups of several waves meet at the barrier also without a row
+        const float rstd = now.rstd;
+        float s0 = 0.0f, s1 = 0.0f, xh[kN][kQ], gw[kN][kQ];
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const int c = (t + i * kT) * kQ;
+                if constexpr (!kWhole) now.drop(i, c < cols ? c - at[i] : 0);
+                float g[kQ];
+                now.input(i, xh[i]);
+                now.dy[i].get(g);
+                const f4 w = lw[t + i * kT];
+#pragma unroll
+                for (int j = 0; j < kQ; ++j) {
+                    xh[i][j] = (xh[i][j] - now.mean) * rstd;
+                    sw[i][j] += g[j] * xh[i][j];
+                    sb[i][j] += g[j];
+                    gw[i][j] = g[j] * w[j];
+                    s0 += gw[i][j];
+                    s1 += gw[i][j] * xh[i][j];
+                }
+            }
+        }
+        s0 = wave_sum(s0);
+        s1 = wave_sum(s1);
+        if constexpr (kT > 64) {
+            if ((threadIdx.x & 63) == 0) {
+                lds[half][2 * (threadIdx.x >> 6)] = s0;
+                lds[half][2 * (threadIdx.x >> 6) + 1] = s1;
+            }
+            __syncthreads();
+            // every lane takes one wave's sums, and lanes next to each other add up
+            constexpr int kWaves = kT / 64;
+            const int l = 2 * (mine * kWaves + (threadIdx.x & (kWaves - 1)));
+            s0 = add_lanes<kWaves>(lds[half][l]);
+            s1 = add_lanes<kWaves>(lds[half][l + 1]);
+        }
+        if (!live) return;
+        // dx = rstd gw - (rstd c2) xh - rstd c1
+        const float c1 = a.rms ? 0.0f : s0 * inv * rstd, c2 = s1 * inv * rstd;
+        T* dxp = static_cast<T*>(a.dx.p) + row * a.dx.pitch;
+        T* yp = static_cast<T*>(a.y.p) + row * a.y.pitch;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int c = (t + i * kT) * kQ, n = kWhole ? kQ : cols - c;
+            float d[kQ], r[kQ] = {};
+            if constexpr (kRes) now.r[i].get(r);
+#pragma unroll
+            for (int j = 0; j < kQ; ++j) d[j] = gw[i][j] * rstd - (xh[i][j] * c2 + c1) + r[j];
+            if (c < cols) Quad<T>::put(dxp + c, d, n);
+            if (again) {
+                const f4 w = lw[t + i * kT], b = lb[t + i * kT];
+#pragma unroll
+                for (int j = 0; j < kQ; ++j) d[j] = xh[i][j] * w[j] + b[j];
+                if (c < cols) Quad<T>::put(yp + c, d, n);
+            }
+        }
+    };
+    // all groups of a workgroup go on while its first one has a row
+    while (true) {
+        odd.load(a, row + groups, at, group);
+        step(even, 0);
+        row += groups;
+        if (row - mine >= a.rows) break;
+        even.load(a, row + groups, at, group);
+        step(odd, 1);
+        row += groups;
+        if (row - mine >= a.rows) break;
+    }
+    // the workgroup's row groups add up in LDS, one after another
+    if constexpr (kRows > 1) {
+        for (int v = 0; v < kRows; ++v) {
+            __syncthreads();
+            if (mine == v) {
+#pragma unroll
+                for (int i = 0; i < kN; ++i) {
+                    const int l = t + i * kT;
+                    f4 w = {sw[i][0], sw[i][1], sw[i][2], sw[i][3]}, b = {sb[i][0], sb[i][1], sb[i][2], sb[i][3]};
+                    if (v) {
+                        w += lw[l];
+                        b += lb[l];
+                    }
+                    lw[l] = w;
+                    lb[l] = b;
+                }
+            }
+        }
+        __syncthreads();
+    }
+    // and all of its threads write them
+    float* out = partial + static_cast<int64_t>(blockIdx.x) * 2 * cols;
+    if constexpr (kRows > 1) {
+        for (int v = threadIdx.x; v < kT * kN; v += kW) {
+            const f4 w = lw[v], b = lb[v];
+            const float ws[kQ] = {w[0], w[1], w[2], w[3]}, bs[kQ] = {b[0], b[1], b[2], b[3]};
+            const int n = cols - v * kQ;
+            if (a.dweight.p) keep(out + v * kQ, ws, n);
+            if (a.dbias.p) keep(out + cols + v * kQ, bs, n);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int c = (t + i * kT) * kQ;
+            if (a.dweight.p) keep(out + c, sw[i], cols - c);
+            if (a.dbias.p) keep(out + cols + c, sb[i], cols - c);
+        }
+    }
+}
+
+template <typename T, int kSrc, bool kRes, int kT, int kN>
+void norm_bwd_run(const NormBwd& a, float* partial, uint32_t blocks, hipStream_t stream) {
+    if (a.cols % kQ == 0) norm_bwd_kernel<T, kSrc, kRes, kT, kN, true><<<blocks, bwd_threads<kT>(), 0, stream>>>(a, partial);
+    else norm_bwd_kernel<T, kSrc, kRes, kT, kN, false><<<blocks, bwd_threads<kT>(), 0, stream>>>(a, partial);
+}
+template <typename T, int kSrc, bool kRes>
+void norm_bwd_shaped(const NormBwd& a, float* partial, uint32_t blocks, hipStream_t stream) {
+    const BwdShape s = norm_bwd_shape(a.cols);
+    switch (s.threads + s.vectors) {
+#define FSDP_SHAPE(kT, kN) case kT + kN: return norm_bwd_run<T, kSrc, kRes, kT, kN>(a, partial, blocks, stream)
+        FSDP_SHAPE(64, 1);
+        FSDP_SHAPE(64, 2);
+        FSDP_SHAPE(64, 3);
+        FSDP_SHAPE(128, 2);
+        FSDP_SHAPE(128, 3);
+        FSDP_SHAPE(256, 2);
+        FSDP_SHAPE(256, 3);
+        FSDP_SHAPE(512, 2);
+        FSDP_SHAPE(512, 3);
+        FSDP_SHAPE(1024, 2);
+        FSDP_SHAPE(1024, 3);
+        FSDP_SHAPE(1024, 4);
+#undef FSDP_SHAPE
+    }
+}
+template <typename T, int kSrc>
+void norm_bwd_res(const NormBwd& a, float* partial, uint32_t blocks, hipStream_t stream) {
+    if (a.dres.p) norm_bwd_shaped<T, kSrc, true>(a, partial, blocks, stream);
+    else norm_bwd_shaped<T, kSrc, false>(a, partial, blocks, stream);
+}
+template <typename T>
+void norm_bwd_rows(const NormBwd& a, float* partial, uint32_t blocks, hipStream_t stream) {
+    if (!a.ckpt.codes) norm_bwd_res<T, kTensor>(a, partial, blocks, stream);
+    else if (a.ckpt.int8) norm_bwd_res<T, kInt8>(a, partial, blocks, stream);
+    else norm_bwd_res<T, kE4m3>(a, partial, blocks, stream);
+}
+
+}  // namespace
+}  // namespace fsdp
