@@ -787,8 +787,10 @@ hipError_t norm_backward_t(const NormBwd& a, hipStream_t stream) {
         norm_bwd_tile_kernel<T, kCkpt><<<static_cast<uint32_t>(w.chunks * w.t.across), kThreads, 0, stream>>>(
             a, stat, partial, w.t.k, w.t.across, w.per);
     }
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (a.rows > 0) {
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     return launch_col_sum(partial, G, 2 * a.cols, a.cols, a.dweight, a.dbias, stream);
 }
 

@@ -94,9 +94,8 @@ template <bool kInt8>
 __device__ __forceinline__ void decode4(uint32_t q, uint32_t byte, float* v) {
     const float s = scale_value(byte);
     if constexpr (kInt8) {
-        const uint32_t u = q ^ 0x80808080u;   // offset by 128
 #pragma unroll
-        for (int j = 0; j < kQ; ++j) v[j] = (static_cast<float>((u >> (8 * j)) & 0xFFu) - 128.0f) * s;
+        for (int j = 0; j < kQ; ++j) v[j] = static_cast<float>(static_cast<int8_t>(q >> (8 * j))) * s;
     } else {
         const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q), false);
         const f2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q), true);
@@ -118,6 +117,16 @@ __device__ __forceinline__ void keep(float* p, const float* v, int n) {
         if (j < n) p[j] = v[j];
 }
 
+// p + i as a scalar address and an unsigned 32-bit offset, which the memory instructions add.
+template <typename T>
+__device__ __forceinline__ const T* from(const T* p, uint32_t i) {
+    return reinterpret_cast<const T*>(reinterpret_cast<const char*>(p) + i * static_cast<uint32_t>(sizeof(T)));
+}
+template <typename T>
+__device__ __forceinline__ T* from(T* p, uint32_t i) {
+    return reinterpret_cast<T*>(reinterpret_cast<char*>(p) + i * static_cast<uint32_t>(sizeof(T)));
+}
+
 // Where the input comes from.
 enum { kTensor = 0, kE4m3 = 1, kInt8 = 2 };
 
@@ -130,8 +139,8 @@ struct BwdRow {
     // at[i]: the column that vector i is read from, group[i]: its scale.  A row past the last
     // is not branched around, which would have the compiler wait for loads that it cannot count:
     // the last row's first columns are read instead, by all lanes at once.
-    __device__ __forceinline__ void load(const NormBwd& a, int64_t row, const int* at, const int* group) {
-        const int mask = row < a.rows ? -1 : 0;
+    __device__ __forceinline__ void load(const NormBwd& a, int64_t row, const uint32_t* at, const uint32_t* group) {
+        const uint32_t mask = row < a.rows ? ~0u : 0u;
         row = row < a.rows ? row : a.rows - 1;
         const T* dp = static_cast<const T*>(a.dy.p) + row * a.dy.pitch;
         const T* xp = static_cast<const T*>(a.x.p) + row * a.x.pitch;
@@ -139,18 +148,18 @@ struct BwdRow {
         const uint8_t* qp = a.ckpt.codes + row * a.ckpt.code_pitch;
         const uint8_t* sp = a.ckpt.scales + row * a.ckpt.scale_pitch;
         rstd = a.rstd[row];
-        mean = a.rms ? 0.0f : a.mean[row];
+        mean = (a.rms ? a.rstd : a.mean)[row];   // no branch between the loads either
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            const int c = at[i] & mask;
-            dy[i].load(dp + c);
+            const uint32_t c = at[i] & mask;   // unsigned: added to a scalar address as it is
+            dy[i].load(from(dp, c));
             if constexpr (kSrc != kTensor) {
-                q[i] = __builtin_nontemporal_load((const u1e*)(qp + c));
-                byte[i] = sp[group[i] & mask];
+                q[i] = *(const u1e*)from(qp, c);   // cached: 256 bytes a wave, lines shared by two (nt: 3-9% slower)
+                byte[i] = *from(sp, group[i] & mask);
             } else {
-                x[i].load(xp + c);
+                x[i].load(from(xp, c));
             }
-            if constexpr (kRes) r[i].load(rp + c);
+            if constexpr (kRes) r[i].load(from(rp, c));
         }
     }
     __device__ __forceinline__ void drop(int i, int k) {
@@ -187,12 +196,12 @@ __global__ void __launch_bounds__(bwd_threads<kT>()) norm_bwd_kernel(NormBwd a, 
     const int cols = static_cast<int>(a.cols);
     const float inv = 1.0f / static_cast<float>(cols);
     const bool again = a.y.p != nullptr;
-    int at[kN], group[kN];
+    uint32_t at[kN], group[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
         const int c = (t + i * kT) * kQ;
-        at[i] = c < cols ? (kWhole ? c : min(c, cols - kQ)) : 0;
-        group[i] = c < cols ? c / kCkptGroup : 0;
+        at[i] = static_cast<uint32_t>(c < cols ? (kWhole ? c : min(c, cols - kQ)) : 0);
+        group[i] = static_cast<uint32_t>(c < cols ? c / kCkptGroup : 0);
     }
     typedef BwdRow<T, kSrc, kRes, kN> Row;
     Row even, odd;
@@ -208,21 +217,22 @@ __global__ void __launch_bounds__(bwd_threads<kT>()) norm_bwd_kernel(NormBwd a, 
     // One row of each group; `half` alternates, for a row's sums must not overwrite those that a
     // slower wave still reads for the row before.
     const auto step = [&](Row& now, int half) __attribute__((always_inline)) {
-        const bool live = row < a.rows;   // groups of several waves meet at the barrier also without a row
-        const float rstd = now.rstd;
+        // groups of several waves meet at the barrier also without a row
+        const bool live = kT == 64 || kRows == 1 || row < a.rows;
+        const float rstd = now.rstd, mean = a.rms ? 0.0f : now.mean;
         float s0 = 0.0f, s1 = 0.0f, xh[kN][kQ], gw[kN][kQ];
         if (live) {
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
                 const int c = (t + i * kT) * kQ;
-                if constexpr (!kWhole) now.drop(i, c < cols ? c - at[i] : 0);
+                if constexpr (!kWhole) now.drop(i, c < cols ? c - static_cast<int>(at[i]) : 0);
                 float g[kQ];
                 now.input(i, xh[i]);
                 now.dy[i].get(g);
                 const f4 w = lw[t + i * kT];
 #pragma unroll
                 for (int j = 0; j < kQ; ++j) {
-                    xh[i][j] = (xh[i][j] - now.mean) * rstd;
+                    xh[i][j] = (xh[i][j] - mean) * rstd;
                     sw[i][j] += g[j] * xh[i][j];
                     sb[i][j] += g[j];
                     gw[i][j] = g[j] * w[j];
@@ -230,6 +240,11 @@ __global__ void __launch_bounds__(bwd_threads<kT>()) norm_bwd_kernel(NormBwd a, 
                     s1 += gw[i][j] * xh[i][j];
                 }
             }
+        } else {
+            // Loads that nothing uses have to be waited for somewhere before their registers are
+            // loaded again; left to the compiler, that is before every row's loads, where the wait
+            // would be for the row's stores as well.
+            __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
         }
         s0 = wave_sum(s0);
         s1 = wave_sum(s1);
@@ -257,25 +272,25 @@ __global__ void __launch_bounds__(bwd_threads<kT>()) norm_bwd_kernel(NormBwd a, 
             if constexpr (kRes) now.r[i].get(r);
 #pragma unroll
             for (int j = 0; j < kQ; ++j) d[j] = gw[i][j] * rstd - (xh[i][j] * c2 + c1) + r[j];
-            if (c < cols) Quad<T>::put(dxp + c, d, n);
+            if (c < cols) Quad<T>::put(from(dxp, static_cast<uint32_t>(c)), d, n);
             if (again) {
                 const f4 w = lw[t + i * kT], b = lb[t + i * kT];
 #pragma unroll
                 for (int j = 0; j < kQ; ++j) d[j] = xh[i][j] * w[j] + b[j];
-                if (c < cols) Quad<T>::put(yp + c, d, n);
+                if (c < cols) Quad<T>::put(from(yp, static_cast<uint32_t>(c)), d, n);
             }
         }
     };
-    // all groups of a workgroup go on while its first one has a row
-    while (true) {
+    // groups of several waves all go on while the workgroup's first one has a row
+    const int64_t behind = kT == 64 ? 0 : mine;
+    while (row - behind < a.rows) {
         odd.load(a, row + groups, at, group);
         step(even, 0);
         row += groups;
-        if (row - mine >= a.rows) break;
+        if (row - behind >= a.rows) break;
         even.load(a, row + groups, at, group);
         step(odd, 1);
         row += groups;
-        if (row - mine >= a.rows) break;
     }
     // the workgroup's row groups add up in LDS, one after another
     if constexpr (kRows > 1) {

@@ -86,12 +86,18 @@ _ACT_BWD = struct.Struct("@" + "Pq" * 4 + "PPPq")
 _NONE = (0, 0)
 
 _fn = None
+_Tensor = None      # torch.Tensor
+_codes = None       # torch dtype -> fsdp_dtype
+_f32 = None
+_device = None      # the current GPU's index
+_raw_stream = None  # its current stream's handle
 
 
 def _lib():
     """The library, with the argument types of this module's calls set once."""
-    global _fn
+    global _fn, _Tensor, _codes, _f32, _device, _raw_stream
     if _fn is None:
+        import torch
         lib = B.load()
         cfg, io, vp = ctypes.c_char_p, ctypes.c_char_p, ctypes.c_void_p
         i64, i32 = ctypes.c_int64, ctypes.c_int32
@@ -106,65 +112,75 @@ def _lib():
                   lib.fsdp_norm_backward, lib.fsdp_norm_workspace, lib.fsdp_act_forward,
                   lib.fsdp_act_backward, lib.fsdp_act_workspace):
             f.restype = i32
+        _Tensor, _f32 = torch.Tensor, torch.float32
+        _codes = {torch.bfloat16: FSDP_BF16, torch.float32: FSDP_F32}
+        _device = torch.cuda.current_device
+        # the handle alone costs 0.1 us, torch.cuda.current_stream's object 2 us
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
         _fn = lib
     return _fn
 
 
-_codes = None
-
-
 def _dtype_code(t, name: str) -> int:
-    global _codes
-    if _codes is None:
-        import torch
-        _codes = {torch.bfloat16: FSDP_BF16, torch.float32: FSDP_F32}
     try:
         return _codes[t.dtype]
     except KeyError:
         raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype)) from None
 
 
-def _check_tensor(t, name: str, device: int) -> None:
-    if not B._is_tensor(t):
+def _refuse(t, name: str, device: int) -> None:
+    """Why a value is no tensor on this GPU."""
+    if not isinstance(t, _Tensor):
         raise TypeError("%s must be a tensor, got %r" % (name, type(t)))
     if not t.is_cuda:
         # a host address would reach the kernels and fault the GPU
         raise ValueError("tensors passed to the library must be on the GPU, %s is on %s"
                          % (name, t.device))
-    if t.get_device() != device:
-        raise ValueError("%s is on GPU %d, the others are on GPU %d"
-                         % (name, t.get_device(), device))
+    raise ValueError("%s is on GPU %d, the others are on GPU %d" % (name, t.get_device(), device))
 
 
-def _extent(t, name: str):
-    """(rows, cols) of an activation tensor: the last dimension, and the ones before it."""
-    if not B._is_tensor(t):
-        raise TypeError("%s must be a tensor, got %r" % (name, type(t)))
-    if t.dim() == 2:
-        return t.shape[0], t.shape[1]
-    if t.dim() < 1:
+def _first(t, name: str):
+    """(rows, cols, dtype, its code, GPU) of the activation that sets them for a call: the last
+    dimension is cols, the ones before it count as rows."""
+    if _fn is None:
+        _lib()
+    if not isinstance(t, _Tensor):
+        _refuse(t, name, 0)
+    code = _dtype_code(t, name)
+    if not t.is_cuda:
+        _refuse(t, name, 0)
+    shape = t.shape
+    if len(shape) == 2:
+        rows, cols = shape
+    elif shape:
+        cols, rows = shape[-1], 1
+        for d in shape[:-1]:
+            rows *= d
+    else:
         raise ValueError("%s must have at least one dimension" % name)
-    cols = t.shape[-1]
-    rows = 1
-    for d in t.shape[:-1]:
-        rows *= d
-    return rows, cols
+    return rows, cols, t.dtype, code, t.get_device()
 
 
 def _rows(t, name: str, rows: int, cols: int, dtype, device: int):
     """(address, pitch) of an activation of rows x cols elements."""
-    _check_tensor(t, name, device)
-    if t.dtype != dtype:
+    if not isinstance(t, _Tensor) or t.get_device() != device:
+        _refuse(t, name, device)
+    if t.dtype is not dtype:
         raise TypeError("%s is %s, the others are %s" % (name, t.dtype, dtype))
-    if _extent(t, name) != (rows, cols):
-        raise ValueError("%s has shape %s, %d rows of %d columns are needed"
-                         % (name, tuple(t.shape), rows, cols))
-    if t.dim() == 2:
+    shape = t.shape
+    if len(shape) == 2:
+        if shape[0] != rows or shape[1] != cols:
+            raise ValueError("%s has shape %s, %d rows of %d columns are needed"
+                             % (name, tuple(shape), rows, cols))
         pitch, inner = t.stride()
         if inner != 1 and cols > 1:
             raise ValueError("the columns of %s must be next to each other (stride 1), got stride %d"
                              % (name, inner))
         return t.data_ptr(), pitch
+    if _first(t, name)[:2] != (rows, cols):
+        raise ValueError("%s has shape %s, %d rows of %d columns are needed"
+                         % (name, tuple(shape), rows, cols))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous or two-dimensional" % name)
     return t.data_ptr(), cols
@@ -173,8 +189,9 @@ def _rows(t, name: str, rows: int, cols: int, dtype, device: int):
 def _vector(t, name: str, n: int, device: int, dtype=None) -> int:
     if t is None:
         return 0
-    _check_tensor(t, name, device)
-    if dtype is not None and t.dtype != dtype:
+    if not isinstance(t, _Tensor) or t.get_device() != device:
+        _refuse(t, name, device)
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.numel() != n:
         raise ValueError("%s holds %d elements, %d are needed" % (name, t.numel(), n))
@@ -184,10 +201,11 @@ def _vector(t, name: str, n: int, device: int, dtype=None) -> int:
 
 
 def _grad_code(dweight, dbias) -> int:
-    codes = {_dtype_code(t, n) for t, n in ((dweight, "dweight"), (dbias, "dbias")) if t is not None}
-    if len(codes) > 1:
+    if dweight is None:
+        return FSDP_F32 if dbias is None else _dtype_code(dbias, "dbias")
+    if dbias is not None and isinstance(dbias, _Tensor) and dbias.dtype is not dweight.dtype:
         raise TypeError("dweight and dbias must have the same dtype")
-    return codes.pop() if codes else FSDP_F32
+    return _dtype_code(dweight, "dweight")
 
 
 def _kind(kind, names: dict, what: str) -> int:
@@ -197,32 +215,19 @@ def _kind(kind, names: dict, what: str) -> int:
         raise ValueError("%s must be one of %s, got %r" % (what, ", ".join(names), kind)) from None
 
 
-class _on_device:
-    """Makes a tensor's GPU the current one for a call, where it is not."""
-
-    __slots__ = ("device", "was")
-
-    def __init__(self, device: int):
-        self.device = device
-        self.was = None
-
-    def __enter__(self):
+def _call(fn, device: int, stream, *args) -> None:
+    """The call on the tensors' GPU and its current stream, or the one given."""
+    current = _device()
+    if current != device:
         import torch
-        current = torch.cuda.current_device()
-        if current != self.device:
-            self.was = current
-            torch.cuda.set_device(self.device)
-
-    def __exit__(self, *exc):
-        if self.was is not None:
-            import torch
-            torch.cuda.set_device(self.was)
-
-
-def _call(fn, device: int, *args) -> None:
-    with _on_device(device):
-        status = fn(*args)
-    if status != 0:
+        with torch.cuda.device(device):
+            return _call(fn, device, stream, *args)
+    if stream is None:
+        stream = _raw_stream(device)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    status = fn(*args, stream)
+    if status:
         B._check(status)
 
 
@@ -231,8 +236,10 @@ class Ckpt:
     (uint8, rows x ceil(cols / 32)), either with any row stride, and the format, "e4m3" or "int8"."""
 
     def __init__(self, codes, scales, format: str):
+        _lib()
         for t, name in ((codes, "codes"), (scales, "scales")):
-            _check_tensor(t, name, codes.get_device() if B._is_tensor(codes) else 0)
+            if not isinstance(t, _Tensor) or not t.is_cuda or t.get_device() != codes.get_device():
+                _refuse(t, name, codes.get_device() if isinstance(codes, _Tensor) else 0)
             if str(t.dtype) != "torch.uint8" or t.dim() != 2:
                 raise TypeError("%s must be a two-dimensional uint8 tensor" % name)
             if t.shape[1] > 1 and t.stride(1) != 1:
@@ -268,8 +275,6 @@ class Ckpt:
 
 
 def _ckpt(ckpt, rows: int, cols: int, device: int) -> int:
-    if ckpt is None:
-        return 0
     if not isinstance(ckpt, Ckpt):
         raise TypeError("ckpt must be a Ckpt, got %r" % type(ckpt))
     return ckpt.check(rows, cols, device)
@@ -277,35 +282,33 @@ def _ckpt(ckpt, rows: int, cols: int, device: int) -> int:
 
 def fsdp_ckpt_pack(x, ckpt: Ckpt, stream=None) -> None:
     """Save x in 8 bits."""
-    rows, cols = _extent(x, "x")
-    code, dev = _dtype_code(x, "x"), x.get_device()
-    xr = _rows(x, "x", rows, cols, x.dtype, dev)
-    _call(_lib().fsdp_ckpt_pack, dev, rows, cols, code, fsdp_rows(*xr), _ckpt(ckpt, rows, cols, dev),
-          B._stream(stream, x))
+    rows, cols, t, code, dev = _first(x, "x")
+    xr = _rows(x, "x", rows, cols, t, dev)
+    _call(_fn.fsdp_ckpt_pack, dev, stream, rows, cols, code, fsdp_rows(*xr),
+          _ckpt(ckpt, rows, cols, dev))
 
 
 def fsdp_ckpt_unpack(ckpt: Ckpt, x, stream=None) -> None:
     """Write the values a checkpoint holds to x (exact in bf16 and fp32)."""
-    rows, cols = _extent(x, "x")
-    code, dev = _dtype_code(x, "x"), x.get_device()
-    xr = _rows(x, "x", rows, cols, x.dtype, dev)
-    _call(_lib().fsdp_ckpt_unpack, dev, rows, cols, code, _ckpt(ckpt, rows, cols, dev),
-          fsdp_rows(*xr), B._stream(stream, x))
+    rows, cols, t, code, dev = _first(x, "x")
+    xr = _rows(x, "x", rows, cols, t, dev)
+    _call(_fn.fsdp_ckpt_unpack, dev, stream, rows, cols, code, _ckpt(ckpt, rows, cols, dev),
+          fsdp_rows(*xr))
 
 
 def _params(weight, bias, cols: int, dev: int):
+    w = _vector(weight, "weight", cols, dev)
+    if not w and cols:
+        raise TypeError("weight must be a tensor, got %r" % type(weight))
     code = _dtype_code(weight, "weight")
-    return code, _vector(weight, "weight", cols, dev), _vector(bias, "bias", cols, dev, weight.dtype)
+    return code, w, 0 if bias is None else _vector(bias, "bias", cols, dev, weight.dtype)
 
 
 def fsdp_norm_forward(x, weight, bias, y, mean, rstd, *, kind: str = "layer", eps: float = 1e-5,
                       residual=None, sum=None, ckpt=None, stream=None) -> None:
     """y = norm(x) or, with `residual`, norm(x + residual); the sum goes to `sum`, the statistics
     to mean (None for "rms") and rstd, and the norm's input in 8 bits to `ckpt`, where given."""
-    import torch
-    rows, cols = _extent(x, "x")
-    t, dev = x.dtype, x.get_device()
-    code = _dtype_code(x, "x")
+    rows, cols, t, code, dev = _first(x, "x")
     pcode, w, b = _params(weight, bias, cols, dev)
     cfg = _CFG.pack(rows, cols, code, pcode, FSDP_F32, 0, _kind(kind, _NORMS, "kind"), eps)
     io = _NORM_FWD.pack(
@@ -313,9 +316,9 @@ def fsdp_norm_forward(x, weight, bias, y, mean, rstd, *, kind: str = "layer", ep
         *(_NONE if residual is None else _rows(residual, "residual", rows, cols, t, dev)),
         *(_NONE if sum is None else _rows(sum, "sum", rows, cols, t, dev)),
         *_rows(y, "y", rows, cols, t, dev), w, b,
-        _vector(mean, "mean", rows, dev, torch.float32),
-        _vector(rstd, "rstd", rows, dev, torch.float32), _ckpt(ckpt, rows, cols, dev))
-    _call(_lib().fsdp_norm_forward, dev, cfg, io, B._stream(stream, x))
+        _vector(mean, "mean", rows, dev, _f32), _vector(rstd, "rstd", rows, dev, _f32),
+        0 if ckpt is None else _ckpt(ckpt, rows, cols, dev))
+    _call(_fn.fsdp_norm_forward, dev, stream, cfg, io)
 
 
 def fsdp_norm_workspace(rows: int, cols: int) -> int:
@@ -326,17 +329,17 @@ def fsdp_norm_workspace(rows: int, cols: int) -> int:
 
 
 def _input(x, rows: int, cols: int, t, dev: int):
-    """((address, pitch), ckpt) of a backward pass's input, a tensor or a checkpoint."""
+    """(address, pitch, checkpoint) of a backward pass's input, a tensor or a checkpoint."""
     if isinstance(x, Ckpt):
-        return _NONE, x.check(rows, cols, dev)
-    return _rows(x, "x", rows, cols, t, dev), 0
+        return 0, 0, x.check(rows, cols, dev)
+    return (*_rows(x, "x", rows, cols, t, dev), 0)
 
 
 def _workspace(ws, dev: int):
-    import torch
     if ws is None:
         return 0, 0
-    return _vector(ws, "workspace", ws.numel(), dev, torch.float32), ws.numel()
+    n = ws.numel() if isinstance(ws, _Tensor) else 0
+    return _vector(ws, "workspace", n, dev, _f32), n
 
 
 def fsdp_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, *,
@@ -345,36 +348,29 @@ def fsdp_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace,
     """Gradients of the norm's input (plus `dres`, where given), weight and bias (either may be
     None) from the input x, a tensor or a Ckpt; `y` receives the norm's output again (`bias` is
     read for it alone).  With `accumulate` dweight and dbias are added to."""
-    import torch
-    rows, cols = _extent(dy, "dy")
-    t, dev = dy.dtype, dy.get_device()
-    code = _dtype_code(dy, "dy")
+    rows, cols, t, code, dev = _first(dy, "dy")
     pcode, w, b = _params(weight, bias, cols, dev)
-    gcode = _grad_code(dweight, dbias)
-    xr, q = _input(x, rows, cols, t, dev)
-    cfg = _CFG.pack(rows, cols, code, pcode, gcode, 1 if accumulate else 0,
+    xp, xpitch, q = _input(x, rows, cols, t, dev)
+    dw, db = _vector(dweight, "dweight", cols, dev), _vector(dbias, "dbias", cols, dev)
+    cfg = _CFG.pack(rows, cols, code, pcode, _grad_code(dweight, dbias), 1 if accumulate else 0,
                     _kind(kind, _NORMS, "kind"), 0.0)
     io = _NORM_BWD.pack(
-        *_rows(dy, "dy", rows, cols, t, dev), *xr,
+        *_rows(dy, "dy", rows, cols, t, dev), xp, xpitch,
         *(_NONE if dres is None else _rows(dres, "dres", rows, cols, t, dev)),
         *_rows(dx, "dx", rows, cols, t, dev),
         *(_NONE if y is None else _rows(y, "y", rows, cols, t, dev)), q, w, b,
-        _vector(mean, "mean", rows, dev, torch.float32),
-        _vector(rstd, "rstd", rows, dev, torch.float32),
-        _vector(dweight, "dweight", cols, dev), _vector(dbias, "dbias", cols, dev),
+        _vector(mean, "mean", rows, dev, _f32), _vector(rstd, "rstd", rows, dev, _f32), dw, db,
         *_workspace(workspace, dev))
-    _call(_lib().fsdp_norm_backward, dev, cfg, io, B._stream(stream, dy))
+    _call(_fn.fsdp_norm_backward, dev, stream, cfg, io)
 
 
 def fsdp_act_forward(x, y, *, kind: str, ckpt=None, stream=None) -> None:
     """y = f(x), f one of "relu", "gelu", "gelu_tanh", "silu"; x in 8 bits to `ckpt`, where given."""
-    rows, cols = _extent(x, "x")
-    t, dev = x.dtype, x.get_device()
-    cfg = _CFG.pack(rows, cols, _dtype_code(x, "x"), FSDP_F32, FSDP_F32, 0,
-                    _kind(kind, _ACTS, "kind"), 0.0)
+    rows, cols, t, code, dev = _first(x, "x")
+    cfg = _CFG.pack(rows, cols, code, FSDP_F32, FSDP_F32, 0, _kind(kind, _ACTS, "kind"), 0.0)
     io = _ACT_FWD.pack(*_rows(x, "x", rows, cols, t, dev), *_rows(y, "y", rows, cols, t, dev),
-                       _ckpt(ckpt, rows, cols, dev))
-    _call(_lib().fsdp_act_forward, dev, cfg, io, B._stream(stream, x))
+                       0 if ckpt is None else _ckpt(ckpt, rows, cols, dev))
+    _call(_fn.fsdp_act_forward, dev, stream, cfg, io)
 
 
 def fsdp_act_workspace(rows: int, cols: int) -> int:
@@ -388,13 +384,13 @@ def fsdp_act_backward(dy, x, dx, dbias=None, workspace=None, *, kind: str, y=Non
                       accumulate: bool = False, stream=None) -> None:
     """dx = dy f'(x) from the input x, a tensor or a Ckpt; dbias (optional) receives the column
     sums of dx, y (optional) the activation's output again."""
-    rows, cols = _extent(dy, "dy")
-    t, dev = dy.dtype, dy.get_device()
-    xr, q = _input(x, rows, cols, t, dev)
-    cfg = _CFG.pack(rows, cols, _dtype_code(dy, "dy"), FSDP_F32, _grad_code(None, dbias),
-                    1 if accumulate else 0, _kind(kind, _ACTS, "kind"), 0.0)
-    io = _ACT_BWD.pack(*_rows(dy, "dy", rows, cols, t, dev), *xr,
+    rows, cols, t, code, dev = _first(dy, "dy")
+    xp, xpitch, q = _input(x, rows, cols, t, dev)
+    db = _vector(dbias, "dbias", cols, dev)
+    cfg = _CFG.pack(rows, cols, code, FSDP_F32, _grad_code(None, dbias), 1 if accumulate else 0,
+                    _kind(kind, _ACTS, "kind"), 0.0)
+    io = _ACT_BWD.pack(*_rows(dy, "dy", rows, cols, t, dev), xp, xpitch,
                        *_rows(dx, "dx", rows, cols, t, dev),
-                       *(_NONE if y is None else _rows(y, "y", rows, cols, t, dev)), q,
-                       _vector(dbias, "dbias", cols, dev), *_workspace(workspace, dev))
-    _call(_lib().fsdp_act_backward, dev, cfg, io, B._stream(stream, dy))
+                       *(_NONE if y is None else _rows(y, "y", rows, cols, t, dev)), q, db,
+                       *_workspace(workspace, dev))
+    _call(_fn.fsdp_act_backward, dev, stream, cfg, io)

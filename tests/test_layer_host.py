@@ -173,8 +173,9 @@ def test_workspaces(lib):
         assert size(-1, 100, ctypes.byref(n)) == RANGE
         assert size(10, 1 << 31, ctypes.byref(n)) == RANGE
         assert size(10, 100, None) == ARG
-        # a workspace grows with neither size alone past a bounded multiple of one row
-        assert size(1 << 30, 1024, ctypes.byref(n)) == OK and n.value <= 2 * (1 << 30) + 4096 * 2 * 1024
+        # a quarter byte an element at most where there are many, so no more than an eighth of a bf16 matrix
+        for r, c in ((1 << 30, 1024), (1 << 20, 512), (8192, 12288), (2048, 65536), (4096, 100000)):
+            assert size(r, c, ctypes.byref(n)) == OK and 0 < n.value <= r * c // 16 + 2 * r + 4096
 
 
 def test_nothing_to_do_needs_no_buffers(lib):
