@@ -516,16 +516,36 @@ norm_bwd_tile_kernel(NormBwd a, const float* stat, float* partial, int k, uint32
 // ---------------------------------------------------------------------------
 // norms, a row in registers: kT threads (a wave, or a whole workgroup) own a row, kN vectors each
 // ---------------------------------------------------------------------------
-// Thread t of a row owns vectors t, t + kT, ...; with kWhole every vector is whole or outside.
+// Thread t of a row owns vectors t, t + kT, ...; with kWhole every vector is whole or outside, else
+// the one that the row's end cuts is read from the row's last 8 columns, and no load is branched
+// around.
 template <int kT> constexpr int group_threads() { return kT == 64 ? kThreads : kT; }
 
 template <bool kWhole, typename T>
-__device__ __forceinline__ void rload(Vec<T>& v, const T* p, int n) {
+__device__ __forceinline__ void rload(Vec<T>& v, const T* row, int c, int cols) {
     if constexpr (kWhole) {
-        if (n > 0) v.load(p);
+        if (c < cols) v.load(row + c);
         else v.zero();
     } else {
-        vload(v, p, n);
+        v.load(row + (c < cols ? min(c, cols - kV) : 0));
+    }
+}
+// the same of a parameter, which other rows read too
+template <bool kWhole>
+__device__ __forceinline__ void pload(Vec<uint16_t>& v, const uint16_t* p, int c, int cols) {
+    if constexpr (kWhole) {
+        if (c < cols) v.r = *(const u4e*)(p + c);
+        else v.zero();
+    } else {
+        v.r = *(const u4e*)(p + (c < cols ? min(c, cols - kV) : 0));
+    }
+}
+// What a vector read from its row's last 8 columns, or outside of it, has to drop.
+template <bool kWhole, typename T>
+__device__ __forceinline__ void settle(Vec<T>& v, int c, int cols) {
+    if constexpr (!kWhole) {
+        if (c >= cols) v.zero();
+        else if (c > cols - kV) v.drop(c - (cols - kV));
     }
 }
 template <bool kWhole, typename T>
@@ -539,22 +559,35 @@ __device__ __forceinline__ void rput(T* p, const float* f, int n) {
     }
 }
 
-template <typename T, int kT, int kN, bool kWhole>
+// The parameters' loads are issued with the row's (kP16: bf16 parameters, held as they are; fp32
+// ones would take twice the registers and are read when they are used).
+template <typename T, bool kP16, int kT, int kN, bool kWhole>
 __global__ void __launch_bounds__(group_threads<kT>()) norm_fwd_kernel(NormFwd a) {
     constexpr int kRows = group_threads<kT>() / kT;
     __shared__ float lds[2][kT / 64];
     const int t = threadIdx.x % kT;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + (kRows > 1 ? threadIdx.x / kT : 0);
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows +
+                        (kRows > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / kT) : 0);
     if (kRows > 1 && row >= a.rows) return;
     const int cols = static_cast<int>(a.cols);
     float v[kN][kV];
+    Vec<uint16_t> pw[kP16 ? kN : 1], pb[kP16 ? kN : 1];
     {
         Vec<T> x[kN];
         const T* xp = static_cast<const T*>(a.x.p) + row * a.x.pitch;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
             const int c = (t + i * kT) * kV;
-            rload<kWhole>(x[i], xp + c, cols - c);
+            rload<kWhole>(x[i], xp, c, cols);
+        }
+        if constexpr (kP16) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const int c = (t + i * kT) * kV;
+                pload<kWhole>(pw[i], static_cast<const uint16_t*>(a.weight), c, cols);
+                if (a.bias) pload<kWhole>(pb[i], static_cast<const uint16_t*>(a.bias), c, cols);
+                else pb[i].zero();
+            }
         }
         if (a.residual.p) {
             Vec<T> r[kN];
@@ -562,11 +595,14 @@ __global__ void __launch_bounds__(group_threads<kT>()) norm_fwd_kernel(NormFwd a
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
                 const int c = (t + i * kT) * kV;
-                rload<kWhole>(r[i], rp + c, cols - c);
+                rload<kWhole>(r[i], rp, c, cols);
             }
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
                 float u[kV], w[kV];
+                const int c = (t + i * kT) * kV;
+                settle<kWhole>(x[i], c, cols);
+                settle<kWhole>(r[i], c, cols);
                 x[i].get(u);
                 r[i].get(w);
 #pragma unroll
@@ -581,6 +617,9 @@ __global__ void __launch_bounds__(group_threads<kT>()) norm_fwd_kernel(NormFwd a
                     vstore(x[i], sp + c, cols - c);
                 }
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) settle<kWhole>(x[i], (t + i * kT) * kV, cols);
         }
 #pragma unroll
         for (int i = 0; i < kN; ++i) x[i].get(v[i]);
@@ -622,8 +661,15 @@ __global__ void __launch_bounds__(group_threads<kT>()) norm_fwd_kernel(NormFwd a
     for (int i = 0; i < kN; ++i) {
         const int c = (t + i * kT) * kV;
         float w[kV], b[kV] = {};
-        param8(a.weight, a.param_bf16, c, cols - c, w);
-        if (a.bias) param8(a.bias, a.param_bf16, c, cols - c, b);
+        if constexpr (kP16) {
+            settle<kWhole>(pw[i], c, cols);
+            if (a.bias) settle<kWhole>(pb[i], c, cols);
+            pw[i].get(w);
+            pb[i].get(b);
+        } else {
+            param8(a.weight, false, c, cols - c, w);
+            if (a.bias) param8(a.bias, false, c, cols - c, b);
+        }
 #pragma unroll
         for (int j = 0; j < kV; ++j) v[i][j] = (v[i][j] - mean) * rstd * w[j] + b[j];
         rput<kWhole>(yp + c, v[i], cols - c);
@@ -708,7 +754,8 @@ void act_backward_t(const ActBwd& a, const Tiles& w, hipStream_t stream) {
     }
 }
 
-// Rows longer than this take the kernels that read a row again for each pass.
+// Rows longer than this (and those shorter than a vector) take the kernels that read a row again
+// for each pass.
 constexpr int64_t kMaxRowCols = 16384;
 
 // Threads of a row and vectors of a thread for the kernels that hold a row in registers.
@@ -718,8 +765,8 @@ struct RowShape {
 RowShape fwd_shape(int64_t cols) {
     const int64_t nv = (cols + kV - 1) / kV;
     if (nv <= 256) return {64, static_cast<int>((nv + 63) / 64)};
-    const int n = static_cast<int>((nv + 255) / 256);
-    return {256, n <= 2 ? 2 : n <= 4 ? 4 : n <= 6 ? 6 : 8};
+    if (nv <= 1536) return {256, static_cast<int>((nv + 255) / 256)};
+    return {512, 4};
 }
 // Whether the backward pass holds a row of these columns in registers.
 bool bwd_in_registers(int64_t cols) { return cols >= 4 && cols <= kMaxRowCols; }
@@ -736,29 +783,35 @@ template <typename T, int kT, int kN>
 void norm_fwd_run(const NormFwd& a, hipStream_t stream) {
     constexpr int kRows = group_threads<kT>() / kT;
     const uint32_t blocks = static_cast<uint32_t>((a.rows + kRows - 1) / kRows);
-    if (a.cols % kV == 0) norm_fwd_kernel<T, kT, kN, true><<<blocks, group_threads<kT>(), 0, stream>>>(a);
-    else norm_fwd_kernel<T, kT, kN, false><<<blocks, group_threads<kT>(), 0, stream>>>(a);
+    const bool whole = a.cols % kV == 0;
+    if (a.param_bf16) {
+        if (whole) norm_fwd_kernel<T, true, kT, kN, true><<<blocks, group_threads<kT>(), 0, stream>>>(a);
+        else norm_fwd_kernel<T, true, kT, kN, false><<<blocks, group_threads<kT>(), 0, stream>>>(a);
+    } else {
+        if (whole) norm_fwd_kernel<T, false, kT, kN, true><<<blocks, group_threads<kT>(), 0, stream>>>(a);
+        else norm_fwd_kernel<T, false, kT, kN, false><<<blocks, group_threads<kT>(), 0, stream>>>(a);
+    }
 }
 template <typename T>
 void norm_forward_t(const NormFwd& a, hipStream_t stream) {
-    if (a.cols > kMaxRowCols) {
+    if (a.cols < kV || a.cols > kMaxRowCols) {
         norm_fwd_long_kernel<T><<<static_cast<uint32_t>(a.rows), kThreads, 0, stream>>>(a);
         return;
     }
     const RowShape s = fwd_shape(a.cols);
-    if (s.threads == 64) {
-        switch (s.vectors) {
-            case 1: return norm_fwd_run<T, 64, 1>(a, stream);
-            case 2: return norm_fwd_run<T, 64, 2>(a, stream);
-            case 3: return norm_fwd_run<T, 64, 3>(a, stream);
-            default: return norm_fwd_run<T, 64, 4>(a, stream);
-        }
-    }
-    switch (s.vectors) {
-        case 2: return norm_fwd_run<T, 256, 2>(a, stream);
-        case 4: return norm_fwd_run<T, 256, 4>(a, stream);
-        case 6: return norm_fwd_run<T, 256, 6>(a, stream);
-        default: return norm_fwd_run<T, 256, 8>(a, stream);
+    switch (s.threads + s.vectors) {
+#define FSDP_SHAPE(kT, kN) case kT + kN: return norm_fwd_run<T, kT, kN>(a, stream)
+        FSDP_SHAPE(64, 1);
+        FSDP_SHAPE(64, 2);
+        FSDP_SHAPE(64, 3);
+        FSDP_SHAPE(64, 4);
+        FSDP_SHAPE(256, 2);
+        FSDP_SHAPE(256, 3);
+        FSDP_SHAPE(256, 4);
+        FSDP_SHAPE(256, 5);
+        FSDP_SHAPE(256, 6);
+        FSDP_SHAPE(512, 4);
+#undef FSDP_SHAPE
     }
 }
 
