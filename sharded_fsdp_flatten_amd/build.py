@@ -34,8 +34,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libfsdpflat.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 
-SOURCES = ["kernels.hip", "layer.hip", "norm_backward_bf16.hip", "norm_backward_f32.hip",
-           "plan.cpp", "fsdp_abi.cpp"]
+SOURCES = ["norm_backward_bf16.hip", "norm_backward_f32.hip", "norm_backward_bf16_nt.hip",
+           "norm_backward_f32_nt.hip", "layer.hip", "kernels.hip", "plan.cpp", "fsdp_abi.cpp"]
 PROBE_LIB_PATH = os.path.join(HERE, "libfsdpprobe.so")
 PROBE_SOURCES = ["probes.hip"]
 

@@ -95,5 +95,8 @@ struct BwdShape {
 BwdShape norm_bwd_shape(int64_t cols);
 void launch_norm_bwd_rows_bf16(const NormBwd& a, float* partial, uint32_t blocks, hipStream_t stream);
 void launch_norm_bwd_rows_f32(const NormBwd& a, float* partial, uint32_t blocks, hipStream_t stream);
+// the same with non-temporal loads
+void launch_norm_bwd_rows_bf16_nt(const NormBwd& a, float* partial, uint32_t blocks, hipStream_t stream);
+void launch_norm_bwd_rows_f32_nt(const NormBwd& a, float* partial, uint32_t blocks, hipStream_t stream);
 
 }  // namespace fsdp

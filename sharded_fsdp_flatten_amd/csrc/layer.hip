@@ -110,7 +110,7 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t b, uint32_t blocks, uint3
 uint32_t xcd_run(uint32_t blocks) { return blocks >= 4096u ? 64u : 0u; }
 
 // y = f(x) and the checkpoint of x, one tile per workgroup.
-template <typename T, int kF>
+template <typename T, int kF, bool kNt>
 __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActFwd a, int k, uint32_t across, uint32_t run) {
     const uint32_t block = xcd_order(blockIdx.x, gridDim.x, run);
     const uint32_t down = block / across, tile = block - down * across;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActFwd a, int k, uint
     const int64_t c = ((static_cast<int64_t>(tile) << k) + (threadIdx.x & ((1 << k) - 1))) * kV;
     const int n = static_cast<int>(min(a.cols - c, int64_t{kV}));
     Vec<T> x;
-    vload(x, static_cast<const T*>(a.x.p) + row * a.x.pitch + c, n);
+    vload<kNt>(x, static_cast<const T*>(a.x.p) + row * a.x.pitch + c, n);
     float v[kV];
     x.get(v);
     if (a.ckpt.codes) pack8(a.ckpt, row, c, n, v);
@@ -265,12 +265,12 @@ struct ActRow {
     u2 q;
     uint32_t byte;
     __device__ __forceinline__ void load(const ActBwd& a, int64_t row, int64_t c, int64_t group) {
-        dy.load(static_cast<const T*>(a.dy.p) + row * a.dy.pitch + c);
+        dy.template load<true>(static_cast<const T*>(a.dy.p) + row * a.dy.pitch + c);
         if constexpr (kCkpt) {
-            q = __builtin_nontemporal_load((const u2e*)(a.ckpt.codes + row * a.ckpt.code_pitch + c));
+            q = *(const u2e*)(a.ckpt.codes + row * a.ckpt.code_pitch + c);
             byte = a.ckpt.scales[row * a.ckpt.scale_pitch + group];
         } else {
-            x.load(static_cast<const T*>(a.x.p) + row * a.x.pitch + c);
+            x.template load<true>(static_cast<const T*>(a.x.p) + row * a.x.pitch + c);
         }
     }
     // row of fewer than 8 columns
@@ -367,11 +367,11 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_long_kernel(NormFwd a) {
     // every pass adds x and the residual anew, to the same rounded sum
     const auto get = [&](int64_t c, int n, float* v, bool store) {
         Vec<T> t;
-        vload(t, x + c, n);
+        vload<false>(t, x + c, n);
         t.get(v);
         if (res) {
             Vec<T> r;
-            vload(r, res + c, n);
+            vload<false>(r, res + c, n);
             float w[kV];
             r.get(w);
 #pragma unroll
@@ -433,7 +433,7 @@ __device__ __forceinline__ void input8(const NormBwd& a, int64_t row, int64_t c,
                 a.ckpt.scales[row * a.ckpt.scale_pitch + c / kCkptGroup], a.ckpt.int8 != 0, v);
     } else {
         Vec<T> t;
-        vload(t, static_cast<const T*>(a.x.p) + row * a.x.pitch + c, n);
+        vload<false>(t, static_cast<const T*>(a.x.p) + row * a.x.pitch + c, n);
         t.get(v);
     }
 }
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_stat_kernel(NormBwd a, floa
         float x[kV], g[kV], w[kV];
         input8<T, kCkpt>(a, row, c, n, x);
         Vec<T> dy;
-        vload(dy, static_cast<const T*>(a.dy.p) + row * a.dy.pitch + c, n);
+        vload<false>(dy, static_cast<const T*>(a.dy.p) + row * a.dy.pitch + c, n);
         dy.get(g);
         param8(a.weight, a.param_bf16, c, n, w);
 #pragma unroll
@@ -490,11 +490,11 @@ norm_bwd_tile_kernel(NormBwd a, const float* stat, float* partial, int k, uint32
         float x[kV], g[kV], r[kV] = {};
         input8<T, kCkpt>(a, row, c, n, x);
         Vec<T> dy;
-        vload(dy, static_cast<const T*>(a.dy.p) + row * a.dy.pitch + c, n);
+        vload<false>(dy, static_cast<const T*>(a.dy.p) + row * a.dy.pitch + c, n);
         dy.get(g);
         if (a.dres.p) {
             Vec<T> t;
-            vload(t, static_cast<const T*>(a.dres.p) + row * a.dres.pitch + c, n);
+            vload<false>(t, static_cast<const T*>(a.dres.p) + row * a.dres.pitch + c, n);
             t.get(r);
         }
 #pragma unroll
@@ -521,13 +521,13 @@ norm_bwd_tile_kernel(NormBwd a, const float* stat, float* partial, int k, uint32
 // around.
 template <int kT> constexpr int group_threads() { return kT == 64 ? kThreads : kT; }
 
-template <bool kWhole, typename T>
+template <bool kWhole, bool kNt, typename T>
 __device__ __forceinline__ void rload(Vec<T>& v, const T* row, int c, int cols) {
     if constexpr (kWhole) {
-        if (c < cols) v.load(row + c);
+        if (c < cols) v.template load<kNt>(row + c);
         else v.zero();
     } else {
-        v.load(row + (c < cols ? min(c, cols - kV) : 0));
+        v.template load<kNt>(row + (c < cols ? min(c, cols - kV) : 0));
     }
 }
 // the same of a parameter, which other rows read too
@@ -561,7 +561,7 @@ __device__ __forceinline__ void rput(T* p, const float* f, int n) {
 
 // The parameters' loads are issued with the row's (kP16: bf16 parameters, held as they are; fp32
 // ones would take twice the registers and are read when they are used).
-template <typename T, bool kP16, int kT, int kN, bool kWhole>
+template <typename T, bool kP16, int kT, int kN, bool kWhole, bool kNt>
 __global__ void __launch_bounds__(group_threads<kT>()) norm_fwd_kernel(NormFwd a) {
     constexpr int kRows = group_threads<kT>() / kT;
     __shared__ float lds[2][kT / 64];
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(group_threads<kT>()) norm_fwd_kernel(NormFwd a
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
             const int c = (t + i * kT) * kV;
-            rload<kWhole>(x[i], xp, c, cols);
+            rload<kWhole, kNt>(x[i], xp, c, cols);
         }
         if constexpr (kP16) {
 #pragma unroll
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(group_threads<kT>()) norm_fwd_kernel(NormFwd a
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
                 const int c = (t + i * kT) * kV;
-                rload<kWhole>(r[i], rp, c, cols);
+                rload<kWhole, kNt>(r[i], rp, c, cols);
             }
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
@@ -698,6 +698,19 @@ CkptRows skip(CkptRows q, int64_t rows) {
     return q;
 }
 
+// Whether a matrix's rows start on 16-byte boundaries.
+bool aligned16(const void* p, int64_t pitch, bool bf16) {
+    return (reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(pitch * (bf16 ? 2 : 4))) % 16 == 0;
+}
+// Whether a call that moves `units` elements for each of rows x cols loads non-temporally.
+bool outgrows_cache(int64_t rows, int64_t cols, bool bf16, int units) {
+    return rows >= kNtBytes / (bf16 ? 2 : 4) / units / cols;
+}
+bool norm_fwd_nt(const NormFwd& a) {
+    return outgrows_cache(a.rows, a.cols, a.bf16, a.residual.p ? 4 : 2) && aligned16(a.x.p, a.x.pitch, a.bf16) &&
+           (!a.residual.p || aligned16(a.residual.p, a.residual.pitch, a.bf16));
+}
+
 // body(first row, rows, tiles across, log2 of a tile's vectors, workgroups) for each run of rows.
 template <typename F>
 hipError_t for_tiles(int64_t rows, int64_t cols, F&& body) {
@@ -715,18 +728,23 @@ hipError_t for_tiles(int64_t rows, int64_t cols, F&& body) {
 
 template <typename T>
 hipError_t act_forward_t(const ActFwd& a, hipStream_t stream) {
+    const bool stream_in = outgrows_cache(a.rows, a.cols, a.bf16, a.f == kNone ? 1 : 2) && aligned16(a.x.p, a.x.pitch, a.bf16);
     return for_tiles(a.rows, a.cols, [&](int64_t r, int64_t n, uint32_t across, int k, uint32_t blocks) {
         ActFwd b = a;
         b.rows = n;
         b.x = skip(a.x, r, a.bf16);
         b.y = skip(a.y, r, a.bf16);
         b.ckpt = skip(a.ckpt, r);
+        const auto go = [&](auto cached, auto nt) {
+            if (stream_in) nt<<<blocks, kThreads, 0, stream>>>(b, k, across, xcd_run(blocks));
+            else cached<<<blocks, kThreads, 0, stream>>>(b, k, across, xcd_run(blocks));
+        };
         switch (a.f) {
-            case kNone: act_fwd_kernel<T, kNone><<<blocks, kThreads, 0, stream>>>(b, k, across, xcd_run(blocks)); break;
-            case kRelu: act_fwd_kernel<T, kRelu><<<blocks, kThreads, 0, stream>>>(b, k, across, xcd_run(blocks)); break;
-            case kGelu: act_fwd_kernel<T, kGelu><<<blocks, kThreads, 0, stream>>>(b, k, across, xcd_run(blocks)); break;
-            case kGeluTanh: act_fwd_kernel<T, kGeluTanh><<<blocks, kThreads, 0, stream>>>(b, k, across, xcd_run(blocks)); break;
-            default: act_fwd_kernel<T, kSilu><<<blocks, kThreads, 0, stream>>>(b, k, across, xcd_run(blocks)); break;
+            case kNone: go(act_fwd_kernel<T, kNone, false>, act_fwd_kernel<T, kNone, true>); break;
+            case kRelu: go(act_fwd_kernel<T, kRelu, false>, act_fwd_kernel<T, kRelu, true>); break;
+            case kGelu: go(act_fwd_kernel<T, kGelu, false>, act_fwd_kernel<T, kGelu, true>); break;
+            case kGeluTanh: go(act_fwd_kernel<T, kGeluTanh, false>, act_fwd_kernel<T, kGeluTanh, true>); break;
+            default: go(act_fwd_kernel<T, kSilu, false>, act_fwd_kernel<T, kSilu, true>); break;
         }
     });
 }
@@ -783,13 +801,16 @@ template <typename T, int kT, int kN>
 void norm_fwd_run(const NormFwd& a, hipStream_t stream) {
     constexpr int kRows = group_threads<kT>() / kT;
     const uint32_t blocks = static_cast<uint32_t>((a.rows + kRows - 1) / kRows);
-    const bool whole = a.cols % kV == 0;
+    const bool whole = a.cols % kV == 0, nt = whole && norm_fwd_nt(a);
+    const auto go = [&](auto kernel) { kernel<<<blocks, group_threads<kT>(), 0, stream>>>(a); };
     if (a.param_bf16) {
-        if (whole) norm_fwd_kernel<T, true, kT, kN, true><<<blocks, group_threads<kT>(), 0, stream>>>(a);
-        else norm_fwd_kernel<T, true, kT, kN, false><<<blocks, group_threads<kT>(), 0, stream>>>(a);
+        if (nt) go(norm_fwd_kernel<T, true, kT, kN, true, true>);
+        else if (whole) go(norm_fwd_kernel<T, true, kT, kN, true, false>);
+        else go(norm_fwd_kernel<T, true, kT, kN, false, false>);
     } else {
-        if (whole) norm_fwd_kernel<T, false, kT, kN, true><<<blocks, group_threads<kT>(), 0, stream>>>(a);
-        else norm_fwd_kernel<T, false, kT, kN, false><<<blocks, group_threads<kT>(), 0, stream>>>(a);
+        if (nt) go(norm_fwd_kernel<T, false, kT, kN, true, true>);
+        else if (whole) go(norm_fwd_kernel<T, false, kT, kN, true, false>);
+        else go(norm_fwd_kernel<T, false, kT, kN, false, false>);
     }
 }
 template <typename T>
@@ -821,8 +842,11 @@ hipError_t norm_backward_t(const NormBwd& a, hipStream_t stream) {
     int64_t G = 0;
     if (a.rows > 0 && bwd_in_registers(a.cols)) {
         G = bwd_groups(a.rows, a.cols);
-        if (a.bf16) launch_norm_bwd_rows_bf16(a, partial, static_cast<uint32_t>(G), stream);
-        else launch_norm_bwd_rows_f32(a, partial, static_cast<uint32_t>(G), stream);
+        const bool nt = outgrows_cache(a.rows, a.cols, a.bf16, 3 + (a.dres.p != nullptr) + (a.y.p != nullptr)) &&
+                        aligned16(a.dy.p, a.dy.pitch, a.bf16) && aligned16(a.x.p, a.x.pitch, a.bf16);
+        const auto rows = a.bf16 ? (nt ? launch_norm_bwd_rows_bf16_nt : launch_norm_bwd_rows_bf16)
+                                 : (nt ? launch_norm_bwd_rows_f32_nt : launch_norm_bwd_rows_f32);
+        rows(a, partial, static_cast<uint32_t>(G), stream);
     } else if (a.rows > 0) {
         const Walk w = plan_walk(a.rows, a.cols);
         G = w.chunks;

@@ -34,7 +34,9 @@ typedef float f4e __attribute__((ext_vector_type(4), aligned(4)));
 template <typename T> struct Vec;
 template <> struct Vec<uint16_t> {
     u4 r;
-    __device__ void load(const uint16_t* p) { r = __builtin_nontemporal_load((const u4e*)p); }
+    template <bool kNt> __device__ void load(const uint16_t* p) {
+        r = kNt ? __builtin_nontemporal_load((const u4e*)p) : *(const u4e*)p;
+    }
     __device__ void load_part(const uint16_t* p, int n) {
         r = u4{0u, 0u, 0u, 0u};
 #pragma unroll
@@ -73,9 +75,9 @@ template <> struct Vec<uint16_t> {
 };
 template <> struct Vec<float> {
     f4 r[2];
-    __device__ void load(const float* p) {
-        r[0] = __builtin_nontemporal_load((const f4e*)p);
-        r[1] = __builtin_nontemporal_load((const f4e*)(p + 4));
+    template <bool kNt> __device__ void load(const float* p) {
+        r[0] = kNt ? __builtin_nontemporal_load((const f4e*)p) : *(const f4e*)p;
+        r[1] = kNt ? __builtin_nontemporal_load((const f4e*)(p + 4)) : *(const f4e*)(p + 4);
     }
     __device__ void load_part(const float* p, int n) {
         zero();
@@ -115,10 +117,20 @@ template <> struct Vec<float> {
     }
 };
 
+// Loads are non-temporal (kNt) where a call's operands outgrow what the 256 MB Infinity Cache can
+// keep, else cached: an activation was written just before it is read here.  kNtBytes: from that
+// many bytes read and written on.  MI355X, nt against cached, operands rotating: norm forward 84 MB
+// 17.1 / 14.6 us, with residual 403 MB 67.5 / 69.0 us; norm backward 148 MB 34.1 / 30.5 us, 201 MB
+// 40.8 / 42.3 us, 604 MB 111 / 117 us; GELU forward 105 MB 19.6 / 17.0 us, 675 MB 107 / 106 us.
+// Rows that start off a 16-byte boundary share lines between vectors and are always cached (norm
+// forward 8192 x 5003: nt 47.0, cached 38.3 us).  Codes are always cached too: a wave's vector is
+// 256 or 512 bytes of them (unpack 8192 x 5003: nt 28.0, cached 20.8 us; aligned the same).
+constexpr int64_t kNtBytes = int64_t{192} << 20;
+
 // n: columns of this vector inside the row (8 or more: whole; 0 or less: none).
-template <typename T>
+template <bool kNt, typename T>
 __device__ __forceinline__ void vload(Vec<T>& v, const T* p, int n) {
-    if (n >= kV) v.load(p);
+    if (n >= kV) v.template load<kNt>(p);
     else if (n > 0) v.load_part(p, n);
     else v.zero();
 }
@@ -250,7 +262,7 @@ __device__ __forceinline__ void decode8(u2 q, uint32_t byte, bool int8, float* v
     }
 }
 __device__ __forceinline__ u2 code_load(const uint8_t* p, int n) {
-    if (n >= kV) return __builtin_nontemporal_load((const u2e*)p);
+    if (n >= kV) return *(const u2e*)p;
     u2 q = {0u, 0u};
 #pragma unroll
     for (int j = 0; j < kV; ++j)

@@ -1,5 +1,5 @@
 // norm_backward.h -- the norms' backward pass for rows that fit in registers; compiled for each
-// activation type in norm_backward_bf16.hip and norm_backward_f32.hip.
+// activation type and load policy in norm_backward_*.hip.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -23,7 +23,9 @@ typedef uint32_t u2h __attribute__((ext_vector_type(2), aligned(2)));
 template <typename T> struct Quad;
 template <> struct Quad<uint16_t> {
     u2 r;
-    __device__ void load(const uint16_t* p) { r = __builtin_nontemporal_load((const u2h*)p); }
+    template <bool kNt> __device__ void load(const uint16_t* p) {
+        r = kNt ? __builtin_nontemporal_load((const u2h*)p) : *(const u2h*)p;
+    }
     // drops the first k elements, zeros behind the last
     __device__ void drop(int k) {
         r = __builtin_bit_cast(u2, __builtin_bit_cast(uint64_t, r) >> (16 * k));
@@ -51,7 +53,9 @@ template <> struct Quad<uint16_t> {
 };
 template <> struct Quad<float> {
     f4 r;
-    __device__ void load(const float* p) { r = __builtin_nontemporal_load((const f4e*)p); }
+    template <bool kNt> __device__ void load(const float* p) {
+        r = kNt ? __builtin_nontemporal_load((const f4e*)p) : *(const f4e*)p;
+    }
     __device__ void drop(int k) {
         if (k & 1) r = f4{r[1], r[2], r[3], 0.0f};
         if (k & 2) r = f4{r[2], r[3], 0.0f, 0.0f};
@@ -131,7 +135,7 @@ __device__ __forceinline__ T* from(T* p, uint32_t i) {
 enum { kTensor = 0, kE4m3 = 1, kInt8 = 2 };
 
 // What a row's backward pass reads, in flight.
-template <typename T, int kSrc, bool kRes, int kN>
+template <typename T, int kSrc, bool kRes, bool kNt, int kN>
 struct BwdRow {
     Quad<T> dy[kN], x[kSrc == kTensor ? kN : 1], r[kRes ? kN : 1];
     uint32_t q[kSrc == kTensor ? 1 : kN], byte[kSrc == kTensor ? 1 : kN];
@@ -152,14 +156,14 @@ struct BwdRow {
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
             const uint32_t c = at[i] & mask;   // unsigned: added to a scalar address as it is
-            dy[i].load(from(dp, c));
+            dy[i].template load<kNt>(from(dp, c));
             if constexpr (kSrc != kTensor) {
-                q[i] = *(const u1e*)from(qp, c);   // cached: 256 bytes a wave, lines shared by two (nt: 3-9% slower)
+                q[i] = *(const u1e*)from(qp, c);
                 byte[i] = *from(sp, group[i] & mask);
             } else {
-                x[i].load(from(xp, c));
+                x[i].template load<kNt>(from(xp, c));
             }
-            if constexpr (kRes) r[i].load(from(rp, c));
+            if constexpr (kRes) r[i].template load<kNt>(from(rp, c));
         }
     }
     __device__ __forceinline__ void drop(int i, int k) {
@@ -184,7 +188,7 @@ template <int kT> constexpr int bwd_threads() { return kT < 512 ? 512 : kT; }
 // the columns are a multiple of 4; else the vector that the row's end cuts is read from the row's
 // last 4 columns.  A vector outside the row reads its first columns, which a weight of 0 and no
 // stores make harmless.
-template <typename T, int kSrc, bool kRes, int kT, int kN, bool kWhole>
+template <typename T, int kSrc, bool kRes, bool kNt, int kT, int kN, bool kWhole>
 __global__ void __launch_bounds__(bwd_threads<kT>()) norm_bwd_kernel(NormBwd a, float* partial) {
     constexpr int kW = bwd_threads<kT>(), kRows = kW / kT;
     __shared__ f4 lw[kT * kN], lb[kT * kN];
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(bwd_threads<kT>()) norm_bwd_kernel(NormBwd a, 
         at[i] = static_cast<uint32_t>(c < cols ? (kWhole ? c : min(c, cols - kQ)) : 0);
         group[i] = static_cast<uint32_t>(c < cols ? c / kCkptGroup : 0);
     }
-    typedef BwdRow<T, kSrc, kRes, kN> Row;
+    typedef BwdRow<T, kSrc, kRes, kNt, kN> Row;
     Row even, odd;
     even.load(a, row, at, group);
     for (int v = threadIdx.x; v < kT * kN; v += kW) {
@@ -332,16 +336,16 @@ __global__ void __launch_bounds__(bwd_threads<kT>()) norm_bwd_kernel(NormBwd a, 
     }
 }
 
-template <typename T, int kSrc, bool kRes, int kT, int kN>
+template <typename T, int kSrc, bool kRes, bool kNt, int kT, int kN>
 void norm_bwd_run(const NormBwd& a, float* partial, uint32_t blocks, hipStream_t stream) {
-    if (a.cols % kQ == 0) norm_bwd_kernel<T, kSrc, kRes, kT, kN, true><<<blocks, bwd_threads<kT>(), 0, stream>>>(a, partial);
-    else norm_bwd_kernel<T, kSrc, kRes, kT, kN, false><<<blocks, bwd_threads<kT>(), 0, stream>>>(a, partial);
+    if (a.cols % kQ == 0) norm_bwd_kernel<T, kSrc, kRes, kNt, kT, kN, true><<<blocks, bwd_threads<kT>(), 0, stream>>>(a, partial);
+    else norm_bwd_kernel<T, kSrc, kRes, kNt, kT, kN, false><<<blocks, bwd_threads<kT>(), 0, stream>>>(a, partial);
 }
-template <typename T, int kSrc, bool kRes>
+template <typename T, int kSrc, bool kRes, bool kNt>
 void norm_bwd_shaped(const NormBwd& a, float* partial, uint32_t blocks, hipStream_t stream) {
     const BwdShape s = norm_bwd_shape(a.cols);
     switch (s.threads + s.vectors) {
-#define FSDP_SHAPE(kT, kN) case kT + kN: return norm_bwd_run<T, kSrc, kRes, kT, kN>(a, partial, blocks, stream)
+#define FSDP_SHAPE(kT, kN) case kT + kN: return norm_bwd_run<T, kSrc, kRes, kNt, kT, kN>(a, partial, blocks, stream)
         FSDP_SHAPE(64, 1);
         FSDP_SHAPE(64, 2);
         FSDP_SHAPE(64, 3);
@@ -357,16 +361,16 @@ void norm_bwd_shaped(const NormBwd& a, float* partial, uint32_t blocks, hipStrea
 #undef FSDP_SHAPE
     }
 }
-template <typename T, int kSrc>
+template <typename T, int kSrc, bool kNt>
 void norm_bwd_res(const NormBwd& a, float* partial, uint32_t blocks, hipStream_t stream) {
-    if (a.dres.p) norm_bwd_shaped<T, kSrc, true>(a, partial, blocks, stream);
-    else norm_bwd_shaped<T, kSrc, false>(a, partial, blocks, stream);
+    if (a.dres.p) norm_bwd_shaped<T, kSrc, true, kNt>(a, partial, blocks, stream);
+    else norm_bwd_shaped<T, kSrc, false, kNt>(a, partial, blocks, stream);
 }
-template <typename T>
+template <typename T, bool kNt>
 void norm_bwd_rows(const NormBwd& a, float* partial, uint32_t blocks, hipStream_t stream) {
-    if (!a.ckpt.codes) norm_bwd_res<T, kTensor>(a, partial, blocks, stream);
-    else if (a.ckpt.int8) norm_bwd_res<T, kInt8>(a, partial, blocks, stream);
-    else norm_bwd_res<T, kE4m3>(a, partial, blocks, stream);
+    if (!a.ckpt.codes) norm_bwd_res<T, kTensor, kNt>(a, partial, blocks, stream);
+    else if (a.ckpt.int8) norm_bwd_res<T, kInt8, kNt>(a, partial, blocks, stream);
+    else norm_bwd_res<T, kE4m3, kNt>(a, partial, blocks, stream);
 }
 
 }  // namespace
