@@ -478,9 +478,8 @@ FSDP_API fsdp_status fsdp_grad_sqnorm_noalloc(const fsdp_unit* unit, int32_t k, 
  * output's is at least cols when there is more than one row.  What lies in an
  * output between a row's end and the next row's start, and behind the last
  * row, stays as it was.  Arithmetic is fp32; a result is rounded once, to
- * nearest even, when it is stored.  Results do not depend on the device's load:
- * every sum has a fixed order that the sizes alone set (rows and columns; for
- * one matrix the same whatever its pitch and address).
+ * nearest even, when it is stored.  Every sum has a fixed order that the call's
+ * arguments alone set: the same call gives the same bits.
  * No operand may overlap an output.  The current device must be the one the
  * buffers and the stream belong to.
  * rows == 0 or cols == 0: nothing is read or written, except that with rows ==
