@@ -108,6 +108,12 @@ def parse_args():
                          "over 32, 64 and 128 ranks at 4.2 M to 26.2 M outputs (flat sums) and over "
                          "128 ranks in groups of 8, accumulating, at 3.5 M to 14.2 M outputs: 8 "
                          "launches each after a 1 GiB read, for rocprofv3's kernel trace")
+    ap.add_argument("--layer-ops", type=int, default=0, metavar="TOKENS",
+                    help="also time the layer operators at the unit's widths for this many tokens "
+                         "(bf16): the norm with residual and 8-bit checkpoint, its backward pass "
+                         "from the checkpoint and from the input, the MLP activation with "
+                         "checkpoint and its backward pass, pack and unpack; 10 launches each "
+                         "after a 1 GiB read")
     return ap.parse_args()
 
 
@@ -594,6 +600,69 @@ def reduce_shapes(B, stream, dev, gen, reps=8):
     return out
 
 
+def layer_widths(shapes):
+    """(d, ff) of a unit's layer: d the input width of its first matrix, ff the widest output of a
+    d-wide matrix that another matrix takes as input (the MLP's)."""
+    two = [tuple(s) for s in shapes if len(s) == 2]
+    inputs = {s[1] for s in two}
+    # a block's first matrix reads d; an embedding's rows are d wide as well
+    d = two[0][1]
+    return d, max((s[0] for s in two if s[1] == d and s[0] in inputs and s[0] != d), default=d)
+
+
+def layer_ops(shapes, tokens, stream, dev, gen, reps=10):
+    """The layer operators at a unit's widths: event medians (ms) of launches that each follow a
+    1 GiB read, and GB/s of the bytes a call cannot do without (every input read once, every
+    output written once; the column sums' partial rows are not counted)."""
+    import torch
+    import sharded_fsdp_flatten_amd as F
+    d, ff = layer_widths(shapes)
+    biased = any(tuple(s) == (ff,) for s in shapes)
+    kind, act = ("layer", "gelu_tanh") if biased else ("rms", "relu")
+    fb = torch.zeros(1 << 28, device=dev)
+    fs = torch.zeros((), device=dev)
+
+    def flush():
+        torch.sum(fb, dim=0, out=fs)
+
+    def n(*shape, std=1.0):
+        return torch.randn(*shape, device=dev, generator=gen).mul_(std).bfloat16()
+
+    x, r, dy, y, s, dx = (n(tokens, d), n(tokens, d), n(tokens, d, std=0.01), *(n(tokens, d) for _ in range(3)))
+    w, b = n(d), n(d)
+    mean, rstd = torch.empty(tokens, device=dev), torch.empty(tokens, device=dev)
+    dw, db = torch.empty(d, device=dev), torch.empty(d, device=dev)
+    ws = torch.empty(F.fsdp_norm_workspace(tokens, d), device=dev)
+    q = F.Ckpt.empty(tokens, d, "e4m3", device=dev)
+    h, g, a, dh = n(tokens, ff), n(tokens, ff, std=0.01), n(tokens, ff), n(tokens, ff)
+    dbias = torch.empty(ff, device=dev)
+    wa = torch.empty(F.fsdp_act_workspace(tokens, ff), device=dev)
+    qh = F.Ckpt.empty(tokens, ff, "e4m3", device=dev)
+    c = 1 + 1 / F.FSDP_CKPT_GROUP  # bytes of a checkpoint's element
+    rows = [
+        ("norm_forward+residual+ckpt", d, 8 + c, lambda: F.fsdp_norm_forward(
+            x, w, b, y, mean, rstd, kind=kind, residual=r, sum=s, ckpt=q)),
+        ("norm_backward from ckpt+residual+y", d, 8 + c, lambda: F.fsdp_norm_backward(
+            dy, q, w, mean, rstd, dx, dw, db, ws, kind=kind, dres=r, y=y, bias=b)),
+        ("norm_backward from input", d, 6, lambda: F.fsdp_norm_backward(
+            dy, s, w, mean, rstd, dx, dw, db, ws, kind=kind)),
+        ("act_forward+ckpt", ff, 4 + c, lambda: F.fsdp_act_forward(h, a, kind=act, ckpt=qh)),
+        ("act_backward from ckpt+y", ff, 6 + c, lambda: F.fsdp_act_backward(
+            g, qh, dh, dbias, wa, kind=act, y=a)),
+        ("ckpt_pack", ff, 2 + c, lambda: F.fsdp_ckpt_pack(h, qh)),
+        ("ckpt_unpack", ff, 2 + c, lambda: F.fsdp_ckpt_unpack(qh, a)),
+    ]
+    out = {"tokens": tokens, "d": d, "ff": ff, "norm": kind, "activation": act, "dtype": "bf16", "ops": {}}
+    for name, cols, per, call in rows:
+        call()
+        ms = _event_median(call, stream, reps, before=flush)
+        nbytes = int(per * tokens * cols)
+        out["ops"][name] = {"cols": cols, "bytes": nbytes, "event_ms_median": round(ms, 4),
+                            "GB/s": round(nbytes / (ms * 1e-3) / 1e9, 1)}
+        print("layer ops: %s done" % name, file=sys.stderr, flush=True)
+    return out
+
+
 def contention_probe(B, u, N, contrib_rows, pre, post, grad, stream, dev, reps=10):
     """The reduction on the tile kernel and on the row-major sweep, alone and overlapped with a
     stream of bf16 GEMMs on a second stream of the same priority (the backward compute that the
@@ -911,6 +980,8 @@ def main():
         result["contention"] = contention_probe(B, u, N, contrib_rows, pre, post, grad, stream, dev)
     if args.reduce_shapes:
         result["reduce_shapes"] = reduce_shapes(B, stream, dev, gen)
+    if args.layer_ops > 0:
+        result["layer_ops"] = layer_ops(unit.shapes, args.layer_ops, stream, dev, gen)
     if args.floor_probe:
         fb = torch.zeros(1 << 28, device=dev)
         fs = torch.zeros((), device=dev)

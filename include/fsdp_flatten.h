@@ -538,7 +538,7 @@ typedef struct {
 } fsdp_ckpt;
 
 typedef struct {
-    int64_t rows, cols;    /* cols < 2^31                                         */
+    int64_t rows, cols;    /* cols <= 2^30                                        */
     int32_t dtype;         /* of the activations and their gradients              */
     int32_t param_dtype;   /* norms: of weight and bias                           */
     int32_t grad_dtype;    /* backward: of dweight and dbias                      */
@@ -598,9 +598,9 @@ typedef struct {
  * Save rows x cols activations in 8 bits (see fsdp_ckpt_format).
  *   x : the activations, of `dtype`.   ckpt : host pointer, read during the call.
  * Errors: FSDP_E_ARG (NULL ckpt; with elements, a NULL buffer), FSDP_E_RANGE
- * (rows or cols negative, cols >= 2^31, dtype, format, a pitch), FSDP_E_ALIGN (x
- * not aligned to its element size), FSDP_E_OVERFLOW (a buffer's extent beyond
- * int64), FSDP_E_HIP.
+ * (rows or cols negative, cols > 2^30, dtype, format, a pitch), FSDP_E_ALIGN (x
+ * not aligned to its element size), FSDP_E_OVERFLOW (rows x cols or a buffer's
+ * extent beyond int64), FSDP_E_HIP.
  */
 FSDP_API fsdp_status fsdp_ckpt_pack(int64_t rows, int64_t cols, int32_t dtype, fsdp_rows x,
                                     const fsdp_ckpt* ckpt, void* stream);

@@ -164,7 +164,8 @@ std::vector<int64_t> param_numels(const fsdp::UnitPlan& u) {
 
 fsdp_status check_extent(int64_t rows, int64_t cols) {
     if (rows < 0) return fail(FSDP_E_RANGE, "rows must not be negative");
-    if (cols < 0 || cols > INT32_MAX) return fail(FSDP_E_RANGE, "cols must be in [0, 2^31)");
+    if (cols < 0 || cols > int64_t{1} << 30) return fail(FSDP_E_RANGE, "cols must be in [0, 2^30]");
+    if (rows > INT64_MAX / 8 / (cols + 1)) return fail(FSDP_E_OVERFLOW, "rows x cols overflows int64");
     return FSDP_OK;
 }
 

@@ -529,6 +529,27 @@ def test_act_far_values(kind):
     assert torch.isnan(y2).all() and torch.isnan(d2).all()
 
 
+def test_more_columns_than_one_column_sum_launch():
+    rows, cols = 3, (1 << 26) + 41
+    g = torch.Generator(device=dev()).manual_seed(5)
+    x = torch.randint(-3, 4, (rows, cols), device=dev(), generator=g, dtype=torch.int8).to(torch.bfloat16)
+    q = F.Ckpt.empty(rows, cols, "int8", device=dev())
+    y, back = torch.empty_like(x), torch.empty_like(x)
+    F.fsdp_act_forward(x, y, kind="relu", ckpt=q)
+    F.fsdp_ckpt_unpack(q, back)
+    assert torch.equal(back, x) and torch.equal(y, x.clamp(min=0))
+    db = torch.full((cols + 64,), 7.0, device=dev())
+    ws = torch.empty(F.fsdp_act_workspace(rows, cols), device=dev())
+    F.fsdp_act_backward(x, q, y, db[:cols], ws, kind="relu")
+    assert torch.equal(db[:cols], (x * (x > 0)).float().sum(0)) and bool((db[cols:] == 7).all())
+    w = torch.ones(cols, dtype=torch.bfloat16, device=dev())
+    mean, rstd = torch.zeros(rows, device=dev()), torch.ones(rows, device=dev())
+    dw = torch.empty(cols, device=dev())
+    ws = torch.empty(F.fsdp_norm_workspace(rows, cols), device=dev())
+    F.fsdp_norm_backward(x, q, w, mean, rstd, y, dw, db[:cols], ws, kind="layer")
+    assert torch.equal(dw, x.float().square().sum(0)) and torch.equal(db[:cols], x.float().sum(0))
+
+
 # ---------------------------------------------------------------------------
 # how they are called
 # ---------------------------------------------------------------------------

@@ -71,7 +71,8 @@ def test_structures_match_their_packed_form():
         assert packed.size == ctypes.sizeof(s)
 
 
-BAD_CFG = [(dict(rows=-1), RANGE), (dict(cols=-1), RANGE), (dict(cols=1 << 31), RANGE), (dict(dtype=0), RANGE),
+BAD_CFG = [(dict(rows=-1), RANGE), (dict(cols=-1), RANGE), (dict(cols=(1 << 30) + 1), RANGE), (dict(rows=(1 << 63) - 1), OVERFLOW),
+           (dict(rows=1 << 40, cols=1 << 30), OVERFLOW), (dict(dtype=0), RANGE),
            (dict(dtype=3), RANGE), (dict(kind=0), RANGE), (dict(kind=9), RANGE)]
 BAD_ROWS = [(dict(p=0), ARG), (dict(p=P + 1), ALIGN), (dict(pitch=-1), RANGE), (dict(pitch=1 << 61), OVERFLOW)]
 
@@ -171,7 +172,9 @@ def test_workspaces(lib):
         assert size(0, 100, ctypes.byref(n)) == OK and n.value == 0
         assert size(10, 0, ctypes.byref(n)) == OK and n.value == 0
         assert size(-1, 100, ctypes.byref(n)) == RANGE
-        assert size(10, 1 << 31, ctypes.byref(n)) == RANGE
+        assert size(10, (1 << 30) + 1, ctypes.byref(n)) == RANGE
+        assert size((1 << 63) - 1, 1, ctypes.byref(n)) == OVERFLOW
+        assert size(1 << 58, 1, ctypes.byref(n)) == OK and n.value > 0
         assert size(10, 100, None) == ARG
         # a quarter byte an element at most where there are many, so no more than an eighth of a bf16 matrix
         for r, c in ((1 << 30, 1024), (1 << 20, 512), (8192, 12288), (2048, 65536), (4096, 100000)):
