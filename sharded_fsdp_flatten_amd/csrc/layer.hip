@@ -1,11 +1,13 @@
 // layer.hip -- HIP kernels of the layer operators for CDNA4 (gfx950): 8-bit activation
 // checkpoints, LayerNorm / RMSNorm and the MLP activation, forward and backward.
 //
-// All of them stream their operands once; what bounds them is HBM.  Every lane owns vectors of
-// 8 neighbouring columns (one 16-byte load of bf16, two of fp32, 8 bytes of codes), four lanes
-// of a quad one group of 32 columns with one scale.  Rows may start at any element: global
+// All of them read their operands once and write their results once (the norms of rows beyond
+// 16384 columns read a row again for each pass over it); what bounds them is HBM.  Every lane owns
+// vectors of 8 neighbouring columns (one 16-byte load of bf16, two of fp32, 8 bytes of codes), four
+// lanes of a quad one group of 32 columns with one scale.  Rows may start at any element: global
 // loads and stores of several dwords work at any address, so odd pitches and widths take the
-// same path, and only the vector that the row's end cuts goes element by element.
+// same path, and the vector that the row's end cuts is read from the row's last whole vector or
+// element by element.  The norms' backward pass over rows in registers is in norm_backward.h.
 // Sums, statistics and the arithmetic between load and store are binary32; a result is rounded
 // once, when it is stored.
 #include <hip/hip_runtime.h>
@@ -104,6 +106,8 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t b, uint32_t blocks, uint3
     const uint32_t r = b % span;
     return b - r + (r & 7u) * run + (r >> 3);
 }
+// Pack 8192 x 12288 one row a lane: as dealt 58.2 us, runs of 16 / 64 / 256 tiles 53.6 / 53.4 /
+// 55.5; unpack 54.7 as dealt, 52.9 with 64.  Below 4096 tiles a run is too large a part of the launch.
 uint32_t xcd_run(uint32_t blocks) { return blocks >= 4096u ? 64u : 0u; }
 
 // Rows of a lane where only a checkpoint is written or read: four from kLongTiles tiles on, all
@@ -132,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActFwd a, int k, uint
         if (r >= a.rows) return;  // whole quads leave together (k >= 2)
         float v[kV];
         x[u].get(v);
-        if (a.ckpt.codes) pack8(a.ckpt, r, c, n, v);
+        if (a.ckpt.codes) pack8<kF == kNone>(a.ckpt, r, c, n, v);
         if constexpr (kF != kNone) {
             float y[kV], d;
 #pragma unroll
@@ -328,6 +332,13 @@ struct ActRow {
 // each, all of whose loads are in flight at once, and ends: its lanes' sums add up in LDS to one
 // partial row.  The vector that the row's end cuts is read from the row's last 8 columns (kNarrow:
 // there are none); rows past the last read it once more, so that no branch stands between loads.
+// Workgroups that walk down their columns with the sums in registers write fewer partial rows and are
+// slower all the same: a load behind a store waits for the store, and the whole grid reads and writes
+// in step (no sums, 2048 x 65536 from e4m3: one row a lane 146 us, walking 177).  16 waves of one row
+// each, 512 columns wide, against 16 of two and 8 of four rows: ReLU 2048 x 65536 162 / 167 / 171 us,
+// GELU 8192 x 12288 131 / 126 / 129, 4096 x 5120 33.5 / 33.1 / 33.7, 128 x 5120 7.5 / 9.0 / 9.3;
+// 1024 columns wide 165, 138, 35.0 and 7.6.  GELU's and SiLU's own arithmetic takes as long as the
+// memory at these rates: 33 vector instructions an element, two of them at a quarter of the rate.
 constexpr int kActThreads = 1024, kActRows = 1;
 constexpr int kActWidest = 6;   // log2 of a block's vectors across, at most
 template <typename T, int kF, bool kCkpt, bool kNarrow>
@@ -445,7 +456,7 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_long_kernel(NormFwd a) {
         float v[kV], w[kV], b[kV] = {};
         const int n = static_cast<int>(min(a.cols - c, int64_t{kV}));
         get(c, n, v, true);
-        if (a.ckpt.codes) pack8(a.ckpt, row, c, n, v);
+        if (a.ckpt.codes) pack8<false>(a.ckpt, row, c, n, v);
         param8(a.weight, a.param_bf16, c, n, w);
         if (a.bias) param8(a.bias, a.param_bf16, c, n, b);
 #pragma unroll
@@ -686,7 +697,7 @@ __global__ void __launch_bounds__(group_threads<kT>()) norm_fwd_kernel(NormFwd a
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
             const int c = (t + i * kT) * kV;
-            pack8(a.ckpt, row, c, cols - c, v[i]);
+            pack8<false>(a.ckpt, row, c, cols - c, v[i]);
         }
     }
     T* yp = static_cast<T*>(a.y.p) + row * a.y.pitch;
@@ -814,7 +825,10 @@ void act_backward_t(const ActBwd& a, const Tiles& w, hipStream_t stream) {
 // for each pass.
 constexpr int64_t kMaxRowCols = 16384;
 
-// Threads of a row and vectors of a thread for the kernels that hold a row in registers.
+// Threads of a row and vectors of a thread for the forward pass over rows in registers: a wave up to
+// 2048 columns (no barrier; 16384 x 1280 18.4 us, as a workgroup's row 21.7), then 256 threads, which
+// up to six vectors each hold 12288 columns in 193 registers (4096 x 12288 with residual: 67.0 us; 512
+// threads of three 70.4), then 512.
 struct RowShape {
     int threads, vectors;
 };
@@ -826,7 +840,11 @@ RowShape fwd_shape(int64_t cols) {
 }
 // Whether the backward pass holds a row of these columns in registers.
 bool bwd_in_registers(int64_t cols) { return cols >= 4 && cols <= kMaxRowCols; }
-// Workgroups of the backward pass over rows in registers: each writes a partial row.
+// Workgroups of the backward pass over rows in registers: each writes a partial row, so there are no
+// more than the device holds at once (two of 8 waves a CU, or one of 16), four rows a group where that
+// leaves 64, and below that a row each, for latency.  777 x 5003: 195 workgroups 16.0 us, 389 19.6,
+// 512 23.4; 128 x 1280: 32 workgroups 7.4 us, 8 10.7; 16384 x 1280 from e4m3: 512 35.4 us, 256 37.6,
+// 768 (not all resident) 48.2.
 int64_t bwd_groups(int64_t rows, int64_t cols) {
     const BwdShape s = norm_bwd_shape(cols);
     const int64_t high = std::max(1, 512 / s.threads);
@@ -911,6 +929,10 @@ hipError_t norm_backward_t(const NormBwd& a, hipStream_t stream) {
 
 }  // namespace
 
+// The fewest threads whose three vectors of 4 hold the row (four, beyond 1024 threads): two of a wave's
+// own rows or a few waves' share a workgroup, and its registers allow two of 8 waves a CU.  Rows of
+// 1024 and 1280 columns as one wave's, four and five vectors: 53.1 and 42.0 us where two waves' take
+// 49.6 and 35.4 (32768 x 1024 from int8, 16384 x 1280 from e4m3).
 BwdShape norm_bwd_shape(int64_t cols) {
     const int64_t nq = (cols + 3) / 4;
     if (nq <= 64) return {64, 1};
