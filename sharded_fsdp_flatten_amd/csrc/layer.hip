@@ -339,6 +339,9 @@ struct ActRow {
 // GELU 8192 x 12288 131 / 126 / 129, 4096 x 5120 33.5 / 33.1 / 33.7, 128 x 5120 7.5 / 9.0 / 9.3;
 // 1024 columns wide 165, 138, 35.0 and 7.6.  GELU's and SiLU's own arithmetic takes as long as the
 // memory at these rates: 33 vector instructions an element, two of them at a quarter of the rate.
+// The blocks go to the XCDs as dealt: a line of scale bytes serves eight neighbouring blocks, and each
+// XCD reads it (7% more bytes), but runs of 8 to 64 blocks an XCD are slower (ReLU 2048 x 65536: 162.7
+// against 168-171 us, GELU 8192 x 12288: 134 against 134-137).
 constexpr int kActThreads = 1024, kActRows = 1;
 constexpr int kActWidest = 6;   // log2 of a block's vectors across, at most
 template <typename T, int kF, bool kCkpt, bool kNarrow>
@@ -774,7 +777,8 @@ hipError_t for_tiles(int64_t rows, int64_t cols, bool long_rows, F&& body) {
 
 template <typename T>
 hipError_t act_forward_t(const ActFwd& a, hipStream_t stream) {
-    const bool stream_in = outgrows_cache(a.rows, a.cols, a.bf16, a.f == kNone ? 1 : 2) && aligned16(a.x.p, a.x.pitch, a.bf16);
+    constexpr bool kNt = sizeof(T) == 2;
+    const bool stream_in = kNt && outgrows_cache(a.rows, a.cols, a.bf16, a.f == kNone ? 1 : 2) && aligned16(a.x.p, a.x.pitch, a.bf16);
     return for_tiles(a.rows, a.cols, a.f == kNone, [&](int64_t r, int64_t n, uint32_t across, int k, uint32_t blocks, bool four) {
         ActFwd b = a;
         b.rows = n;
@@ -787,13 +791,13 @@ hipError_t act_forward_t(const ActFwd& a, hipStream_t stream) {
         };
         switch (a.f) {
             case kNone:
-                if (four) go(act_fwd_kernel<T, kNone, false, kLongRows>, act_fwd_kernel<T, kNone, true, kLongRows>);
-                else go(act_fwd_kernel<T, kNone, false, 1>, act_fwd_kernel<T, kNone, true, 1>);
+                if (four) go(act_fwd_kernel<T, kNone, false, kLongRows>, act_fwd_kernel<T, kNone, kNt, kLongRows>);
+                else go(act_fwd_kernel<T, kNone, false, 1>, act_fwd_kernel<T, kNone, kNt, 1>);
                 break;
-            case kRelu: go(act_fwd_kernel<T, kRelu, false, 1>, act_fwd_kernel<T, kRelu, true, 1>); break;
-            case kGelu: go(act_fwd_kernel<T, kGelu, false, 1>, act_fwd_kernel<T, kGelu, true, 1>); break;
-            case kGeluTanh: go(act_fwd_kernel<T, kGeluTanh, false, 1>, act_fwd_kernel<T, kGeluTanh, true, 1>); break;
-            default: go(act_fwd_kernel<T, kSilu, false, 1>, act_fwd_kernel<T, kSilu, true, 1>); break;
+            case kRelu: go(act_fwd_kernel<T, kRelu, false, 1>, act_fwd_kernel<T, kRelu, kNt, 1>); break;
+            case kGelu: go(act_fwd_kernel<T, kGelu, false, 1>, act_fwd_kernel<T, kGelu, kNt, 1>); break;
+            case kGeluTanh: go(act_fwd_kernel<T, kGeluTanh, false, 1>, act_fwd_kernel<T, kGeluTanh, kNt, 1>); break;
+            default: go(act_fwd_kernel<T, kSilu, false, 1>, act_fwd_kernel<T, kSilu, kNt, 1>); break;
         }
     });
 }
@@ -857,14 +861,15 @@ template <typename T, int kT, int kN>
 void norm_fwd_run(const NormFwd& a, hipStream_t stream) {
     constexpr int kRows = group_threads<kT>() / kT;
     const uint32_t blocks = static_cast<uint32_t>((a.rows + kRows - 1) / kRows);
-    const bool whole = a.cols % kV == 0, nt = whole && norm_fwd_nt(a);
+    constexpr bool kNt = sizeof(T) == 2;   // fp32 vectors are loaded through the cache in any case
+    const bool whole = a.cols % kV == 0, nt = kNt && whole && norm_fwd_nt(a);
     const auto go = [&](auto kernel) { kernel<<<blocks, group_threads<kT>(), 0, stream>>>(a); };
     if (a.param_bf16) {
-        if (nt) go(norm_fwd_kernel<T, true, kT, kN, true, true>);
+        if (nt) go(norm_fwd_kernel<T, true, kT, kN, true, kNt>);
         else if (whole) go(norm_fwd_kernel<T, true, kT, kN, true, false>);
         else go(norm_fwd_kernel<T, true, kT, kN, false, false>);
     } else {
-        if (nt) go(norm_fwd_kernel<T, false, kT, kN, true, true>);
+        if (nt) go(norm_fwd_kernel<T, false, kT, kN, true, kNt>);
         else if (whole) go(norm_fwd_kernel<T, false, kT, kN, true, false>);
         else go(norm_fwd_kernel<T, false, kT, kN, false, false>);
     }
