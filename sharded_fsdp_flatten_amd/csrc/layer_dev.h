@@ -242,26 +242,31 @@ __device__ __forceinline__ u2 encode8(const float* v, bool int8, uint32_t* byte)
     }
     return q;
 }
-__device__ __forceinline__ void decode8(u2 q, uint32_t byte, bool int8, float* v) {
-    const float s = scale_value(byte);
-    if (int8) {
+// Four values of a word of codes.  gfx950's scaled conversion takes e4m3 codes and the scale's
+// exponent field, which the byte is (255: NaN; e4m3 never has the byte 0).
+template <bool kInt8>
+__device__ __forceinline__ void decode4(uint32_t q, uint32_t byte, float* v) {
+    if constexpr (kInt8) {
+        const float s = scale_value(byte);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t u = q[h] ^ 0x80808080u;   // offset by 128
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[4 * h + j] = (static_cast<float>((u >> (8 * j)) & 0xFFu) - 128.0f) * s;
-        }
+        for (int j = 0; j < 4; ++j) v[j] = static_cast<float>(static_cast<int8_t>(q >> (8 * j))) * s;
     } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q[h]), false);
-            const f2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q[h]), true);
-            v[4 * h] = a[0] * s;
-            v[4 * h + 1] = a[1] * s;
-            v[4 * h + 2] = b[0] * s;
-            v[4 * h + 3] = b[1] * s;
-        }
+        const float s = __builtin_bit_cast(float, byte << 23);
+        const f2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q, s, false);
+        const f2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q, s, true);
+        v[0] = a[0];
+        v[1] = a[1];
+        v[2] = b[0];
+        v[3] = b[1];
+    }
+}
+__device__ __forceinline__ void decode8(u2 q, uint32_t byte, bool int8, float* v) {
+    if (int8) {
+        decode4<true>(q[0], byte, v);
+        decode4<true>(q[1], byte, v + 4);
+    } else {
+        decode4<false>(q[0], byte, v);
+        decode4<false>(q[1], byte, v + 4);
     }
 }
 __device__ __forceinline__ u2 code_load(const uint8_t* p, int n) {

@@ -94,22 +94,6 @@ __device__ __forceinline__ f4 param4(const void* w, bool bf16, int64_t c, int n)
     }
     return v;
 }
-template <bool kInt8>
-__device__ __forceinline__ void decode4(uint32_t q, uint32_t byte, float* v) {
-    const float s = scale_value(byte);
-    if constexpr (kInt8) {
-#pragma unroll
-        for (int j = 0; j < kQ; ++j) v[j] = static_cast<float>(static_cast<int8_t>(q >> (8 * j))) * s;
-    } else {
-        const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q), false);
-        const f2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q), true);
-        v[0] = a[0] * s;
-        v[1] = a[1] * s;
-        v[2] = b[0] * s;
-        v[3] = b[1] * s;
-    }
-}
-
 // Partial sums, which the next kernel reads.
 __device__ __forceinline__ void keep(float* p, const float* v, int n) {
     if (n >= kQ) {
