@@ -54,15 +54,29 @@ __device__ __forceinline__ void activate(float h, float* y, float* d) {
         *y = h * s;
         *d = s + *y * (1.0f - s) * (2.0f * a + 6.0f * a * c * h2);
     } else {
-        // Phi(h) by Hastings' rational form of erfc (Abramowitz and Stegun 7.1.26, absolute error
-        // 1.5e-7): erfc(z) = t (a1 + t (a2 + ...)) e^-z^2, t = 1 / (1 + p z), z = |h| / sqrt 2;
-        // the exponential is also the density's, which f' needs.
-        const float z = __builtin_fabsf(h) * 0.70710678118654752f;
-        const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * z);
-        const float e = fast_exp(-z * z);
-        const float poly = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
-        const float q = 0.5f * poly * e;                 // Phi(-|h|)
-        const float phi = h < 0.0f ? q : 1.0f - q;
+        // Q = Phi(-|h|) = e^(-h^2/2) R(|h|).  R, the scaled complementary error function's half, is analytic
+        // in q = a / (a + 3), which takes a >= 0 to [0, 1): a polynomial of degree 9 in q, the minimax of the
+        // relative error on [0, 14.6] (1.0e-8 with these coefficients, fitted to erfcx in binary64), with R(0)
+        // = 1/2 held exactly, so that near 0 the reciprocal's error reaches Q only times q.  Q is within
+        // 1e-7 and within (6 + 4|h| + h^2) 2^-24 of itself; a form of a bounded absolute error alone loses the
+        // negative tail, where y is h Q.  The clamp (part of the product's instruction) turns an infinite h's
+        // q into a number; the exponential is 0 there.  bf16 4096 x 5120 with checkpoint forward 23.6 us and
+        // from it backward 36.2 (22.1 and 34.9 with five coefficients and Phi off by 4e-7), fp32 36.2 and 57.4.
+        const float a = __builtin_fabsf(h);
+        const float q = __builtin_amdgcn_fmed3f(a * __builtin_amdgcn_rcpf(a + 3.0f), 0.0f, 1.0f);
+        const float e = __builtin_amdgcn_exp2f(h * h * (-0.5f * 1.44269504088896341f));
+        float r = 2.719713748e-02f;
+        r = r * q - 9.296188504e-02f;
+        r = r * q + 8.368366957e-02f;
+        r = r * q + 9.343822487e-03f;
+        r = r * q + 6.212504953e-02f;
+        r = r * q - 1.587376297e-01f;
+        r = r * q - 2.869739830e-01f;
+        r = r * q + 1.053155661e+00f;
+        r = r * q - 1.196826577e+00f;
+        r = r * q + 0.5f;
+        const float tail = r * e;
+        const float phi = h < 0.0f ? tail : 1.0f - tail;
         *y = h * phi;
         *d = phi + h * e * 0.39894228040143268f;
     }
