@@ -34,6 +34,9 @@ enum { kNone = 0, kRelu = 1, kGelu = 2, kGeluTanh = 3, kSilu = 4 };
 __device__ __forceinline__ float fast_exp(float x) {
     return __builtin_amdgcn_exp2f(x * 1.44269504088896341f);
 }
+// 1 - s of s = 1 / (1 + e) as e s, whose error is relative: f' multiplies it by h, and the GELU's by up to
+// 6 more.  The clamp (part of the product's instruction) makes inf x 0 a 0, where s is 0 too.
+__device__ __forceinline__ float rest(float e, float s) { return __builtin_amdgcn_fmed3f(e * s, 0.0f, 1.0f); }
 // f(h) and f'(h).
 template <int kF>
 __device__ __forceinline__ void activate(float h, float* y, float* d) {
@@ -41,18 +44,18 @@ __device__ __forceinline__ void activate(float h, float* y, float* d) {
         *y = h <= 0.0f ? 0.0f : h;                       // NaN stays NaN
         *d = h > 0.0f ? 1.0f : (h <= 0.0f ? 0.0f : h);
     } else if constexpr (kF == kSilu) {
-        const float s = __builtin_amdgcn_rcpf(1.0f + fast_exp(-h));
+        const float e = fast_exp(-h), s = __builtin_amdgcn_rcpf(1.0f + e);
         *y = h * s;
-        *d = s * (1.0f + h * (1.0f - s));
+        *d = s * (1.0f + h * rest(e, s));
     } else if constexpr (kF == kGeluTanh) {
         // (1 + tanh u) / 2 = 1 / (1 + e^-2u), u = sqrt(2/pi) (h + 0.044715 h^3).
         // h^2 is capped where the logistic function is flat, so that no product overflows to 0 x inf;
         // a NaN comes through h
         constexpr float a = 0.79788456080286536f, c = 0.044715f, l = -2.0f * a * 1.44269504088896341f;
         const float h2 = __builtin_fminf(h * h, 1000.0f);
-        const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(h * (l + l * c * h2)));
+        const float e = __builtin_amdgcn_exp2f(h * (l + l * c * h2)), s = __builtin_amdgcn_rcpf(1.0f + e);
         *y = h * s;
-        *d = s + *y * (1.0f - s) * (2.0f * a + 6.0f * a * c * h2);
+        *d = s + *y * rest(e, s) * (2.0f * a + 6.0f * a * c * h2);
     } else {
         // Q = Phi(-|h|) = e^(-h^2/2) R(|h|).  R, the scaled complementary error function's half, is analytic
         // in q = a / (a + 3), which takes a >= 0 to [0, 1): a polynomial of degree 9 in q, the minimax of the

@@ -77,3 +77,35 @@ def test_gelu_of_infinities_and_nan():
     y, d = y[0].tolist(), d[0].tolist()
     assert y[0] == float("inf") and np.isnan(y[1]) and np.isnan(y[2])
     assert y[3:] == [h[0, 3].item(), 0, h[0, 5].item(), 0, 17, 0] and d[3:] == [1, 0, 1, 0, 1, 0]
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["gelu_tanh", "silu"])
+def test_logistic_activations(kind, t):
+    """s = 1 / (1 + E), w = 1 - s = E s.  E = e^-z has the relative error rz U |z| of its argument (SiLU: the
+    product with log2(e) and that constant, 2; GELU: two constants, h^2, a multiply-add and a product, 4) and
+    2 U of the exponential; 1 + E, its reciprocal and a product add 4 U.  f' is s (1 + h w), or
+    s + h s w p with p = 2a + 6ac h^2.  Where s is below the smallest normal number it may be 0."""
+    x = arguments(t, 13.0)
+    y, d = both(kind, x)
+    h = x.double().cpu().numpy()
+    a, c = np.sqrt(2 / np.pi), 0.044715
+    z, rz = (h, 2) if kind == "silu" else (2 * a * (h + c * h ** 3), 4)
+    with np.errstate(over="ignore"):
+        s, w = 1 / (1 + np.exp(-z)), 1 / (1 + np.exp(z))
+    U = R.U
+    re = (rz * np.abs(z) + 2) * U
+    es, ew = s * (w * re + 3 * U), w * (s * re + 4 * U)
+    want = h * s
+    ey = np.abs(h) * es + U * np.abs(want)
+    if kind == "silu":
+        k = 1 + h * w
+        slope = s * k
+        ed = np.abs(k) * es + s * (np.abs(h) * (ew + U * w) + U * np.abs(k)) + U * np.abs(slope)
+    else:
+        p = 2 * a + 6 * a * c * h * h
+        slope = s + want * w * p
+        ed = es + p * (w * ey + np.abs(want) * (ew + 5 * U * w)) + U * np.abs(slope)
+    half = R.HALF[t] if t == "bf16" else 0
+    inside(y, want, ey + (np.abs(want) + ey) * half + 1000 * TINY, h, "y")
+    inside(d, slope, ed + (np.abs(slope) + ed) * half + 1000 * TINY, h, "f'")
