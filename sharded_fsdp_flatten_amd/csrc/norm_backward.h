@@ -176,8 +176,8 @@ template <int kT> constexpr int bwd_threads() { return kT < 512 ? 512 : kT; }
 // against 48.7), nor do other orders of the rows over the XCDs (within 1%).  Weight and bias lie in LDS: read as
 // memory, they would make a row wait for the next one's loads, which return in order.  kWhole:
 // the columns are a multiple of 4; else the vector that the row's end cuts is read from the row's
-// last 4 columns.  A vector outside the row reads its first columns, which a weight of 0 and no
-// stores make harmless.
+// last 4 columns.  A vector outside the row reads its first columns, and is left out of the row's sums
+// and not stored.
 template <typename T, int kSrc, bool kRes, bool kNt, int kT, int kN, bool kWhole>
 __global__ void __launch_bounds__(bwd_threads<kT>()) norm_bwd_kernel(NormBwd a, float* partial) {
     constexpr int kW = bwd_threads<kT>(), kRows = kW / kT;
@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(bwd_threads<kT>()) norm_bwd_kernel(NormBwd a, 
                 now.input(i, xh[i]);
                 now.dy[i].get(g);
                 const f4 w = lw[t + i * kT];
+                const float t0 = s0, t1 = s1;
 #pragma unroll
                 for (int j = 0; j < kQ; ++j) {
                     xh[i][j] = (xh[i][j] - mean) * rstd;
@@ -232,6 +233,11 @@ __global__ void __launch_bounds__(bwd_threads<kT>()) norm_bwd_kernel(NormBwd a, 
                     gw[i][j] = g[j] * w[j];
                     s0 += gw[i][j];
                     s1 += gw[i][j] * xh[i][j];
+                }
+                // only a thread's last vector can lie outside; an infinity that it read would make its 0s NaN
+                if (i + 1 == kN) {
+                    s0 = c < cols ? s0 : t0;
+                    s1 = c < cols ? s1 : t1;
                 }
             }
         } else {
