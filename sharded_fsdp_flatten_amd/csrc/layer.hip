@@ -862,16 +862,16 @@ RowShape fwd_shape(int64_t cols) {
 // Whether the backward pass holds a row of these columns in registers.
 bool bwd_in_registers(int64_t cols) { return cols >= 4 && cols <= kMaxRowCols; }
 // Workgroups of the backward pass over rows in registers: each writes a partial row, so there are no
-// more than the device holds at once (two of 8 waves a CU, or one of 16), four rows a group where that
+// more than the device holds at once (256 CUs with `resident` each), four rows a group where that
 // leaves 64, and below that a row each, for latency.  777 x 5003: 195 workgroups 16.0 us, 389 19.6,
-// 512 23.4; 128 x 1280: 32 workgroups 7.4 us, 8 10.7; 16384 x 1280 from e4m3: 512 35.4 us, 256 37.6,
-// 768 (not all resident) 48.2.
-int64_t bwd_groups(int64_t rows, int64_t cols) {
-    const BwdShape s = norm_bwd_shape(cols);
-    const int64_t high = std::max(1, 512 / s.threads);
-    const int64_t most = s.threads == 1024 ? 256 : 512;
+// 512 23.4; 128 x 1280: 32 workgroups 7.4 us, 8 10.7.  Two resident, 512 workgroups against 256: 32768 x 1024
+// from int8 45.0 / 50.2 us, 16384 x 1280 from e4m3 29.7 / 28.6.  One resident (a residual gradient in each), 256
+// against 512, and against 512 held to 128 registers: fp32 16384 x 704 37.8 / 40.2 / 52.8 us, 16384 x 1280
+// 60.8 / 63.6 / 63.6, 4096 x 5120 63.3 / 68.3 / 74.8; bf16 from int8 8192 x 5003 101 / 109 / 115.
+int64_t bwd_groups(int64_t rows, int64_t cols, int resident) {
+    const int64_t high = std::max(1, 512 / norm_bwd_shape(cols).threads);
     const int64_t each = (rows + high - 1) / high;
-    return std::min(most, std::max(std::min<int64_t>(each, 64), (each + 3) / 4));
+    return std::min<int64_t>(256 * resident, std::max(std::min<int64_t>(each, 64), (each + 3) / 4));
 }
 
 template <typename T, int kT, int kN>
@@ -919,7 +919,8 @@ hipError_t norm_backward_t(const NormBwd& a, hipStream_t stream) {
     float* partial = a.workspace;
     int64_t G = 0;
     if (a.rows > 0 && bwd_in_registers(a.cols)) {
-        G = bwd_groups(a.rows, a.cols);
+        const BwdShape shape = norm_bwd_shape(a.cols);
+        G = bwd_groups(a.rows, a.cols, norm_bwd_resident(a.bf16, kCkpt, a.dres.p, shape.threads, shape.vectors));
         const bool nt = outgrows_cache(a.rows, a.cols, a.bf16, 3 + (a.dres.p != nullptr) + (a.y.p != nullptr)) &&
                         aligned16(a.dy.p, a.dy.pitch, a.bf16) && aligned16(a.x.p, a.x.pitch, a.bf16);
         const auto rows = a.bf16 ? (nt ? launch_norm_bwd_rows_bf16_nt : launch_norm_bwd_rows_bf16)
@@ -965,7 +966,11 @@ BwdShape norm_bwd_shape(int64_t cols) {
 
 int64_t norm_workspace_floats(int64_t rows, int64_t cols) {
     if (rows == 0 || cols == 0) return 0;
-    if (bwd_in_registers(cols)) return 2 * bwd_groups(rows, cols) * cols;
+    if (bwd_in_registers(cols)) {
+        // the most that any type and source takes
+        const BwdShape shape = norm_bwd_shape(cols);
+        return 2 * bwd_groups(rows, cols, norm_bwd_resident(true, false, false, shape.threads, shape.vectors)) * cols;
+    }
     int64_t n, r;
     if (__builtin_mul_overflow(2 * plan_walk(rows, cols).chunks, cols, &n)) return -1;
     if (__builtin_mul_overflow(rows, int64_t{2}, &r) || __builtin_add_overflow(r, 3, &r) ||

@@ -164,6 +164,11 @@ struct BwdRow {
 
 // A workgroup is 8 waves, or the 16 of a row that takes as many.
 template <int kT> constexpr int bwd_threads() { return kT < 512 ? 512 : kT; }
+// Waves a SIMD (four of them a CU) of the workgroups that the launch counts on being resident.
+template <typename T, int kSrc, bool kRes, int kT, int kN>
+constexpr int bwd_waves() {
+    return norm_bwd_resident(sizeof(T) == 2, kSrc != kTensor, kRes, kT, kN) * bwd_threads<kT>() / 256;
+}
 
 // Row groups of kT threads, kN vectors a thread, take rows g, g + groups, ... with the next row's
 // loads in flight, and keep the column sums of all their rows in registers; a workgroup adds up
@@ -179,7 +184,7 @@ template <int kT> constexpr int bwd_threads() { return kT < 512 ? 512 : kT; }
 // last 4 columns.  A vector outside the row reads its first columns, and is left out of the row's sums
 // and not stored.
 template <typename T, int kSrc, bool kRes, bool kNt, int kT, int kN, bool kWhole>
-__global__ void __launch_bounds__(bwd_threads<kT>()) norm_bwd_kernel(NormBwd a, float* partial) {
+__global__ void __launch_bounds__(bwd_threads<kT>(), (bwd_waves<T, kSrc, kRes, kT, kN>())) norm_bwd_kernel(NormBwd a, float* partial) {
     constexpr int kW = bwd_threads<kT>(), kRows = kW / kT;
     __shared__ f4 lw[kT * kN], lb[kT * kN];
     __shared__ float lds[2][2 * (kW / 64)];
