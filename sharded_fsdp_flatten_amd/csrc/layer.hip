@@ -313,18 +313,18 @@ hipError_t launch_col_sum(const float* partial, int64_t G, int64_t pitch, int64_
 }
 
 // What a lane reads of one row for the activation's backward pass.
-template <typename T, bool kCkpt>
+template <typename T, bool kCkpt, bool kNt>
 struct ActRow {
     Vec<T> dy, x;
     u2 q;
     uint32_t byte;
     __device__ __forceinline__ void load(const ActBwd& a, int64_t row, int64_t c, int64_t group) {
-        dy.template load<true>(static_cast<const T*>(a.dy.p) + row * a.dy.pitch + c);
+        dy.template load<kNt>(static_cast<const T*>(a.dy.p) + row * a.dy.pitch + c);
         if constexpr (kCkpt) {
             q = *(const u2e*)(a.ckpt.codes + row * a.ckpt.code_pitch + c);
             byte = a.ckpt.scales[row * a.ckpt.scale_pitch + group];
         } else {
-            x.template load<true>(static_cast<const T*>(a.x.p) + row * a.x.pitch + c);
+            x.template load<kNt>(static_cast<const T*>(a.x.p) + row * a.x.pitch + c);
         }
     }
     // row of fewer than 8 columns
@@ -361,7 +361,7 @@ struct ActRow {
 // against 168-171 us, GELU 8192 x 12288: 134 against 134-137).
 constexpr int kActThreads = 1024, kActRows = 1;
 constexpr int kActWidest = 6;   // log2 of a block's vectors across, at most
-template <typename T, int kF, bool kCkpt, bool kNarrow>
+template <typename T, int kF, bool kCkpt, bool kNarrow, bool kNt>
 __global__ void __launch_bounds__(kActThreads)
 act_bwd_kernel(ActBwd a, int k, uint32_t across) {
     __shared__ float lds[kV * kActThreads];
@@ -372,7 +372,7 @@ act_bwd_kernel(ActBwd a, int k, uint32_t across) {
     const int skip = n > 0 ? static_cast<int>(c - at) : 0;
     const int high = kActThreads >> k;
     const int64_t row = static_cast<int64_t>(down) * kActRows * high + (threadIdx.x >> k), last = a.rows - 1;
-    ActRow<T, kCkpt> in[kActRows];
+    ActRow<T, kCkpt, kNt> in[kActRows];
 #pragma unroll
     for (int u = 0; u < kActRows; ++u) {
         const int64_t r = min(row + u * high, last);
@@ -827,18 +827,22 @@ Tiles act_tiles(int64_t rows, int64_t cols) {
     return t;
 }
 template <typename T, int kF, bool kCkpt>
-void act_backward_f(const ActBwd& a, const Tiles& t, hipStream_t stream) {
-    const uint32_t blocks = static_cast<uint32_t>(t.down * t.across);
-    if (a.cols < kV) act_bwd_kernel<T, kF, kCkpt, true><<<blocks, kActThreads, 0, stream>>>(a, t.k, t.across);
-    else act_bwd_kernel<T, kF, kCkpt, false><<<blocks, kActThreads, 0, stream>>>(a, t.k, t.across);
+void act_backward_f(const ActBwd& a, const Tiles& t, bool nt, hipStream_t stream) {
+    constexpr bool kNt = sizeof(T) == 2;   // fp32 vectors are loaded through the cache in any case
+    const auto go = [&](auto kernel) {
+        kernel<<<static_cast<uint32_t>(t.down * t.across), kActThreads, 0, stream>>>(a, t.k, t.across);
+    };
+    if (a.cols < kV) go(act_bwd_kernel<T, kF, kCkpt, true, false>);
+    else if (kNt && nt) go(act_bwd_kernel<T, kF, kCkpt, false, kNt>);
+    else go(act_bwd_kernel<T, kF, kCkpt, false, false>);
 }
 template <typename T, bool kCkpt>
-void act_backward_t(const ActBwd& a, const Tiles& w, hipStream_t stream) {
+void act_backward_t(const ActBwd& a, const Tiles& w, bool nt, hipStream_t stream) {
     switch (a.f) {
-        case kRelu: return act_backward_f<T, kRelu, kCkpt>(a, w, stream);
-        case kGelu: return act_backward_f<T, kGelu, kCkpt>(a, w, stream);
-        case kGeluTanh: return act_backward_f<T, kGeluTanh, kCkpt>(a, w, stream);
-        default: return act_backward_f<T, kSilu, kCkpt>(a, w, stream);
+        case kRelu: return act_backward_f<T, kRelu, kCkpt>(a, w, nt, stream);
+        case kGelu: return act_backward_f<T, kGelu, kCkpt>(a, w, nt, stream);
+        case kGeluTanh: return act_backward_f<T, kGeluTanh, kCkpt>(a, w, nt, stream);
+        default: return act_backward_f<T, kSilu, kCkpt>(a, w, nt, stream);
     }
 }
 
@@ -1004,6 +1008,8 @@ hipError_t launch_act_backward(const ActBwd& a, hipStream_t stream) {
     // runs of rows, as in the forward pass; each run's partial rows follow those before
     const int64_t high = static_cast<int64_t>(kActThreads >> t.k) * kActRows;
     const int64_t run = std::max<int64_t>(1, kMaxBlocks / 2 / t.across) * high;
+    const bool nt = outgrows_cache(a.rows, a.cols, a.bf16, 3 + (a.y.p != nullptr)) &&
+                    aligned16(a.dy.p, a.dy.pitch, a.bf16) && aligned16(a.x.p, a.x.pitch, a.bf16);
     for (int64_t r = 0; r < a.rows; r += run) {
         ActBwd b = a;
         b.rows = std::min(run, a.rows - r);
@@ -1016,11 +1022,11 @@ hipError_t launch_act_backward(const ActBwd& a, hipStream_t stream) {
         Tiles u = t;
         u.down = (b.rows + high - 1) / high;
         if (a.bf16) {
-            if (a.ckpt.codes) act_backward_t<uint16_t, true>(b, u, stream);
-            else act_backward_t<uint16_t, false>(b, u, stream);
+            if (a.ckpt.codes) act_backward_t<uint16_t, true>(b, u, nt, stream);
+            else act_backward_t<uint16_t, false>(b, u, nt, stream);
         } else {
-            if (a.ckpt.codes) act_backward_t<float, true>(b, u, stream);
-            else act_backward_t<float, false>(b, u, stream);
+            if (a.ckpt.codes) act_backward_t<float, true>(b, u, nt, stream);
+            else act_backward_t<float, false>(b, u, nt, stream);
         }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;

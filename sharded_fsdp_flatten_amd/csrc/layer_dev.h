@@ -124,9 +124,12 @@ template <> struct Vec<float> {
 // keep, else cached: an activation was written just before it is read here.  kNtBytes: from that
 // many bytes read and written on.  MI355X, nt against cached, operands rotating: norm forward 84 MB
 // 17.1 / 14.6 us, with residual 403 MB 67.5 / 69.0 us; norm backward 148 MB 34.1 / 30.5 us, 201 MB
-// 40.8 / 42.3 us, 604 MB 111 / 117 us; GELU forward 105 MB 19.6 / 17.0 us, 675 MB 107 / 106 us.
-// Rows that start off a 16-byte boundary share lines between vectors and are always cached (norm
-// forward 8192 x 5003: nt 47.0, cached 38.3 us).  Codes are always cached too: a wave's vector is
+// 40.8 / 42.3 us, 604 MB 111 / 117 us, fp32 63 MB 20.6 / 17.6, 252 MB 53.9 / 57.2, 1.2 GB 214 / 228;
+// GELU forward 105 MB 19.6 / 17.0 us, 675 MB 107 / 106 us; ReLU backward from e4m3 with y 37 MB 12.2 / 11.1
+// us, 147 MB 29.6 / 27.9, 472 MB 76.7 / 83.8.  Rows that start off a 16-byte boundary share lines
+// between vectors and are always cached (norm forward 8192 x 5003: nt 47.0, cached 38.3 us; ReLU backward
+// 8192 x 12289 133.3 / 128.4), but for a residual gradient beside aligned rows, which goes with them (norm
+// backward 8192 x 12288 with an odd pitch there 151 / 158 us).  Codes are always cached too: a wave's vector is
 // 256 or 512 bytes of them (unpack 8192 x 5003: nt 28.0, cached 20.8 us; aligned the same).
 constexpr int64_t kNtBytes = int64_t{192} << 20;
 
