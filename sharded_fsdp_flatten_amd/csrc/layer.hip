@@ -767,8 +767,8 @@ bool aligned16(const void* p, int64_t pitch, bool bf16) {
     return (reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(pitch * (bf16 ? 2 : 4))) % 16 == 0;
 }
 // Whether a call that moves `units` elements for each of rows x cols loads non-temporally.
-bool outgrows_cache(int64_t rows, int64_t cols, bool bf16, int units) {
-    return rows >= kNtBytes / (bf16 ? 2 : 4) / units / cols;
+bool outgrows_cache(int64_t rows, int64_t cols, bool bf16, int units, int64_t bytes = kNtBytes) {
+    return rows >= bytes / (bf16 ? 2 : 4) / units / cols;
 }
 bool norm_fwd_nt(const NormFwd& a) {
     return outgrows_cache(a.rows, a.cols, a.bf16, a.residual.p ? 4 : 2) && aligned16(a.x.p, a.x.pitch, a.bf16) &&
@@ -1008,7 +1008,7 @@ hipError_t launch_act_backward(const ActBwd& a, hipStream_t stream) {
     // runs of rows, as in the forward pass; each run's partial rows follow those before
     const int64_t high = static_cast<int64_t>(kActThreads >> t.k) * kActRows;
     const int64_t run = std::max<int64_t>(1, kMaxBlocks / 2 / t.across) * high;
-    const bool nt = outgrows_cache(a.rows, a.cols, a.bf16, 3 + (a.y.p != nullptr)) &&
+    const bool nt = outgrows_cache(a.rows, a.cols, a.bf16, 3 + (a.y.p != nullptr), kActBwdNtBytes) &&
                     aligned16(a.dy.p, a.dy.pitch, a.bf16) && aligned16(a.x.p, a.x.pitch, a.bf16);
     for (int64_t r = 0; r < a.rows; r += run) {
         ActBwd b = a;

@@ -125,13 +125,16 @@ template <> struct Vec<float> {
 // many bytes read and written on.  MI355X, nt against cached, operands rotating: norm forward 84 MB
 // 17.1 / 14.6 us, with residual 403 MB 67.5 / 69.0 us; norm backward 148 MB 34.1 / 30.5 us, 201 MB
 // 40.8 / 42.3 us, 604 MB 111 / 117 us, fp32 63 MB 20.6 / 17.6, 252 MB 53.9 / 57.2, 1.2 GB 214 / 228;
-// GELU forward 105 MB 19.6 / 17.0 us, 675 MB 107 / 106 us; ReLU backward from e4m3 with y 37 MB 12.2 / 11.1
-// us, 147 MB 29.6 / 27.9, 472 MB 76.7 / 83.8.  Rows that start off a 16-byte boundary share lines
+// GELU forward 105 MB 19.6 / 17.0 us, 675 MB 107 / 106 us.  The activation's backward pass finds the
+// forward pass's matrices between its own and takes kActBwdNtBytes: behind the forward pass, three / six sets
+// of operands rotating, 18 MB 13.9 / 13.3 and 14.0 / 13.2 us for both, 37 MB 18.8 / 17.7 and 18.8 / 17.8, 73 MB
+// 29.2 / 26.4 and 29.4 / 31.6, 147 MB 49.9 / 52.7 and 53.1 / 53.6; alone, 147 MB 31.7 / 28.3 and 31.8 / 32.6, 472 MB
+// 76.7 / 83.8.  Rows that start off a 16-byte boundary share lines
 // between vectors and are always cached (norm forward 8192 x 5003: nt 47.0, cached 38.3 us; ReLU backward
 // 8192 x 12289 133.3 / 128.4), but for a residual gradient beside aligned rows, which goes with them (norm
 // backward 8192 x 12288 with an odd pitch there 151 / 158 us).  Codes are always cached too: a wave's vector is
 // 256 or 512 bytes of them (unpack 8192 x 5003: nt 28.0, cached 20.8 us; aligned the same).
-constexpr int64_t kNtBytes = int64_t{192} << 20;
+constexpr int64_t kNtBytes = int64_t{192} << 20, kActBwdNtBytes = int64_t{64} << 20;
 
 // n: columns of this vector inside the row (8 or more: whole; 0 or less: none).
 template <bool kNt, typename T>
