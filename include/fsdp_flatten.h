@@ -499,8 +499,9 @@ typedef enum { FSDP_BF16 = 1, FSDP_F32 = 2 } fsdp_dtype;
  *     Off by at most 2^-4 of the element's own size (half of 2^(s-9) below
  *     2^(s-6)): for groups with outliers.
  *   FSDP_CKPT_INT8 : codes are integers -127..127 in two's complement;
- *     |x| / 2^s < 127.5, s >= -127.  Off by at most half of 2^s, 1/128 of
- *     the group's largest magnitude: for groups of similar magnitudes.
+ *     |x| / 2^s < 127.5, s >= -127.  Off by at most half of 2^s, which is no more
+ *     than 1/127.5 of the group's largest magnitude where s > -127: for groups of
+ *     similar magnitudes.
  * Rounding is to nearest, ties to even.  Every value a code stands for is a
  * bf16 number, so reading back is exact in bf16 and fp32 (one exception: an
  * element that rounds to 2^128 reads back as infinity).  A group

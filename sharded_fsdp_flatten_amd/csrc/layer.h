@@ -95,7 +95,7 @@ struct BwdShape {
 BwdShape norm_bwd_shape(int64_t cols);
 // Workgroups of these kernels that a CU holds at once: two of 8 waves with 128 registers or one of 16
 // waves; one of 8 waves with more registers where a row's three vectors and a residual gradient are fp32
-// or come with codes (126-150; held to 128 they spill up to 40).
+// or come with codes (up to 150; held to 128 they spill up to 40).
 constexpr int norm_bwd_resident(bool bf16, bool ckpt, bool residual, int threads, int vectors) {
     return threads > 512 || (vectors == 3 && residual && (!bf16 || ckpt)) ? 1 : 2;
 }

@@ -63,8 +63,9 @@ __device__ __forceinline__ void activate(float h, float* y, float* d) {
         // = 1/2 held exactly, so that near 0 the reciprocal's error reaches Q only times q.  Q is within
         // 1e-7 and within (6 + 4|h| + h^2) 2^-24 of itself; a form of a bounded absolute error alone loses the
         // negative tail, where y is h Q.  The clamp (part of the product's instruction) turns an infinite h's
-        // q into a number; the exponential is 0 there.  bf16 4096 x 5120 with checkpoint forward 23.6 us and
-        // from it backward 36.2 (22.1 and 34.9 with five coefficients and Phi off by 4e-7), fp32 36.2 and 57.4.
+        // q into a number; the exponential is 0 there.  bf16 4096 x 5120 with checkpoint forward 23.5 us and
+        // from it backward 35.2, fp32 36.4 and 58.0 (22.1, 34.9, 36.2 and 58.1 with five coefficients and Phi
+        // off by 4e-7).
         const float a = __builtin_fabsf(h);
         const float q = __builtin_amdgcn_fmed3f(a * __builtin_amdgcn_rcpf(a + 3.0f), 0.0f, 1.0f);
         const float e = __builtin_amdgcn_exp2f(h * h * (-0.5f * 1.44269504088896341f));
@@ -352,13 +353,14 @@ struct ActRow {
 // Workgroups that walk down their columns with the sums in registers write fewer partial rows and are
 // slower all the same: a load behind a store waits for the store, and the whole grid reads and writes
 // in step (no sums, 2048 x 65536 from e4m3: one row a lane 146 us, walking 177).  16 waves of one row
-// each, 512 columns wide, against 16 of two and 8 of four rows: ReLU 2048 x 65536 162 / 167 / 171 us,
-// GELU 8192 x 12288 131 / 126 / 129, 4096 x 5120 33.5 / 33.1 / 33.7, 128 x 5120 7.5 / 9.0 / 9.3;
-// 1024 columns wide 165, 138, 35.0 and 7.6.  GELU's and SiLU's own arithmetic takes as long as the
-// memory at these rates: 33 vector instructions an element, two of them at a quarter of the rate.
+// each, 512 columns wide, against 16 of two and 8 of four rows, from e4m3 with y: ReLU 2048 x 65536 166 / 168 /
+// 166 us, 4096 x 5120 29.6 / 31.1 / 31.1, GELU (tanh) 8192 x 12288 131 / 126 / 127, 4096 x 5120 32.2 / 31.8 / 32.0,
+// 128 x 5120 6.8 / 8.0 / 8.1, GELU 8192 x 12288 151 / 136 / 137 (bf16; fp32 252 / 268 / 264); 1024 columns wide
+// 168, 30.6, 136, 33.6, 6.8 and 157.  The arithmetic of SiLU and the GELUs takes as long as the memory or
+// longer: 33, 38 (tanh) and 48 vector instructions an element, two of them at a quarter of the rate; ReLU's 29.
 // The blocks go to the XCDs as dealt: a line of scale bytes serves eight neighbouring blocks, and each
-// XCD reads it (7% more bytes), but runs of 8 to 64 blocks an XCD are slower (ReLU 2048 x 65536: 162.7
-// against 168-171 us, GELU 8192 x 12288: 134 against 134-137).
+// XCD reads it (7% more bytes), but runs of 8 to 64 blocks an XCD are slower (ReLU 2048 x 65536 by 3-5%,
+// GELU (tanh) 8192 x 12288 by 0-2%).
 constexpr int kActThreads = 1024, kActRows = 1;
 constexpr int kActWidest = 6;   // log2 of a block's vectors across, at most
 template <typename T, int kF, bool kCkpt, bool kNarrow, bool kNt>
@@ -867,8 +869,8 @@ RowShape fwd_shape(int64_t cols) {
 bool bwd_in_registers(int64_t cols) { return cols >= 4 && cols <= kMaxRowCols; }
 // Workgroups of the backward pass over rows in registers: each writes a partial row, so there are no
 // more than the device holds at once (256 CUs with `resident` each), four rows a group where that
-// leaves 64, and below that a row each, for latency.  777 x 5003: 195 workgroups 16.0 us, 389 19.6,
-// 512 23.4; 128 x 1280: 32 workgroups 7.4 us, 8 10.7.  Two resident, 512 workgroups against 256: 32768 x 1024
+// leaves 64, and below that a row each, for latency.  777 x 5003: 195 workgroups 15.3 us, 389 17.7,
+// 512 19.4; 128 x 1280: 32 workgroups 6.9 us, 8 9.7.  Two resident, 512 workgroups against 256: 32768 x 1024
 // from int8 45.0 / 50.2 us, 16384 x 1280 from e4m3 29.7 / 28.6.  One resident (a residual gradient in each), 256
 // against 512, and against 512 held to 128 registers: fp32 16384 x 704 37.8 / 40.2 / 52.8 us, 16384 x 1280
 // 60.8 / 63.6 / 63.6, 4096 x 5120 63.3 / 68.3 / 74.8; bf16 from int8 8192 x 5003 101 / 109 / 115.
@@ -958,8 +960,9 @@ hipError_t norm_backward_t(const NormBwd& a, hipStream_t stream) {
 
 // The fewest threads whose three vectors of 4 hold the row (four, beyond 1024 threads): two of a wave's
 // own rows or a few waves' share a workgroup, and its registers allow two of 8 waves a CU.  Rows of
-// 1024 and 1280 columns as one wave's, four and five vectors: 53.1 and 42.0 us where two waves' take
-// 49.6 and 35.4 (32768 x 1024 from int8, 16384 x 1280 from e4m3).
+// 1024 and 1280 columns as one wave's, four and five vectors, leave one workgroup a CU, as fast on many
+// rows (32768 x 1024 from int8 45.3 us, 16384 x 1280 from e4m3 29.8) and slower on few (128 x 1280 8.9 us
+// against 7.0).
 BwdShape norm_bwd_shape(int64_t cols) {
     const int64_t nq = (cols + 3) / 4;
     if (nq <= 64) return {64, 1};

@@ -285,7 +285,7 @@ __device__ __forceinline__ u2 code_load(const uint8_t* p, int n) {
 }
 // Codes are stored non-temporally (kNt) by a pass that writes nothing else, and through the cache
 // beside a norm's or an activation's output (pack 8192 x 12288: nt 52.8, cached 55.9 us; norm forward
-// and backward from int8 32768 x 1024: 80.6 / 75.9 us, ReLU 2048 x 65536: 267 / 260 us).
+// and backward from int8 32768 x 1024: 77.7 / 73.6 us, ReLU 2048 x 65536: 267 / 259 us).
 template <bool kNt>
 __device__ __forceinline__ void code_store(uint8_t* p, u2 q, int n) {
     if (n >= kV) {

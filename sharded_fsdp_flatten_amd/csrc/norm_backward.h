@@ -182,10 +182,10 @@ constexpr int bwd_waves() {
 // its groups' sums and writes one partial row of each.  One pass over the data: dy and the input
 // are read once, and dx (and y) written once, with the row's two means between.
 // Bound by HBM, at the rate of a grid that stays resident (loads wait behind stores, and the
-// workgroups read and write in step): 8192 x 12288 bf16 105 us and 604 MB, 5.7 TB/s; 32768 x
-// 1024 from int8 with y 40 us and 236 MB, 5.9; 24 and 17 vector instructions an element take
-// half that time at most.  More rows in flight do not help (two ahead: 49.7 us for the latter
-// against 48.7), nor do other orders of the rows over the XCDs (within 1%).  Weight and bias lie in LDS: read as
+// workgroups read and write in step).  This kernel alone, in a kernel trace: 8192 x 12288 bf16 107 us and 604 MB,
+// 5.6 TB/s; 32768 x 1024 from int8 with y 41 us and 236 MB, 5.7; 24 and 17 vector instructions an element take
+// half that time at most.  More rows in flight do not help (two ahead: 2% slower at the latter
+// size), nor do other orders of the rows over the XCDs (within 1%).  Weight and bias lie in LDS: read as
 // memory, they would make a row wait for the next one's loads, which return in order.  kWhole:
 // the columns are a multiple of 4; else the vector that the row's end cuts is read from the row's
 // last 4 columns.  A vector outside the row reads its first columns, is left out of the sums
