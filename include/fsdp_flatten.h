@@ -58,7 +58,7 @@ extern "C" {
 #define FSDP_API
 #endif
 
-#define FSDP_ABI_VERSION 4
+#define FSDP_ABI_VERSION 5
 #define FSDP_ALL_RANKS (-1)
 #define FSDP_MAX_NDIM 8
 
@@ -666,6 +666,258 @@ FSDP_API fsdp_status fsdp_act_workspace(int64_t rows, int64_t cols, int64_t* n_f
  */
 FSDP_API fsdp_status fsdp_act_backward(const fsdp_layer_cfg* cfg, const fsdp_act_bwd* io,
                                        void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions: the rotation of queries and keys by their position in
+ * the sequence, around the attention's matrix products.
+ * ------------------------------------------------------------------------ */
+
+/* Which elements of a head form pair i of the `rot` rotated ones. */
+typedef enum {
+    FSDP_ROTARY_HALF = 1,        /* i and i + rot / 2                                       */
+    FSDP_ROTARY_INTERLEAVED = 2  /* 2 i and 2 i + 1                                         */
+} fsdp_rotary_layout;
+
+/* How frequencies are scaled for contexts `factor` times the trained one. */
+typedef enum {
+    FSDP_ROTARY_NONE = 0,        /* f_i = base^(-2 i / rot)                                 */
+    FSDP_ROTARY_LINEAR = 1,      /* f_i / factor                                            */
+    FSDP_ROTARY_NTK = 2,         /* the base is base factor^(rot / (rot - 2)): the first pair
+                                    keeps its frequency, the last one is divided by factor  */
+    FSDP_ROTARY_PARTS = 3        /* f_i (k_i + (1 - k_i) / factor), k_i how far the turns
+                                    trained_len f_i / (2 pi) are from `low` (0) to `high` (1) */
+} fsdp_rotary_scaling;
+
+/* Heads of a batch of sequences: element d of head h of token t of sequence b at
+ * data + b batch_pitch + t token_pitch + h head_pitch + d, so that any order of
+ * the dimensions, and queries and keys inside a packed matrix, can be given.
+ * data NULL: not given.  Pitches are elements, >= 0. */
+typedef struct {
+    void* data;
+    int64_t batch_pitch, token_pitch, head_pitch;
+} fsdp_heads;
+
+typedef struct {
+    int64_t batch, tokens;
+    int64_t heads, kv_heads;   /* of q and of k                                             */
+    int64_t head_dim, rot;     /* rot: even, 2..head_dim; the rest of a head is copied;
+                                  head_dim <= 1024; heads and kv_heads <= 65536             */
+    int64_t start;             /* without positions: token t of every sequence is at start + t */
+    int32_t dtype;             /* of q and k                                                */
+    int32_t layout;            /* an fsdp_rotary_layout                                     */
+    float scale;               /* finite: what is rotated is multiplied by it as well       */
+    int32_t reserved;          /* ignored; set it to 0                                      */
+} fsdp_rotary_cfg;
+
+typedef struct {
+    fsdp_heads q, q_out;       /* q_out may be q itself (the same data and pitches)         */
+    fsdp_heads k, k_out;       /* optional (kv_heads 0: ignored); k_out may be k itself     */
+    const int64_t* positions;  /* optional: batch x tokens device integers                  */
+    const double* freqs;       /* rot / 2 device doubles: angle a position, in radians      */
+} fsdp_rotary_io;
+
+/*
+ * Frequencies of rot / 2 pairs, computed in double (host pointer out; no HIP
+ * call).  trained_len, low and high are read for FSDP_ROTARY_PARTS only, factor
+ * for any scaling but FSDP_ROTARY_NONE.
+ * Errors: FSDP_E_ARG (NULL out), FSDP_E_RANGE (rot odd, below 2 or
+ * above 1024, 2 with FSDP_ROTARY_NTK; base not finite or <= 0; scaling;
+ * factor not finite or <= 0; trained_len < 1; low and high not finite or low >=
+ * high).
+ */
+FSDP_API fsdp_status fsdp_rotary_freqs(int64_t rot, double base, int32_t scaling, double factor,
+                                       int64_t trained_len, double low, double high, double* out);
+
+/*
+ * Rotate pair (a, b) of every head of q and k at position x by the angle w = x f_i:
+ *   (a, b) -> scale (a cos w - b sin w, a sin w + b cos w)
+ * The angle is reduced in binary64: with |x f_i| up to 2^30 it is within 2^-21 of a
+ * turn's radian even at the end of a long context; cosine and sine are
+ * binary32, results rounded once.  Elements behind the rotated ones are copied bit for
+ * bit (in place: left alone).  In place, no other operand may overlap.
+ * An output's heads, tokens and sequences must not overlap: of the pitches with more than one
+ * entry, each from the smallest up must pass the extent of those before it.
+ * batch, tokens or heads + kv_heads == 0: nothing is done.
+ * Errors: FSDP_E_ARG (NULL cfg or io; with elements, a NULL buffer or freqs),
+ * FSDP_E_RANGE (sizes negative, rot, head_dim, dtype, layout, scale, pitches),
+ * FSDP_E_ALIGN, FSDP_E_OVERFLOW (an extent or the number of elements beyond int64), FSDP_E_HIP.
+ */
+FSDP_API fsdp_status fsdp_rotary_forward(const fsdp_rotary_cfg* cfg, const fsdp_rotary_io* io,
+                                         void* stream);
+
+/* The gradients of fsdp_rotary_forward's inputs from those of its outputs: the same
+ * with the angle -w (q and k hold the outputs' gradients).  Errors as there. */
+FSDP_API fsdp_status fsdp_rotary_backward(const fsdp_rotary_cfg* cfg, const fsdp_rotary_io* io,
+                                          void* stream);
+
+/* ------------------------------------------------------------------------
+ * Token log probabilities: what a step ends with, the loss of every token and
+ * the gradient of the logits.
+ * ------------------------------------------------------------------------ */
+
+#define FSDP_LOGPROB_MAX_TOP 64
+
+typedef struct {
+    int64_t rows, cols;        /* cols: the vocabulary, <= 2^30                             */
+    int32_t dtype;             /* of the logits and their gradient                          */
+    int32_t top;               /* forward: alternatives wanted, 0..FSDP_LOGPROB_MAX_TOP, <= cols */
+    float scale;               /* finite, > 0: the logits are multiplied by it (1 / temperature) */
+    int32_t reserved;          /* ignored; set it to 0                                      */
+} fsdp_logprob_cfg;
+
+typedef struct {
+    fsdp_rows logits;
+    const int64_t* tokens;     /* optional: rows device integers                            */
+    float* logprob;            /* with tokens: rows floats                                  */
+    float* max;                /* rows floats                                               */
+    float* logsum;             /* rows floats                                               */
+    float* entropy;            /* optional: rows floats                                     */
+    float* top_logprob;        /* with top: rows x top floats                               */
+    int64_t* top_token;        /* with top: rows x top integers                             */
+    float* workspace;          /* device pointer, 16-byte aligned; unused where
+                                  fsdp_logprob_workspace is 0                               */
+    int64_t workspace_len;     /* floats                                                    */
+} fsdp_logprob_fwd;
+
+typedef struct {
+    fsdp_rows logits;
+    fsdp_rows dlogits;         /* may be the logits themselves (the same data and pitch)    */
+    const int64_t* tokens;     /* with dlogprob                                             */
+    const float* dlogprob;     /* optional: rows floats                                     */
+    const float* dentropy;     /* optional: rows floats                                     */
+    const float* max;          /* as the forward pass wrote them                            */
+    const float* logsum;
+    const float* entropy;      /* with dentropy                                             */
+} fsdp_logprob_bwd;
+
+/* Floats of workspace fsdp_logprob_forward needs for these sizes (0 where a row is not split).
+ * Host only.  Errors: FSDP_E_ARG (NULL n_floats), FSDP_E_RANGE (rows, cols, top). */
+FSDP_API fsdp_status fsdp_logprob_workspace(int64_t rows, int64_t cols, int32_t top,
+                                            int64_t* n_floats);
+
+/*
+ * Log probabilities of given tokens.  With z_j = scale x_j over a row's cols logits x:
+ *   max = max z_j;  logsum = log(sum over j of e^(z_j - max))
+ *   logprob = (z_t - max) - logsum for the row's token t
+ *   entropy = -sum over j of p_j log p_j,  p_j = e^(z_j - max - logsum)
+ *   top_token, top_logprob: the `top` largest logits' columns and log probabilities, in falling
+ *             order, equal logits by rising column
+ * max is rounded, and logsum is of the rounded one: their sum is the logarithm of the sum of
+ * e^z_j.  Sums are binary32.
+ * A token outside [0, cols) is none (a padded position): its logprob is 0.
+ * Logits of -infinity are masked: their probability is 0, and their logprob -infinity.  A
+ * row that holds nothing else (or only logits whose product with scale is -infinity in binary32) has max -infinity, logsum 0, entropy 0 and every logprob
+ * -infinity.  A row that holds a NaN or +infinity (or a product that is) has NaN for logsum, entropy and every logprob
+ * (tokens that are none apart); a NaN is ranked as -infinity.
+ * Every partial result read was written by the same call: the workspace needs no clearing,
+ * and calls that share one must be ordered.
+ * rows or cols == 0: nothing is written.
+ * Errors: FSDP_E_ARG (NULL cfg or io; with elements, NULL logits, max or logsum, one of tokens
+ * and logprob without the other, top without its buffers, a NULL workspace where one is needed),
+ * FSDP_E_RANGE (sizes, dtype, top, scale, a pitch, workspace_len), FSDP_E_ALIGN,
+ * FSDP_E_OVERFLOW, FSDP_E_HIP.
+ */
+FSDP_API fsdp_status fsdp_logprob_forward(const fsdp_logprob_cfg* cfg, const fsdp_logprob_fwd* io,
+                                          void* stream);
+
+/*
+ * Gradient of the logits from those of the log probabilities (dl) and entropies (dh):
+ *   dlogits_j = scale (dl ([j = t] - p_j) - dh p_j (log p_j + entropy))
+ * dl counts as 0 for a token that is none.  Where both dl and dh are 0 (or not given), and
+ * where the forward pass found no logit above -infinity, the row's gradient is 0 whatever the
+ * logits hold, and they are not read.
+ * Errors: FSDP_E_ARG (NULL cfg or io; neither dlogprob nor dentropy; with elements, NULL logits,
+ * dlogits, max or logsum, dlogprob without tokens, dentropy without entropy), FSDP_E_RANGE,
+ * FSDP_E_ALIGN, FSDP_E_OVERFLOW, FSDP_E_HIP.
+ */
+FSDP_API fsdp_status fsdp_logprob_backward(const fsdp_logprob_cfg* cfg, const fsdp_logprob_bwd* io,
+                                           void* stream);
+
+/* ------------------------------------------------------------------------
+ * AdamW over many tensors: the shards of a rank's units (or the row shards of
+ * its parameters) in a few launches, each tensor with its group's hyper-parameters, states in
+ * 32 or 8 bits.
+ * ------------------------------------------------------------------------ */
+
+/* How exp_avg (m) and exp_avg_sq (v) are held.  In 8 bits a state of n elements is one buffer:
+ * n codes, filled up to a multiple of 16 bytes, then ceil(n / 32) scale bytes, one for every 32
+ * elements in order (the last group may be shorter).  A scale byte b stands for 2^(b - 127); an
+ * element is its code times that.  255: the group held an infinity or a NaN, and reads back as NaN
+ * throughout.  All bytes 0 is a state of zeros.
+ *   m: 8-bit floats with a sign, 4 exponent bits of bias 7, 3 mantissa bits, largest 448;
+ *      scales from 2^-124
+ *   v: 8-bit floats without a sign, 5 exponent bits of bias 15, 3 mantissa bits, largest 61440
+ *      (the 8 bits below the sign of a binary16 number); scales from 2^-116
+ * The scale is the smallest power of two at which the group's largest magnitude is not above
+ * the largest code.  Every value a code stands for is a bf16 number.
+ * Codes are rounded at random: the code below a magnitude or the one above it, with the odds
+ * of its place between them, so that a state's expected value is the exact one (to nearest, v would
+ * not move while a step changes it by less than half a code, as beta2 = 0.999 does).  The random
+ * number of element j of the list's tensor i in step t is a hash of (seed, t, i, j): the same
+ * call gives the same bits. */
+typedef enum {
+    FSDP_STATE_F32 = 1,
+    FSDP_STATE_8BIT = 2,
+    FSDP_STATE_BF16 = 3        /* fsdp_adam_convert only                                    */
+} fsdp_state_format;
+
+#define FSDP_ADAM_MAX_GROUPS 16
+
+typedef struct {
+    int64_t numel;
+    float* param;              /* updated in place                                          */
+    const void* grad;          /* numel elements of grad_dtype                              */
+    void* exp_avg;             /* states of the list's format, updated in place             */
+    void* exp_avg_sq;
+    uint16_t* param_bf16;      /* optional: receives bf16(new param)                        */
+    int32_t group;             /* index into groups                                         */
+    int32_t reserved;          /* ignored; set it to 0                                      */
+} fsdp_adam_tensor;
+
+typedef struct {
+    int32_t n_tensors, n_groups;
+    int32_t state_format;      /* FSDP_STATE_F32 or FSDP_STATE_8BIT                         */
+    int32_t grad_dtype;        /* FSDP_BF16 or FSDP_F32                                     */
+    uint64_t seed;             /* 8-bit states: of the random numbers                       */
+    const float* grad_scale;   /* optional: device pointer to one float; every gradient is
+                                  multiplied by it first (clipping, unscaling)              */
+    const float* skip;         /* optional: device pointer to one float; where it is not 0
+                                  (fsdp_grad_unscale's found_inf) the step changes nothing   */
+} fsdp_adam_list;
+
+/* Bytes of the 8-bit state of numel elements.  Host only.  Errors: FSDP_E_ARG (NULL bytes),
+ * FSDP_E_RANGE (numel negative), FSDP_E_OVERFLOW. */
+FSDP_API fsdp_status fsdp_adam_state_bytes(int64_t numel, int64_t* bytes);
+
+/*
+ * One AdamW step over a list of tensors: for each of them what fsdp_adam_shard
+ * computes with its group's cfg, with states in 32 bits bit for bit (after the rounded multiply by
+ * *grad_scale, where given).  With 8-bit states param is updated from the new m and v before
+ * their rounding.
+ *   tensors : host array of n_tensors, groups : host array of n_groups; both are read during
+ *             the call.
+ * No two tensors may overlap.  The list is cut into as many launches as its table needs (50
+ * tensors a launch).
+ * Errors: FSDP_E_ARG (NULL list; NULL tensors or groups with tensors; a NULL buffer of a tensor
+ * with elements), FSDP_E_RANGE (n_tensors negative, n_groups outside
+ * 1..FSDP_ADAM_MAX_GROUPS, state_format, grad_dtype, a numel negative, a tensor's group, a group's
+ * values as for fsdp_adam_shard), FSDP_E_ALIGN, FSDP_E_OVERFLOW (numel > 2^40), FSDP_E_HIP.
+ */
+FSDP_API fsdp_status fsdp_adam_tensors(const fsdp_adam_list* list, const fsdp_adam_tensor* tensors,
+                                       const fsdp_adamw_cfg* groups, void* stream);
+
+/*
+ * Copy the states of a list of tensors from one format to another, of which one has to be
+ * FSDP_STATE_8BIT: to save 8-bit states, or to start from others.  From 8 bits the values are exact
+ * (in bf16 as well); to 8 bits they are rounded as by a step of the number `step` with the
+ * same seed.  Only numel, exp_avg and exp_avg_sq of the tensors are read; exp_avg_sq must hold
+ * no negative values.  numel has to be the same in both lists.
+ * Errors: FSDP_E_ARG (NULL arrays or buffers), FSDP_E_RANGE (n_tensors, the formats, numel, step < 1),
+ * FSDP_E_ALIGN, FSDP_E_OVERFLOW, FSDP_E_HIP.
+ */
+FSDP_API fsdp_status fsdp_adam_convert(int32_t n_tensors, const fsdp_adam_tensor* from,
+                                       int32_t from_format, const fsdp_adam_tensor* to,
+                                       int32_t to_format, uint64_t seed, int64_t step, void* stream);
 
 #ifdef __cplusplus
 }

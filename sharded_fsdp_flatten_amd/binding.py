@@ -16,7 +16,7 @@ FSDP_FLAT = 1
 FSDP_ROWS = 2
 FSDP_ALL_RANKS = -1
 FSDP_MAX_NDIM = 8
-ABI_VERSION = 4  # FSDP_ABI_VERSION of include/fsdp_flatten.h this binding marshals for
+ABI_VERSION = 5  # FSDP_ABI_VERSION of include/fsdp_flatten.h this binding marshals for
 
 STATUS_NAMES = {0: "FSDP_OK", 1: "FSDP_E_ARG", 2: "FSDP_E_RANGE", 3: "FSDP_E_ALIGN",
                 4: "FSDP_E_OVERFLOW", 5: "FSDP_E_NOMEM", 6: "FSDP_E_HIP",
@@ -472,4 +472,8 @@ ABI_FUNCTIONS = ["fsdp_abi_version", "fsdp_last_error", "fsdp_status_string", "f
                  # the layer operators, bound in layer.py
                  "fsdp_ckpt_pack", "fsdp_ckpt_unpack", "fsdp_norm_forward", "fsdp_norm_workspace",
                  "fsdp_norm_backward", "fsdp_act_forward", "fsdp_act_workspace",
-                 "fsdp_act_backward"]
+                 "fsdp_act_backward",
+                 # the training step's other operators, bound in train.py
+                 "fsdp_rotary_freqs", "fsdp_rotary_forward", "fsdp_rotary_backward",
+                 "fsdp_logprob_workspace", "fsdp_logprob_forward", "fsdp_logprob_backward",
+                 "fsdp_adam_state_bytes", "fsdp_adam_tensors", "fsdp_adam_convert"]

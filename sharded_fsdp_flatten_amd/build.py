@@ -35,7 +35,8 @@ LIB_NAME = "libfsdpflat.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 SOURCES = ["norm_backward_bf16.hip", "norm_backward_f32.hip", "norm_backward_bf16_nt.hip",
-           "norm_backward_f32_nt.hip", "layer.hip", "kernels.hip", "plan.cpp", "fsdp_abi.cpp"]
+           "norm_backward_f32_nt.hip", "layer.hip", "kernels.hip", "rotary.hip", "logprob.hip",
+           "adam_tensors.hip", "plan.cpp", "fsdp_abi.cpp"]
 PROBE_LIB_PATH = os.path.join(HERE, "libfsdpprobe.so")
 PROBE_SOURCES = ["probes.hip"]
 

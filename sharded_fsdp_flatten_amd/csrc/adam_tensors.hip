@@ -1,0 +1,414 @@
+// adam_tensors.hip -- AdamW over a list of tensors, states in fp32 or 8 bits, and the conversion between
+// state formats.
+//
+// A launch carries a table of tensors in its arguments; a workgroup takes one tile of one tensor.  With
+// fp32 states every element takes the operations of the single shard's step, each rounded on its own.
+// 8-bit states (m: e4m3, v: e5m3, a power-of-two scale for 32 elements) are read, updated in fp32, and
+// rounded at random to codes again.  Bound by HBM: 28 bytes an element with fp32 states, 16.1 with 8-bit ones.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "train.h"
+
+#pragma clang fp contract(off)
+
+namespace fsdp {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = kThreads * 8;   // elements of a workgroup
+constexpr int kLaunch = 50;           // tensors of a launch (kernel-argument budget)
+constexpr int64_t kMaxTiles = int64_t{1} << 22;
+
+typedef uint32_t u2e __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u1e __attribute__((aligned(1)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef float f4e __attribute__((ext_vector_type(4), aligned(4)));
+typedef float f2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+
+// ---------------------------------------------------------------------------
+// 8-bit states
+// ---------------------------------------------------------------------------
+struct FormatM {   // e4m3, signed
+    static constexpr int kMinExp = -6, kLowByte = 3, kTopExp = 8;
+    static constexpr uint32_t kTopMant = 0x600000u;   // 448 = 1.75 x 2^8
+};
+struct FormatV {   // e5m3, unsigned: the 8 bits below the sign of a binary16 number
+    static constexpr int kMinExp = -14, kLowByte = 11, kTopExp = 15;
+    static constexpr uint32_t kTopMant = 0x700000u;   // 61440 = 1.875 x 2^15
+};
+
+// The scale byte of a group with this largest magnitude: the smallest power of two at which it is not
+// above the largest code.
+template <typename F>
+__device__ __forceinline__ uint32_t scale_byte(float amax) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, amax), e = b >> 23, m = b & 0x7FFFFFu;
+    if (e == 255u) return 255u;
+    return static_cast<uint32_t>(max(static_cast<int>(e) - F::kTopExp + (m > F::kTopMant), F::kLowByte));
+}
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+    // 2^(byte - 127); 255: NaN; 0 (a state of zeros): 0
+    return __builtin_bit_cast(float, byte == 255u ? 0x7FC00000u : byte << 23);
+}
+// x, scaled by 1 / 2^s, rounded at random to a code's value.
+template <typename F>
+__device__ __forceinline__ float round_code(float x, float inv, uint32_t r16) {
+    const float y = fabsf(x) * inv;
+    // an eighth of the power of two below y, and its inverse
+    const uint32_t e = max(__builtin_bit_cast(uint32_t, y) & 0x7F800000u, static_cast<uint32_t>(F::kMinExp + 127) << 23);
+    const float q = __builtin_bit_cast(float, e - (3u << 23)), iq = __builtin_bit_cast(float, (257u << 23) - e);
+    const float n = floorf(y * iq + static_cast<float>(r16) * 0x1p-16f);
+    return copysignf(n * q, x);
+}
+// Four codes of a word, and back.  Values that are codes convert exactly.
+__device__ __forceinline__ uint32_t pack_m(const float* v) {
+    int w = 0;
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], w, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], w, true);
+    return static_cast<uint32_t>(w);
+}
+__device__ __forceinline__ uint32_t pack_v(const float* v) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        w |= static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<_Float16>(v[j])) >> 7 & 0xFFu) << (8 * j);
+    return w;
+}
+__device__ __forceinline__ void unpack_m(uint32_t w, float scale, float* v) {
+    const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false);
+    const f2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), true);
+    v[0] = a[0] * scale;
+    v[1] = a[1] * scale;
+    v[2] = b[0] * scale;
+    v[3] = b[1] * scale;
+}
+__device__ __forceinline__ void unpack_v(uint32_t w, float scale, float* v) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint16_t h = static_cast<uint16_t>(((w >> (8 * j)) & 255u) << 7);
+        v[j] = static_cast<float>(__builtin_bit_cast(_Float16, h)) * scale;
+    }
+}
+// Random bits of an element: a xor-shift-multiply hash of its number and the tensor's key (multipliers
+// next to 2^32 times the golden ratio, and the square roots of 2 and 3); m takes the upper 16, v the lower.
+__device__ __forceinline__ uint32_t random_bits(uint64_t element, uint32_t key) {
+    uint32_t x = static_cast<uint32_t>(element) * 0x9E3779B1u + key + static_cast<uint32_t>(element >> 32) * 0xDDB3D743u;
+    x ^= x >> 15;
+    x *= 0xB504F333u;
+    x ^= x >> 13;
+    x *= 0xDDB3D743u;
+    return x ^ (x >> 16);
+}
+// The largest of a group's eight lanes.
+__device__ __forceinline__ float group_max(float x) {
+    const auto dpp = [](float v, auto ctrl) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xF, 0xF, true));
+    };
+    // magnitudes as bits, so that a NaN is the largest
+    const auto top = [](float a, float b) {
+        return __builtin_bit_cast(float, max(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)));
+    };
+    x = top(x, dpp(x, std::integral_constant<int, 0xB1>{}));   // lanes xor 1
+    x = top(x, dpp(x, std::integral_constant<int, 0x4E>{}));   // xor 2
+    return top(x, dpp(x, std::integral_constant<int, 0x141>{}));  // the half row mirrored
+}
+__device__ __forceinline__ float largest(const float* v) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a = max(a, __builtin_bit_cast(uint32_t, v[j]) & 0x7FFFFFFFu);
+    return __builtin_bit_cast(float, a);
+}
+// Four elements of a state (n of them inside the tensor), element `at` its first.
+template <typename F>
+__device__ __forceinline__ void load8(const uint8_t* s, int64_t at, int n, int64_t scales, float* v) {
+    uint32_t w = 0;
+    if (n >= 4) {
+        w = *(const u1e*)(s + at);
+    } else {
+        for (int j = 0; j < 3; ++j)
+            if (j < n) w |= static_cast<uint32_t>(s[at + j]) << (8 * j);
+    }
+    const float scale = n > 0 ? scale_value(s[scales + at / kStateGroup]) : 0.0f;
+    if constexpr (F::kTopExp == 8) unpack_m(w, scale, v);
+    else unpack_v(w, scale, v);
+}
+// Every lane of a group calls it; values behind the tensor's end are 0.
+template <typename F>
+__device__ __forceinline__ void store8(uint8_t* s, int64_t at, int n, int64_t scales, const float* v, const uint32_t* r, bool high) {
+    const uint32_t byte = scale_byte<F>(group_max(largest(v)));
+    uint32_t w = 0;
+    if (byte != 255u) {
+        const float inv = __builtin_bit_cast(float, (254u - byte) << 23);
+        float c[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[j] = round_code<F>(v[j], inv, high ? r[j] >> 16 : r[j] & 0xFFFFu);
+        w = F::kTopExp == 8 ? pack_m(c) : pack_v(c);
+    }
+    if (n >= 4) {
+        *(u1e*)(s + at) = w;
+    } else {
+        for (int j = 0; j < 3; ++j)
+            if (j < n) s[at + j] = static_cast<uint8_t>(w >> (8 * j));
+    }
+    if (n > 0 && (threadIdx.x & 7) == 0) s[scales + at / kStateGroup] = static_cast<uint8_t>(byte);
+}
+
+// ---------------------------------------------------------------------------
+// four elements of an fp32 or bf16 array
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void load4(const float* p, int n, float* v) {
+    if (n >= 4) {
+        const f4 t = *(const f4e*)p;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = t[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = j < n ? p[j] : 0.0f;
+    }
+}
+__device__ __forceinline__ void load4(const uint16_t* p, int n, float* v) {
+    uint32_t w[2] = {0u, 0u};
+    if (n >= 4) {
+        const u2e t = *(const u2e*)p;
+        w[0] = t[0];
+        w[1] = t[1];
+    } else {
+        for (int j = 0; j < 3; ++j)
+            if (j < n) w[j >> 1] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __builtin_bit_cast(float, j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+}
+__device__ __forceinline__ void store4(float* p, int n, const float* v) {
+    if (n >= 4) {
+        *(f4e*)p = f4{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < n) p[j] = v[j];
+    }
+}
+__device__ __forceinline__ void store4(uint16_t* p, int n, const float* v) {
+    u2e w;
+    w[0] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v[0], v[1]}), bf2));
+    w[1] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v[2], v[3]}), bf2));
+    if (n >= 4) {
+        *(u2e*)p = w;
+    } else {
+        for (int j = 0; j < 3; ++j)
+            if (j < n) p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the step
+// ---------------------------------------------------------------------------
+struct Entry {
+    float* p;
+    const void* g;
+    void *m, *v;
+    uint16_t* pb;
+    int64_t n;
+    uint32_t bias;      // the tensor's tiles that earlier launches took
+    uint32_t key;
+    uint32_t group, unused;
+};
+struct Table {
+    uint32_t start[kLaunch];   // first tile of each entry; beyond the last entry: all tiles
+    Entry e[kLaunch];
+    AdamScalars sc[kAdamGroups];
+    const float *grad_scale, *skip;
+};
+static_assert(sizeof(Table) <= 4096 - 64, "the table must fit one kernel argument block");
+
+__device__ __forceinline__ void adam1(float& p, float g, float& m, float& v, const AdamScalars& s) {
+    p = p * s.decay;
+    m = s.b1 * m + s.omb1 * g;
+    const float gg = g * g;
+    v = s.b2 * v + s.omb2 * gg;
+    const float den = sqrtf(v) / s.bc2s + s.eps;
+    p = p - s.step_size * (m / den);
+}
+
+template <typename G, bool k8>
+__global__ void __launch_bounds__(kThreads) adam_tensors_kernel(Table t) {
+    if (t.skip && *t.skip != 0.0f) return;
+    uint32_t k = 0;
+    for (int i = 1; i < kLaunch; ++i) k += t.start[i] <= blockIdx.x ? 1u : 0u;
+    const Entry& e = t.e[k];
+    const AdamScalars s = t.sc[e.group];
+    const float gs = t.grad_scale ? *t.grad_scale : 1.0f;
+    const int64_t base = (static_cast<int64_t>(blockIdx.x - t.start[k]) + e.bias) * kTile;
+    const int64_t scales = (e.n + 15) / 16 * 16;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t at = base + 4 * (threadIdx.x + h * kThreads);
+        const int n = static_cast<int>(max(min(e.n - at, int64_t{4}), int64_t{0}));
+        float p[4], g[4], m[4], v[4];
+        load4(e.p + at, n, p);
+        load4(static_cast<const G*>(e.g) + at, n, g);
+        if constexpr (k8) {
+            load8<FormatM>(static_cast<const uint8_t*>(e.m), at, n, scales, m);
+            load8<FormatV>(static_cast<const uint8_t*>(e.v), at, n, scales, v);
+        } else {
+            load4(static_cast<const float*>(e.m) + at, n, m);
+            load4(static_cast<const float*>(e.v) + at, n, v);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) adam1(p[j], t.grad_scale ? g[j] * gs : g[j], m[j], v[j], s);
+        store4(e.p + at, n, p);
+        if (e.pb) store4(e.pb + at, n, p);
+        if constexpr (k8) {
+            uint32_t r[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                r[j] = random_bits(static_cast<uint64_t>(at + j), e.key);
+                if (j >= n) m[j] = v[j] = 0.0f;
+            }
+            store8<FormatM>(static_cast<uint8_t*>(e.m), at, n, scales, m, r, true);
+            store8<FormatV>(static_cast<uint8_t*>(e.v), at, n, scales, v, r, false);
+        } else {
+            store4(static_cast<float*>(e.m) + at, n, m);
+            store4(static_cast<float*>(e.v) + at, n, v);
+        }
+    }
+}
+
+struct CopyEntry {
+    const void *m, *v;
+    void *m_to, *v_to;
+    int64_t n;
+    uint32_t bias, key;
+};
+struct CopyTable {
+    uint32_t start[kLaunch];
+    CopyEntry e[kLaunch];
+};
+
+template <State kFrom, State kTo>
+__global__ void __launch_bounds__(kThreads) adam_convert_kernel(CopyTable t) {
+    uint32_t k = 0;
+    for (int i = 1; i < kLaunch; ++i) k += t.start[i] <= blockIdx.x ? 1u : 0u;
+    const CopyEntry& e = t.e[k];
+    const int64_t base = (static_cast<int64_t>(blockIdx.x - t.start[k]) + e.bias) * kTile;
+    const int64_t scales = (e.n + 15) / 16 * 16;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t at = base + 4 * (threadIdx.x + h * kThreads);
+        const int n = static_cast<int>(max(min(e.n - at, int64_t{4}), int64_t{0}));
+        float m[4], v[4];
+        if constexpr (kFrom == State::k8Bit) {
+            load8<FormatM>(static_cast<const uint8_t*>(e.m), at, n, scales, m);
+            load8<FormatV>(static_cast<const uint8_t*>(e.v), at, n, scales, v);
+        } else if constexpr (kFrom == State::kBF16) {
+            load4(static_cast<const uint16_t*>(e.m) + at, n, m);
+            load4(static_cast<const uint16_t*>(e.v) + at, n, v);
+        } else {
+            load4(static_cast<const float*>(e.m) + at, n, m);
+            load4(static_cast<const float*>(e.v) + at, n, v);
+        }
+        if constexpr (kTo == State::k8Bit) {
+            uint32_t r[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[j] = random_bits(static_cast<uint64_t>(at + j), e.key);
+            store8<FormatM>(static_cast<uint8_t*>(e.m_to), at, n, scales, m, r, true);
+            store8<FormatV>(static_cast<uint8_t*>(e.v_to), at, n, scales, v, r, false);
+        } else if constexpr (kTo == State::kBF16) {
+            store4(static_cast<uint16_t*>(e.m_to) + at, n, m);
+            store4(static_cast<uint16_t*>(e.v_to) + at, n, v);
+        } else {
+            store4(static_cast<float*>(e.m_to) + at, n, m);
+            store4(static_cast<float*>(e.v_to) + at, n, v);
+        }
+    }
+}
+
+int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
+
+// Cuts a list into launches: fill(table slot, list index, tiles taken before) for every entry, then
+// launch(tiles).  A tensor too long for one launch goes on in the next.
+template <typename TableT, typename List, typename Fill, typename Launch>
+hipError_t in_launches(const List& list, TableT& t, Fill&& fill, Launch&& launch) {
+    int used = 0;
+    int64_t tiles = 0;
+    const auto flush = [&]() -> hipError_t {
+        if (!used) return hipSuccess;
+        for (int i = used; i < kLaunch; ++i) t.start[i] = UINT32_MAX;
+        launch(static_cast<uint32_t>(tiles));
+        used = 0;
+        tiles = 0;
+        return hipGetLastError();
+    };
+    for (size_t i = 0; i < list.size(); ++i) {
+        const int64_t all = tiles_of(list[i].n);
+        for (int64_t done = 0; done < all;) {
+            const int64_t now = std::min(all - done, kMaxTiles - tiles);
+            t.start[used] = static_cast<uint32_t>(tiles);
+            fill(used++, list[i], static_cast<uint32_t>(done));
+            done += now;
+            tiles += now;
+            if (used == kLaunch || tiles == kMaxTiles) {
+                const hipError_t e = flush();
+                if (e != hipSuccess) return e;
+            }
+        }
+    }
+    return flush();
+}
+
+template <typename G, bool k8>
+hipError_t step(const std::vector<AdamTensor>& list, Table& t, hipStream_t stream) {
+    return in_launches(
+        list, t,
+        [&](int i, const AdamTensor& a, uint32_t bias) {
+            t.e[i] = {a.p, a.g, a.m, a.v, a.pb, a.n, bias, a.key, static_cast<uint32_t>(a.group), 0};
+        },
+        [&](uint32_t tiles) { adam_tensors_kernel<G, k8><<<dim3(tiles), kThreads, 0, stream>>>(t); });
+}
+
+template <State kFrom, State kTo>
+hipError_t convert(const std::vector<StateCopy>& list, hipStream_t stream) {
+    CopyTable t{};
+    return in_launches(
+        list, t,
+        [&](int i, const StateCopy& a, uint32_t bias) { t.e[i] = {a.m, a.v, a.m_to, a.v_to, a.n, bias, a.key}; },
+        [&](uint32_t tiles) { adam_convert_kernel<kFrom, kTo><<<dim3(tiles), kThreads, 0, stream>>>(t); });
+}
+
+uint64_t mix64(uint64_t k) {
+    k = (k ^ (k >> 30)) * 0xBF58476D1CE4E5B9ull;
+    k = (k ^ (k >> 27)) * 0x94D049BB133111EBull;
+    return k ^ (k >> 31);
+}
+
+}  // namespace
+
+uint32_t adam_key(uint64_t seed, int64_t step, int64_t tensor) {
+    constexpr uint64_t kGolden = 0x9E3779B97F4A7C15ull;
+    return static_cast<uint32_t>(mix64(mix64(seed + kGolden * static_cast<uint64_t>(step)) +
+                                       kGolden * (static_cast<uint64_t>(tensor) + 1)));
+}
+
+hipError_t launch_adam_tensors(const std::vector<AdamTensor>& list, const AdamScalars* groups, int n_groups,
+                               bool state8, bool grad_bf16, const float* grad_scale, const float* skip,
+                               hipStream_t stream) {
+    Table t{};
+    std::copy(groups, groups + n_groups, t.sc);
+    t.grad_scale = grad_scale;
+    t.skip = skip;
+    if (state8) return grad_bf16 ? step<uint16_t, true>(list, t, stream) : step<float, true>(list, t, stream);
+    return grad_bf16 ? step<uint16_t, false>(list, t, stream) : step<float, false>(list, t, stream);
+}
+
+hipError_t launch_adam_convert(const std::vector<StateCopy>& list, State from, State to, hipStream_t stream) {
+    if (from == State::k8Bit)
+        return to == State::kBF16 ? convert<State::k8Bit, State::kBF16>(list, stream)
+                                  : convert<State::k8Bit, State::kF32>(list, stream);
+    return from == State::kBF16 ? convert<State::kBF16, State::k8Bit>(list, stream)
+                                : convert<State::kF32, State::k8Bit>(list, stream);
+}
+
+}  // namespace fsdp

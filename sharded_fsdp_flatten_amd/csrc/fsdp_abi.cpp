@@ -13,11 +13,13 @@
 #include <memory>
 #include <new>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "kernels.h"
 #include "layer.h"
 #include "plan.h"
+#include "train.h"
 
 struct fsdp_unit {
     fsdp::UnitPlan plan;
@@ -254,6 +256,147 @@ fsdp_status check_grad(const fsdp_layer_cfg* c, void* p, const char* name, fsdp:
     return s != FSDP_OK ? s : check_buf(p, 1, elem_size(c->grad_dtype), name);
 }
 
+// AdamW's hyper-parameters, and the scalars that a step takes from them: Kingma & Ba's bias corrections
+// and decoupled decay in double, each rounded once to float.
+fsdp_status adam_scalars(const fsdp_adamw_cfg& cfg, fsdp::AdamScalars* sc) {
+    if (cfg.step < 1) return fail(FSDP_E_RANGE, "step must be >= 1");
+    if (!(cfg.beta1 >= 0.0 && cfg.beta1 < 1.0)) return fail(FSDP_E_RANGE, "beta1 not in [0,1)");
+    if (!(cfg.beta2 >= 0.0 && cfg.beta2 < 1.0)) return fail(FSDP_E_RANGE, "beta2 not in [0,1)");
+    if (!std::isfinite(cfg.lr)) return fail(FSDP_E_RANGE, "lr must be finite");
+    if (!std::isfinite(cfg.eps) || cfg.eps < 0.0)
+        return fail(FSDP_E_RANGE, "eps must be finite and >= 0");
+    if (!std::isfinite(cfg.weight_decay)) return fail(FSDP_E_RANGE, "weight_decay must be finite");
+    const double t = static_cast<double>(cfg.step);
+    sc->decay = static_cast<float>(1.0 - cfg.lr * cfg.weight_decay);
+    sc->b1 = static_cast<float>(cfg.beta1);
+    sc->omb1 = static_cast<float>(1.0 - cfg.beta1);
+    sc->b2 = static_cast<float>(cfg.beta2);
+    sc->omb2 = static_cast<float>(1.0 - cfg.beta2);
+    sc->step_size = static_cast<float>(cfg.lr / (1.0 - std::pow(cfg.beta1, t)));
+    sc->bc2s = static_cast<float>(std::sqrt(1.0 - std::pow(cfg.beta2, t)));
+    sc->eps = static_cast<float>(cfg.eps);
+    return FSDP_OK;
+}
+
+// ---- rotary ----
+
+// n[i] entries `pitch[i]` apart, innermost elements `inner` long: the extent in elements, and for an
+// output that no two entries overlap.
+fsdp_status check_heads(const fsdp_heads& x, int64_t batch, int64_t tokens, int64_t heads, int64_t inner,
+                        size_t elem, bool out, const char* name) {
+    fsdp_status s = check_buf(x.data, 1, elem, name);
+    if (s != FSDP_OK) return s;
+    int64_t n[3] = {batch, tokens, heads}, pitch[3] = {x.batch_pitch, x.token_pitch, x.head_pitch};
+    for (const int64_t p : pitch)
+        if (p < 0) return fail(FSDP_E_RANGE, std::string(name) + " has a negative pitch");
+    for (int i = 0; i < 2; ++i)  // by pitch, the smallest first
+        for (int j = 0; j < 2 - i; ++j)
+            if (pitch[j] > pitch[j + 1]) {
+                std::swap(pitch[j], pitch[j + 1]);
+                std::swap(n[j], n[j + 1]);
+            }
+    int64_t extent = inner;
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] == 1) continue;
+        if (out && pitch[i] < extent)
+            return fail(FSDP_E_RANGE, std::string(name) + "'s heads, tokens or sequences overlap");
+        int64_t more;
+        if (__builtin_mul_overflow(n[i] - 1, pitch[i], &more) ||
+            __builtin_add_overflow(extent, more, &extent) || extent > INT64_MAX / 8)
+            return fail(FSDP_E_OVERFLOW, std::string(name) + "'s extent overflows int64");
+    }
+    return FSDP_OK;
+}
+
+fsdp::Heads heads_of(const fsdp_heads& x) {
+    return {x.data, x.batch_pitch, x.token_pitch, x.head_pitch};
+}
+
+fsdp_status rotary_impl(const fsdp_rotary_cfg* c, const fsdp_rotary_io* io, float sign, const char* who,
+                        void* stream) {
+    if (!c || !io) return fail(FSDP_E_ARG, c ? "io is NULL" : "cfg is NULL");
+    if (c->batch < 0 || c->tokens < 0) return fail(FSDP_E_RANGE, "batch and tokens must not be negative");
+    if (c->heads < 0 || c->heads > 65536 || c->kv_heads < 0 || c->kv_heads > 65536)
+        return fail(FSDP_E_RANGE, "heads and kv_heads must be in [0, 65536]");
+    if (c->head_dim < 2 || c->head_dim > 1024) return fail(FSDP_E_RANGE, "head_dim must be in [2, 1024]");
+    if (c->rot < 2 || c->rot > c->head_dim || c->rot % 2)
+        return fail(FSDP_E_RANGE, "rot must be even, in [2, head_dim]");
+    fsdp_status s;
+    if ((s = check_dtype(c->dtype, "dtype")) != FSDP_OK) return s;
+    if (c->layout != FSDP_ROTARY_HALF && c->layout != FSDP_ROTARY_INTERLEAVED)
+        return fail(FSDP_E_RANGE, "layout must be FSDP_ROTARY_HALF or FSDP_ROTARY_INTERLEAVED");
+    if (!std::isfinite(c->scale)) return fail(FSDP_E_RANGE, "scale must be finite");
+    const int64_t heads = c->heads + c->kv_heads;
+    if (c->batch == 0 || c->tokens == 0 || heads == 0) return ok();
+    if (c->tokens > INT64_MAX / 8 / c->batch / heads / c->head_dim)
+        return fail(FSDP_E_OVERFLOW, "batch x tokens x heads x head_dim overflows int64");
+    const size_t e = elem_size(c->dtype);
+    const auto check = [&](const fsdp_heads& x, int64_t n, bool out, const char* name) {
+        return n == 0 ? FSDP_OK : check_heads(x, c->batch, c->tokens, n, c->head_dim, e, out, name);
+    };
+    if ((s = check(io->q, c->heads, false, "q")) != FSDP_OK ||
+        (s = check(io->q_out, c->heads, true, "q_out")) != FSDP_OK ||
+        (s = check(io->k, c->kv_heads, false, "k")) != FSDP_OK ||
+        (s = check(io->k_out, c->kv_heads, true, "k_out")) != FSDP_OK ||
+        (s = check_buf(io->positions, io->positions != nullptr, sizeof(int64_t), "positions")) != FSDP_OK ||
+        (s = check_buf(io->freqs, 1, sizeof(double), "freqs")) != FSDP_OK)
+        return s;
+    fsdp::Rotary a{};
+    a.batch = c->batch;
+    a.tokens = c->tokens;
+    a.heads = c->heads;
+    a.kv_heads = c->kv_heads;
+    a.start = c->start;
+    a.head_dim = static_cast<int32_t>(c->head_dim);
+    a.rot = static_cast<int32_t>(c->rot);
+    a.bf16 = c->dtype == FSDP_BF16;
+    a.interleaved = c->layout == FSDP_ROTARY_INTERLEAVED;
+    a.scale = c->scale;
+    a.sign = sign;
+    a.q = heads_of(io->q);
+    a.q_out = heads_of(io->q_out);
+    a.k = heads_of(io->k);
+    a.k_out = heads_of(io->k_out);
+    a.positions = io->positions;
+    a.freqs = io->freqs;
+    const hipError_t err = fsdp::launch_rotary(a, static_cast<hipStream_t>(stream));
+    return err != hipSuccess ? hip_fail(err, (std::string(who) + " launch").c_str()) : ok();
+}
+
+// ---- log probabilities ----
+
+fsdp_status check_logprob(const fsdp_logprob_cfg* c) {
+    fsdp_status s;
+    if ((s = check_extent(c->rows, c->cols)) != FSDP_OK || (s = check_dtype(c->dtype, "dtype")) != FSDP_OK)
+        return s;
+    if (!std::isfinite(c->scale) || c->scale <= 0.0f)
+        return fail(FSDP_E_RANGE, "scale must be finite and above 0");
+    return FSDP_OK;
+}
+
+fsdp_status check_top(int64_t cols, int32_t top) {
+    if (top < 0 || top > FSDP_LOGPROB_MAX_TOP || (cols > 0 && top > cols))
+        return fail(FSDP_E_RANGE, "top must be in [0, FSDP_LOGPROB_MAX_TOP], and no more than cols");
+    return FSDP_OK;
+}
+
+// ---- AdamW over many tensors ----
+
+constexpr int64_t kMaxNumel = int64_t{1} << 40;
+
+fsdp_status check_numel(int64_t n) {
+    if (n < 0) return fail(FSDP_E_RANGE, "a tensor's numel is negative");
+    if (n > kMaxNumel) return fail(FSDP_E_OVERFLOW, "a tensor's numel is above 2^40");
+    return FSDP_OK;
+}
+
+// Buffers of a tensor's state; format F32, BF16 or 8BIT.
+fsdp_status check_state(const fsdp_adam_tensor& t, int32_t format) {
+    const size_t e = format == FSDP_STATE_F32 ? 4 : format == FSDP_STATE_BF16 ? 2 : 1;
+    const fsdp_status s = check_buf(t.exp_avg, t.numel, e, "a tensor's exp_avg");
+    return s != FSDP_OK ? s : check_buf(t.exp_avg_sq, t.numel, e, "a tensor's exp_avg_sq");
+}
+
 fsdp::RowsIn in(const fsdp_rows& r) { return {r.data, r.pitch}; }
 fsdp::RowsOut out(const fsdp_rows& r) { return {r.data, r.pitch}; }
 
@@ -429,32 +572,15 @@ fsdp_status fsdp_adam_shard(const fsdp_unit* unit, float* param, const float* gr
         if (!unit) return fail(FSDP_E_ARG, "unit is NULL");
         if (!cfg) return fail(FSDP_E_ARG, "cfg is NULL");
         const fsdp::UnitPlan& u = unit->plan;
-        if (cfg->step < 1) return fail(FSDP_E_RANGE, "step must be >= 1");
-        if (!(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0)) return fail(FSDP_E_RANGE, "beta1 not in [0,1)");
-        if (!(cfg->beta2 >= 0.0 && cfg->beta2 < 1.0)) return fail(FSDP_E_RANGE, "beta2 not in [0,1)");
-        if (!std::isfinite(cfg->lr)) return fail(FSDP_E_RANGE, "lr must be finite");
-        if (!std::isfinite(cfg->eps) || cfg->eps < 0.0)
-            return fail(FSDP_E_RANGE, "eps must be finite and >= 0");
-        if (!std::isfinite(cfg->weight_decay)) return fail(FSDP_E_RANGE, "weight_decay must be finite");
-        fsdp_status s;
+        fsdp::AdamScalars sc;
+        fsdp_status s = adam_scalars(*cfg, &sc);
+        if (s != FSDP_OK) return s;
         if ((s = check_buf(param, u.S, sizeof(float), "param")) != FSDP_OK) return s;
         if ((s = check_buf(grad, u.S, sizeof(float), "grad")) != FSDP_OK) return s;
         if ((s = check_buf(exp_avg, u.S, sizeof(float), "exp_avg")) != FSDP_OK) return s;
         if ((s = check_buf(exp_avg_sq, u.S, sizeof(float), "exp_avg_sq")) != FSDP_OK) return s;
         if (param_bf16 && !aligned_to(param_bf16, sizeof(uint16_t)))
             return fail(FSDP_E_ALIGN, "param_bf16 is not aligned to its element size");
-        // Kingma & Ba's bias corrections and decoupled decay, scalars in double,
-        // each rounded once to float.
-        const double t = static_cast<double>(cfg->step);
-        fsdp::AdamScalars sc;
-        sc.decay = static_cast<float>(1.0 - cfg->lr * cfg->weight_decay);
-        sc.b1 = static_cast<float>(cfg->beta1);
-        sc.omb1 = static_cast<float>(1.0 - cfg->beta1);
-        sc.b2 = static_cast<float>(cfg->beta2);
-        sc.omb2 = static_cast<float>(1.0 - cfg->beta2);
-        sc.step_size = static_cast<float>(cfg->lr / (1.0 - std::pow(cfg->beta1, t)));
-        sc.bc2s = static_cast<float>(std::sqrt(1.0 - std::pow(cfg->beta2, t)));
-        sc.eps = static_cast<float>(cfg->eps);
         if (u.S == 0) return ok();
         const hipError_t e = fsdp::launch_adamw(param, grad, exp_avg, exp_avg_sq, param_bf16, u.S, sc,
                                                 static_cast<hipStream_t>(stream));
@@ -837,6 +963,225 @@ fsdp_status fsdp_act_backward(const fsdp_layer_cfg* cfg, const fsdp_act_bwd* io,
         a.workspace = io->workspace;
         const hipError_t err = fsdp::launch_act_backward(a, static_cast<hipStream_t>(stream));
         return err != hipSuccess ? hip_fail(err, "fsdp_act_backward launch") : ok();
+    });
+}
+
+fsdp_status fsdp_rotary_freqs(int64_t rot, double base, int32_t scaling, double factor, int64_t trained_len,
+                              double low, double high, double* out) {
+    return guarded("fsdp_rotary_freqs", [&]() -> fsdp_status {
+        if (!out) return fail(FSDP_E_ARG, "out is NULL");
+        if (rot < 2 || rot > 1024 || rot % 2) return fail(FSDP_E_RANGE, "rot must be even, in [2, 1024]");
+        if (!std::isfinite(base) || base <= 0.0) return fail(FSDP_E_RANGE, "base must be finite and above 0");
+        if (scaling < FSDP_ROTARY_NONE || scaling > FSDP_ROTARY_PARTS)
+            return fail(FSDP_E_RANGE, "scaling must be an fsdp_rotary_scaling");
+        if (scaling != FSDP_ROTARY_NONE && (!std::isfinite(factor) || factor <= 0.0))
+            return fail(FSDP_E_RANGE, "factor must be finite and above 0");
+        if (scaling == FSDP_ROTARY_NTK && rot == 2)
+            return fail(FSDP_E_RANGE, "FSDP_ROTARY_NTK needs more than one pair");
+        if (scaling == FSDP_ROTARY_PARTS) {
+            if (trained_len < 1) return fail(FSDP_E_RANGE, "trained_len must be at least 1");
+            if (!std::isfinite(low) || !std::isfinite(high) || low >= high)
+                return fail(FSDP_E_RANGE, "low must be below high, both finite");
+        }
+        const double r = static_cast<double>(rot);
+        const double b = scaling == FSDP_ROTARY_NTK ? base * std::pow(factor, r / (r - 2.0)) : base;
+        for (int64_t i = 0; i < rot / 2; ++i) {
+            double f = std::pow(b, -2.0 * static_cast<double>(i) / r);
+            if (scaling == FSDP_ROTARY_LINEAR) f /= factor;
+            if (scaling == FSDP_ROTARY_PARTS) {
+                const double turns = static_cast<double>(trained_len) * f * 0.15915494309189533577;
+                const double k = std::fmin(1.0, std::fmax(0.0, (turns - low) / (high - low)));
+                f = f * k + f / factor * (1.0 - k);
+            }
+            out[i] = f;
+        }
+        return ok();
+    });
+}
+
+fsdp_status fsdp_rotary_forward(const fsdp_rotary_cfg* cfg, const fsdp_rotary_io* io, void* stream) {
+    return guarded("fsdp_rotary_forward", [&]() -> fsdp_status {
+        return rotary_impl(cfg, io, 1.0f, "fsdp_rotary_forward", stream);
+    });
+}
+
+fsdp_status fsdp_rotary_backward(const fsdp_rotary_cfg* cfg, const fsdp_rotary_io* io, void* stream) {
+    return guarded("fsdp_rotary_backward", [&]() -> fsdp_status {
+        return rotary_impl(cfg, io, -1.0f, "fsdp_rotary_backward", stream);
+    });
+}
+
+fsdp_status fsdp_logprob_workspace(int64_t rows, int64_t cols, int32_t top, int64_t* n_floats) {
+    return guarded("fsdp_logprob_workspace", [&]() -> fsdp_status {
+        if (!n_floats) return fail(FSDP_E_ARG, "n_floats is NULL");
+        fsdp_status s;
+        if ((s = check_extent(rows, cols)) != FSDP_OK || (s = check_top(cols, top)) != FSDP_OK) return s;
+        const int64_t n = fsdp::logprob_workspace_floats(rows, cols, top);
+        if (n < 0) return fail(FSDP_E_OVERFLOW, "the workspace's size overflows int64");
+        *n_floats = n;
+        return ok();
+    });
+}
+
+fsdp_status fsdp_logprob_forward(const fsdp_logprob_cfg* cfg, const fsdp_logprob_fwd* io, void* stream) {
+    return guarded("fsdp_logprob_forward", [&]() -> fsdp_status {
+        if (!cfg || !io) return fail(FSDP_E_ARG, cfg ? "io is NULL" : "cfg is NULL");
+        const int64_t R = cfg->rows, C = cfg->cols;
+        fsdp_status s;
+        if ((s = check_logprob(cfg)) != FSDP_OK || (s = check_top(C, cfg->top)) != FSDP_OK) return s;
+        if (R == 0 || C == 0) return ok();
+        if ((io->tokens != nullptr) != (io->logprob != nullptr))
+            return fail(FSDP_E_ARG, "tokens and logprob must be given together");
+        const int64_t top = cfg->top;
+        if ((s = check_rows(io->logits.data, io->logits.pitch, R, C, elem_size(cfg->dtype), false, "logits")) != FSDP_OK ||
+            (s = check_buf(io->tokens, io->tokens != nullptr, sizeof(int64_t), "tokens")) != FSDP_OK ||
+            (s = check_buf(io->logprob, io->logprob != nullptr, sizeof(float), "logprob")) != FSDP_OK ||
+            (s = check_buf(io->max, 1, sizeof(float), "max")) != FSDP_OK ||
+            (s = check_buf(io->logsum, 1, sizeof(float), "logsum")) != FSDP_OK ||
+            (s = check_buf(io->entropy, io->entropy != nullptr, sizeof(float), "entropy")) != FSDP_OK ||
+            (s = check_buf(io->top_logprob, top, sizeof(float), "top_logprob")) != FSDP_OK ||
+            (s = check_buf(io->top_token, top, sizeof(int64_t), "top_token")) != FSDP_OK ||
+            (s = check_workspace(io->workspace, io->workspace_len,
+                                 fsdp::logprob_workspace_floats(R, C, cfg->top))) != FSDP_OK)
+            return s;
+        fsdp::LogprobFwd a{};
+        a.rows = R;
+        a.cols = C;
+        a.bf16 = cfg->dtype == FSDP_BF16;
+        a.top = cfg->top;
+        a.scale = cfg->scale;
+        a.x = in(io->logits);
+        a.tokens = io->tokens;
+        a.logprob = io->logprob;
+        a.max = io->max;
+        a.logsum = io->logsum;
+        a.entropy = io->entropy;
+        a.top_logprob = io->top_logprob;
+        a.top_token = io->top_token;
+        a.workspace = io->workspace;
+        const hipError_t err = fsdp::launch_logprob_forward(a, static_cast<hipStream_t>(stream));
+        return err != hipSuccess ? hip_fail(err, "fsdp_logprob_forward launch") : ok();
+    });
+}
+
+fsdp_status fsdp_logprob_backward(const fsdp_logprob_cfg* cfg, const fsdp_logprob_bwd* io, void* stream) {
+    return guarded("fsdp_logprob_backward", [&]() -> fsdp_status {
+        if (!cfg || !io) return fail(FSDP_E_ARG, cfg ? "io is NULL" : "cfg is NULL");
+        const int64_t R = cfg->rows, C = cfg->cols;
+        fsdp_status s;
+        if ((s = check_logprob(cfg)) != FSDP_OK) return s;
+        if (!io->dlogprob && !io->dentropy) return fail(FSDP_E_ARG, "neither dlogprob nor dentropy is given");
+        if (R == 0 || C == 0) return ok();
+        const size_t e = elem_size(cfg->dtype);
+        if ((s = check_rows(io->logits.data, io->logits.pitch, R, C, e, false, "logits")) != FSDP_OK ||
+            (s = check_rows(io->dlogits.data, io->dlogits.pitch, R, C, e, true, "dlogits")) != FSDP_OK ||
+            (s = check_buf(io->tokens, io->dlogprob != nullptr, sizeof(int64_t), "tokens")) != FSDP_OK ||
+            (s = check_buf(io->dlogprob, io->dlogprob != nullptr, sizeof(float), "dlogprob")) != FSDP_OK ||
+            (s = check_buf(io->dentropy, io->dentropy != nullptr, sizeof(float), "dentropy")) != FSDP_OK ||
+            (s = check_buf(io->max, 1, sizeof(float), "max")) != FSDP_OK ||
+            (s = check_buf(io->logsum, 1, sizeof(float), "logsum")) != FSDP_OK ||
+            (s = check_buf(io->entropy, io->dentropy != nullptr, sizeof(float), "entropy")) != FSDP_OK)
+            return s;
+        fsdp::LogprobBwd a{};
+        a.rows = R;
+        a.cols = C;
+        a.bf16 = cfg->dtype == FSDP_BF16;
+        a.scale = cfg->scale;
+        a.x = in(io->logits);
+        a.dx = out(io->dlogits);
+        a.tokens = io->tokens;
+        a.dl = io->dlogprob;
+        a.dh = io->dentropy;
+        a.max = io->max;
+        a.logsum = io->logsum;
+        a.entropy = io->entropy;
+        const hipError_t err = fsdp::launch_logprob_backward(a, static_cast<hipStream_t>(stream));
+        return err != hipSuccess ? hip_fail(err, "fsdp_logprob_backward launch") : ok();
+    });
+}
+
+fsdp_status fsdp_adam_state_bytes(int64_t numel, int64_t* bytes) {
+    return guarded("fsdp_adam_state_bytes", [&]() -> fsdp_status {
+        if (!bytes) return fail(FSDP_E_ARG, "bytes is NULL");
+        const fsdp_status s = check_numel(numel);
+        if (s != FSDP_OK) return s;
+        *bytes = fsdp::state_scales(numel) + (numel + fsdp::kStateGroup - 1) / fsdp::kStateGroup;
+        return ok();
+    });
+}
+
+fsdp_status fsdp_adam_tensors(const fsdp_adam_list* list, const fsdp_adam_tensor* tensors,
+                              const fsdp_adamw_cfg* groups, void* stream) {
+    return guarded("fsdp_adam_tensors", [&]() -> fsdp_status {
+        if (!list) return fail(FSDP_E_ARG, "list is NULL");
+        if (list->n_tensors < 0) return fail(FSDP_E_RANGE, "n_tensors must not be negative");
+        if (list->state_format != FSDP_STATE_F32 && list->state_format != FSDP_STATE_8BIT)
+            return fail(FSDP_E_RANGE, "state_format must be FSDP_STATE_F32 or FSDP_STATE_8BIT");
+        fsdp_status s;
+        if ((s = check_dtype(list->grad_dtype, "grad_dtype")) != FSDP_OK) return s;
+        if (list->n_groups < 1 || list->n_groups > FSDP_ADAM_MAX_GROUPS)
+            return fail(FSDP_E_RANGE, "n_groups must be in [1, FSDP_ADAM_MAX_GROUPS]");
+        if (!groups) return fail(FSDP_E_ARG, "groups is NULL");
+        if (list->n_tensors > 0 && !tensors) return fail(FSDP_E_ARG, "tensors is NULL");
+        fsdp::AdamScalars sc[FSDP_ADAM_MAX_GROUPS];
+        for (int32_t i = 0; i < list->n_groups; ++i)
+            if ((s = adam_scalars(groups[i], &sc[i])) != FSDP_OK) return s;
+        if ((s = check_buf(list->grad_scale, list->grad_scale != nullptr, sizeof(float), "grad_scale")) != FSDP_OK ||
+            (s = check_buf(list->skip, list->skip != nullptr, sizeof(float), "skip")) != FSDP_OK)
+            return s;
+        const bool state8 = list->state_format == FSDP_STATE_8BIT;
+        std::vector<fsdp::AdamTensor> t;
+        t.reserve(static_cast<size_t>(list->n_tensors));
+        for (int32_t i = 0; i < list->n_tensors; ++i) {
+            const fsdp_adam_tensor& x = tensors[i];
+            if ((s = check_numel(x.numel)) != FSDP_OK) return s;
+            if (x.group < 0 || x.group >= list->n_groups) return fail(FSDP_E_RANGE, "a tensor's group is not in groups");
+            if ((s = check_buf(x.param, x.numel, sizeof(float), "a tensor's param")) != FSDP_OK ||
+                (s = check_buf(x.grad, x.numel, elem_size(list->grad_dtype), "a tensor's grad")) != FSDP_OK ||
+                (s = check_state(x, list->state_format)) != FSDP_OK ||
+                (s = check_buf(x.param_bf16, x.param_bf16 != nullptr, sizeof(uint16_t), "a tensor's param_bf16")) != FSDP_OK)
+                return s;
+            if (x.numel == 0) continue;
+            t.push_back({x.numel, x.param, x.grad, x.exp_avg, x.exp_avg_sq, x.param_bf16,
+                         state8 ? fsdp::adam_key(list->seed, groups[x.group].step, i) : 0, x.group});
+        }
+        const hipError_t e = fsdp::launch_adam_tensors(t, sc, list->n_groups, state8, list->grad_dtype == FSDP_BF16,
+                                                       list->grad_scale, list->skip, static_cast<hipStream_t>(stream));
+        return e != hipSuccess ? hip_fail(e, "fsdp_adam_tensors launch") : ok();
+    });
+}
+
+fsdp_status fsdp_adam_convert(int32_t n_tensors, const fsdp_adam_tensor* from, int32_t from_format,
+                              const fsdp_adam_tensor* to, int32_t to_format, uint64_t seed, int64_t step,
+                              void* stream) {
+    return guarded("fsdp_adam_convert", [&]() -> fsdp_status {
+        if (n_tensors < 0) return fail(FSDP_E_RANGE, "n_tensors must not be negative");
+        const auto known = [](int32_t f) { return f >= FSDP_STATE_F32 && f <= FSDP_STATE_BF16; };
+        if (!known(from_format) || !known(to_format))
+            return fail(FSDP_E_RANGE, "the formats must be FSDP_STATE_F32, FSDP_STATE_8BIT or FSDP_STATE_BF16");
+        if ((from_format == FSDP_STATE_8BIT) == (to_format == FSDP_STATE_8BIT))
+            return fail(FSDP_E_RANGE, "one of the formats, and one only, must be FSDP_STATE_8BIT");
+        if (step < 1) return fail(FSDP_E_RANGE, "step must be >= 1");
+        if (n_tensors > 0 && (!from || !to)) return fail(FSDP_E_ARG, from ? "to is NULL" : "from is NULL");
+        std::vector<fsdp::StateCopy> t;
+        t.reserve(static_cast<size_t>(n_tensors));
+        for (int32_t i = 0; i < n_tensors; ++i) {
+            fsdp_status s;
+            if ((s = check_numel(from[i].numel)) != FSDP_OK) return s;
+            if (from[i].numel != to[i].numel)
+                return fail(FSDP_E_RANGE, "a tensor's numel differs between the lists");
+            if ((s = check_state(from[i], from_format)) != FSDP_OK || (s = check_state(to[i], to_format)) != FSDP_OK)
+                return s;
+            if (from[i].numel == 0) continue;
+            t.push_back({from[i].numel, from[i].exp_avg, from[i].exp_avg_sq, to[i].exp_avg, to[i].exp_avg_sq,
+                         to_format == FSDP_STATE_8BIT ? fsdp::adam_key(seed, step, i) : 0});
+        }
+        const auto state = [](int32_t f) {
+            return f == FSDP_STATE_F32 ? fsdp::State::kF32 : f == FSDP_STATE_BF16 ? fsdp::State::kBF16 : fsdp::State::k8Bit;
+        };
+        const hipError_t e = fsdp::launch_adam_convert(t, state(from_format), state(to_format),
+                                                       static_cast<hipStream_t>(stream));
+        return e != hipSuccess ? hip_fail(e, "fsdp_adam_convert launch") : ok();
     });
 }
 
