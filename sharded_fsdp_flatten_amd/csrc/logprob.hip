@@ -43,6 +43,9 @@ __device__ __forceinline__ float weighted(float e, float u) { return e * fmaxf(u
 struct Row {
     float max, logsum, entropy;
     __device__ bool empty() const { return max == -INFINITY && logsum == 0.0f; }
+    __device__ float logprob(float x, float scale) const {
+        return empty() ? -INFINITY : fmaf(x, scale, -max) - logsum;
+    }
 };
 __device__ __forceinline__ Row finish(const Part& p, float scale) {
     Row r;
@@ -60,90 +63,315 @@ __device__ __forceinline__ float value(const uint16_t* p) {
 }
 __device__ __forceinline__ float value(const float* p) { return *p; }
 
-// A logit's place in the order of alternatives: larger values first, then lower columns; NaN as
-// -infinity.  Larger keys come first; no two are equal; 0 is below every key.
-__device__ __forceinline__ uint64_t rank_key(float x, uint32_t col) {
+// A logit's place in the order of alternatives: larger values first, then lower places; NaN as
+// -infinity.  Larger keys come first; no two of a row are equal; 0 is below every key.
+__device__ __forceinline__ uint32_t rank_bits(float x) {
     x = x == x ? x + 0.0f : -INFINITY;  // -0 as 0
     const uint32_t b = __builtin_bit_cast(uint32_t, x);
-    const uint32_t o = b & 0x80000000u ? ~b : b | 0x80000000u;
-    return static_cast<uint64_t>(o) << 32 | static_cast<uint32_t>(~col);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float ranked_value(uint32_t o) {
+    return __builtin_bit_cast(float, o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+__device__ __forceinline__ uint64_t key_of(uint32_t bits, uint32_t place) {
+    return static_cast<uint64_t>(bits) << 32 | static_cast<uint32_t>(~place);
 }
 
-template <typename T, bool kEntropy>
-__global__ void __launch_bounds__(kThreads) logprob_fwd_kernel(LogprobFwd a, int64_t row0) {
-    __shared__ Part parts[kThreads / 64];
-    __shared__ uint64_t keys[kThreads / 64];
-    const int64_t row = row0 + blockIdx.x;
-    const T* x = static_cast<const T*>(a.x.p) + row * a.x.pitch;
+// ---------------------------------------------------------------------------
+// over a wave
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float wave_max(float x) {
+    const auto bits = [](float a) { return __builtin_bit_cast(uint32_t, a); };
+    const auto val = [](uint32_t a) { return __builtin_bit_cast(float, a); };
+    x = fmaxf(x, val(dpp<kQuadXor1>(bits(x))));
+    x = fmaxf(x, val(dpp<kQuadXor2>(bits(x))));
+    x = fmaxf(x, val(dpp<kHalfMirror>(bits(x))));
+    x = fmaxf(x, val(dpp<kMirror>(bits(x))));
+    const auto r = __builtin_amdgcn_permlane16_swap(bits(x), bits(x), false, false);
+    x = fmaxf(val(r[0]), val(r[1]));
+    const auto t = __builtin_amdgcn_permlane32_swap(bits(x), bits(x), false, false);
+    return fmaxf(val(t[0]), val(t[1]));
+}
+// Join of the wave's lanes, the same in each: moved to the common maximum, then added.  (A product fused
+// into the first addition would round differently in the two lanes that exchange it.)
+__device__ __forceinline__ Part wave_join(Part p, float k) {
+#pragma clang fp contract(off)
+    const float m = wave_max(p.m), d = shift(p.m, m, k), f = __builtin_amdgcn_exp2f(d);
+    return Part{m, wave_sum(p.s * f), wave_sum(f * (p.t + d * p.s))};
+}
+// How many of the wave's keys are larger than the lane's.
+__device__ __forceinline__ int wave_rank(uint64_t key) {
+    int rank = 0;
+    const int hi = static_cast<int>(key >> 32), lo = static_cast<int>(key);
+#pragma unroll 8
+    for (int l = 0; l < 64; ++l) {
+        const uint64_t other = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, l))) << 32 |
+                               static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, l));
+        rank += other > key ? 1 : 0;
+    }
+    return rank;
+}
+// The key of that rank; 0 where the wave has none.
+__device__ __forceinline__ uint64_t key_at(uint64_t key, int rank, int want) {
+    const uint64_t has = __ballot(rank == want && key != 0);
+    if (!has) return 0;
+    const int l = __builtin_ctzll(has);
+    return static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key >> 32), l))) << 32 |
+           static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key), l));
+}
+
+// ---------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------
+// Candidates for the alternatives that a workgroup gathers; more than that go the slow way.
+constexpr int kCandidates = 2560;
+
+// A row in `parts` runs of `per` columns, one workgroup each; with more than one the runs' results meet
+// in the workspace and logprob_join_kernel.
+struct Split {
+    uint32_t parts;
+    int64_t per;
+};
+// What a run leaves in the workspace (then its `top` keys in falling order, 0 where it has fewer).
+constexpr int kPartFloats = 4;
+
+__device__ __forceinline__ float* part_at(const LogprobFwd& a, const Split& sp, int64_t row, uint32_t part) {
+    return a.workspace + (row * sp.parts + part) * (kPartFloats + 2 * a.top);
+}
+
+// Statistics, and the given token's log probability, of a whole row.
+template <typename T>
+__device__ __forceinline__ void put_row(const LogprobFwd& a, int64_t row, const Row& r) {
+    a.max[row] = r.max;
+    a.logsum[row] = r.logsum;
+    if (a.entropy) a.entropy[row] = r.entropy;
+    if (a.tokens) {
+        const int64_t tok = a.tokens[row];
+        float lp = 0.0f;
+        if (tok >= 0 && tok < a.cols)
+            lp = r.logprob(value(static_cast<const T*>(a.x.p) + row * a.x.pitch + tok), a.scale);
+        a.logprob[row] = lp;
+    }
+}
+__device__ __forceinline__ void put_top(const LogprobFwd& a, int64_t row, int i, uint64_t key, const Row& r) {
+    a.top_token[row * a.top + i] = static_cast<uint32_t>(~static_cast<uint32_t>(key));
+    a.top_logprob[row * a.top + i] = r.logprob(ranked_value(static_cast<uint32_t>(key >> 32)), a.scale);
+}
+
+// Lane t of a run takes its head's element t (the head ends at a 16-byte boundary), vectors t, t + kT, ...
+// of 8 columns, and its tail's element t - 8.
+//
+// Alternatives, in the pass over the logits: every lane remembers its largest logit and the first place
+// (vector) that held it.  The k-th largest of these keys bounds the k-th largest logit from below, for they
+// are of different logits; a bound that takes no sorting across waves is the larger of the lowest over the
+// waves of their (k / waves)-th key and the highest of their k-th.  Only lanes whose own key reaches it can
+// hold one of the k: they read their logits again (from the cache) and gather what reaches it, and the
+// place of a candidate is how many are larger.
+template <typename T, int kT, bool kEntropy, bool kTop, bool kNt>
+__global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp, int64_t row0) {
+    constexpr int kW = kT / 64, kU = 4;
+    __shared__ Part parts[kW];
+    __shared__ uint64_t bound[kTop ? 2 * kW : 1];
+    __shared__ uint64_t keys[kTop ? kCandidates : 1];
+    __shared__ uint32_t count;
+    const int64_t row = row0 + blockIdx.x / sp.parts;
+    const uint32_t part = blockIdx.x % sp.parts;
+    const int64_t c0 = part * sp.per;
+    const int64_t n = min(a.cols - c0, sp.per);
+    const T* x = static_cast<const T*>(a.x.p) + row * a.x.pitch + c0;
     const float k = static_cast<float>(a.scale * kLog2e);
+    const int t = threadIdx.x;
+    if (kTop && t == 0) count = 0;
+    const int head = static_cast<int>(min(static_cast<int64_t>((16 - reinterpret_cast<uintptr_t>(x) % 16) % 16 / sizeof(T)), n));
+    const uint32_t nv = static_cast<uint32_t>((n - head) / kV);
+    const int tail = static_cast<int>(n - head - static_cast<int64_t>(nv) * kV);
+    const T* body = x + head;
+
     Part p = {-INFINITY, 0.0f, 0.0f};
-    for (int64_t c = threadIdx.x * kV; c < a.cols; c += kThreads * kV) {
-        const int n = static_cast<int>(min(a.cols - c, int64_t{kV}));
-        Vec<T> t;
-        vload<false>(t, x + c, n);
-        float v[kV];
-        t.get(v);
-        Part q = {-INFINITY, 0.0f, 0.0f};
+    // places, in the columns' order: element t of the head t, vector i of the body i + 8, element j of
+    // the tail nv + 8 + j
+    uint32_t place = t < head ? t : static_cast<uint32_t>(t) < nv ? t + 8u : nv + t;
+    const auto one = [&](float v, uint32_t at) {
+        const float m = fmaxf(p.m, v), d = shift(p.m, m, k), f = __builtin_amdgcn_exp2f(d);
+        const float u = (v - anchor(m)) * k, e = __builtin_amdgcn_exp2f(u);
+        if (kEntropy) p.t = f * (p.t + d * p.s) + weighted(e, u);
+        p.s = p.s * f + e;
+        if (m > p.m) place = at;
+        p.m = m;
+    };
+    if (t < head) one(value(x + t), t);
+    for (uint32_t i = t; i < nv; i += kU * kT) {
+        Vec<T> w[kU];
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            if (j >= n) v[j] = -INFINITY;
-            q.m = fmaxf(q.m, v[j]);
+        for (int j = 0; j < kU; ++j) {
+            // a lane beyond the end reads the last vector again
+            const uint32_t at = min(i + j * kT, nv - 1);
+            w[j].template load<kNt>(body + static_cast<int64_t>(at) * kV);
         }
-        const float r = anchor(q.m);
+        float v[kU][kV], top = p.m;
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            const float u = (v[j] - r) * k, e = __builtin_amdgcn_exp2f(u);
-            q.s += e;
-            if constexpr (kEntropy) q.t += weighted(e, u);
+        for (int j = 0; j < kU; ++j) {
+            w[j].get(v[j]);
+            float g = fmaxf(fmaxf(fmaxf(v[j][0], v[j][1]), fmaxf(v[j][2], v[j][3])), fmaxf(fmaxf(v[j][4], v[j][5]), fmaxf(v[j][6], v[j][7])));
+            if (i + j * kT >= nv) g = -INFINITY;
+            if (kTop && g > top) place = i + j * kT + 8u;
+            top = fmaxf(top, g);
         }
-        p = join(p, q, k);
+        const float d = shift(p.m, top, k), f = __builtin_amdgcn_exp2f(d), r = anchor(top);
+        if (kEntropy) p.t = f * (p.t + d * p.s);
+        p.s *= f;
+        p.m = top;
+#pragma unroll
+        for (int j = 0; j < kU; ++j) {
+            if (i + j * kT >= nv) break;
+#pragma unroll
+            for (int q = 0; q < kV; ++q) {
+                const float u = (v[j][q] - r) * k, e = __builtin_amdgcn_exp2f(u);
+                p.s += e;
+                if (kEntropy) p.t += weighted(e, u);
+            }
+        }
     }
-    // join the lanes, then the waves
-    for (int d = 1; d < 64; d <<= 1) {
-        Part q = {__shfl_xor(p.m, d), __shfl_xor(p.s, d), __shfl_xor(p.t, d)};
-        // both sides of a pair join in the same order
-        p = threadIdx.x & d ? join(q, p, k) : join(p, q, k);
+    if (t >= 8 && t - 8 < tail) one(value(body + static_cast<int64_t>(nv) * kV + (t - 8)), nv + t);
+
+    // the wave's sums, and its bounds on the alternatives
+    const bool any = t < head || static_cast<uint32_t>(t) < nv || (t >= 8 && t - 8 < tail);
+    const uint64_t mine = kTop && any ? key_of(rank_bits(p.m), place) : 0;
+    if constexpr (kTop) {
+        const int rank = wave_rank(mine), share = (a.top + kW - 1) / kW;
+        const uint64_t low = key_at(mine, rank, share - 1), high = key_at(mine, rank, a.top - 1);
+        if ((t & 63) == 0) {
+            bound[t >> 6] = low;
+            bound[kW + (t >> 6)] = high;
+        }
     }
-    if ((threadIdx.x & 63) == 0) parts[threadIdx.x >> 6] = p;
+    p = wave_join(p, k);
+    if ((t & 63) == 0) parts[t >> 6] = p;
     __syncthreads();
     p = parts[0];
-    for (int i = 1; i < kThreads / 64; ++i) p = join(p, parts[i], k);
+#pragma unroll
+    for (int i = 1; i < kW; ++i) p = join(p, parts[i], k);
+    const bool whole = sp.parts == 1;
+    float* ws = whole ? nullptr : part_at(a, sp, row, part);
     const Row r = finish(p, a.scale);
-    const auto logprob = [&](float v) {
-        return r.empty() ? -INFINITY : fmaf(v, a.scale, -r.max) - r.logsum;
-    };
-    if (threadIdx.x == 0) {
-        a.max[row] = r.max;
-        a.logsum[row] = r.logsum;
-        if (a.entropy) a.entropy[row] = r.entropy;
-        if (a.tokens) {
-            const int64_t tok = a.tokens[row];
-            a.logprob[row] = tok >= 0 && tok < a.cols ? logprob(value(x + tok)) : 0.0f;
+    if (t == 0) {
+        if (whole) {
+            put_row<T>(a, row, r);
+        } else {
+            ws[0] = p.m;
+            ws[1] = p.s;
+            ws[2] = p.t;
         }
     }
-    // alternatives one by one: the largest key below the last one
-    uint64_t last = ~uint64_t{0};
-    for (int i = 0; i < a.top; ++i) {
-        uint64_t best = 0;
-        for (int64_t c = threadIdx.x; c < a.cols; c += kThreads) {
-            const uint64_t key = rank_key(value(x + c), static_cast<uint32_t>(c));
-            if (key < last && key > best) best = key;
+    if constexpr (kTop) {
+        uint64_t least = bound[0], most = bound[kW];
+#pragma unroll
+        for (int i = 1; i < kW; ++i) {
+            least = min(least, bound[i]);
+            most = max(most, bound[kW + i]);
         }
-        for (int d = 1; d < 64; d <<= 1) {
-            const uint64_t o = static_cast<uint64_t>(__shfl_xor(static_cast<unsigned long long>(best), d));
-            best = o > best ? o : best;
+        const uint64_t reach = max(least, most);
+        const auto put = [&](int i, uint64_t key) {
+            if (whole) put_top(a, row, i, key, r);
+            else reinterpret_cast<uint64_t*>(ws + kPartFloats)[i] = key;
+        };
+        const auto gather = [&](float v, uint32_t at, int64_t col) {
+            const uint32_t bits = rank_bits(v);
+            if (key_of(bits, at) < reach) return;
+            const uint32_t slot = atomicAdd(&count, 1u);
+            if (slot < kCandidates) keys[slot] = key_of(bits, static_cast<uint32_t>(c0 + col));
+        };
+        if (mine != 0 && mine >= reach) {
+            if (t < head) gather(value(x + t), t, t);
+            for (uint32_t i = t; i < nv; i += kT) {
+                Vec<T> w;
+                w.template load<false>(body + static_cast<int64_t>(i) * kV);
+                float v[kV];
+                w.get(v);
+#pragma unroll
+                for (int q = 0; q < kV; ++q) gather(v[q], i + 8u, head + static_cast<int64_t>(i) * kV + q);
+            }
+            if (t >= 8 && t - 8 < tail) {
+                const int64_t col = head + static_cast<int64_t>(nv) * kV + (t - 8);
+                gather(value(x + col), nv + t, col);
+            }
         }
         __syncthreads();
-        if ((threadIdx.x & 63) == 0) keys[threadIdx.x >> 6] = best;
-        __syncthreads();
-        best = keys[0];
-        for (int w = 1; w < kThreads / 64; ++w) best = keys[w] > best ? keys[w] : best;
-        last = best;
-        if (threadIdx.x == 0) {
-            const int64_t col = static_cast<uint32_t>(~static_cast<uint32_t>(best));
-            a.top_token[row * a.top + i] = col;
-            a.top_logprob[row * a.top + i] = logprob(value(x + col));
+        const uint32_t got = count;
+        if (got <= kCandidates) {
+            for (uint32_t i = t; i < got; i += kT) {
+                const uint64_t key = keys[i];
+                int place_of = 0;
+                for (uint32_t j = 0; j < got; ++j) place_of += keys[j] > key ? 1 : 0;
+                if (place_of < a.top) put(place_of, key);
+            }
+            // a run shorter than the alternatives wanted
+            for (uint32_t i = got + t; i < static_cast<uint32_t>(a.top); i += kT) put(static_cast<int>(i), 0);
+            return;
         }
+        // too many candidates (one lane's columns hold most of the largest logits): one by one, the
+        // largest key below the last one
+        uint64_t last = ~uint64_t{0};
+        for (int i = 0; i < a.top; ++i) {
+            uint64_t best = 0;
+            for (int64_t c = t; c < n; c += kT) {
+                const uint64_t key = key_of(rank_bits(value(x + c)), static_cast<uint32_t>(c0 + c));
+                if (key < last && key > best) best = key;
+            }
+            for (int d = 1; d < 64; d <<= 1) {
+                const uint64_t o = static_cast<uint64_t>(__shfl_xor(static_cast<unsigned long long>(best), d));
+                best = max(best, o);
+            }
+            __syncthreads();
+            if ((t & 63) == 0) keys[t >> 6] = best;
+            __syncthreads();
+            best = keys[0];
+            for (int w = 1; w < kW; ++w) best = max(best, keys[w]);
+            last = best;
+            if (t == 0) put(i, best);
+        }
+    }
+}
+
+// The runs of a row joined, in their order; the alternatives from the runs' own.
+constexpr int kMaxParts = 64;
+template <typename T>
+__global__ void __launch_bounds__(kThreads) logprob_join_kernel(LogprobFwd a, Split sp, int64_t row0) {
+    __shared__ uint64_t keys[kMaxParts * kMaxTop];
+    __shared__ uint32_t count;
+    const int64_t row = row0 + blockIdx.x;
+    const int t = threadIdx.x;
+    const float k = static_cast<float>(a.scale * kLog2e);
+    if (t == 0) count = 0;
+    // every wave joins all of them
+    const int l = t & 63;
+    Part p = {-INFINITY, 0.0f, 0.0f};
+    uint64_t least = 0;
+    if (l < static_cast<int>(sp.parts)) {
+        const float* ws = part_at(a, sp, row, l);
+        p = Part{ws[0], ws[1], ws[2]};
+        // a run's last key: it has that many, all of them at least as large
+        if (a.top) least = reinterpret_cast<const uint64_t*>(ws + kPartFloats)[a.top - 1];
+    }
+    p = wave_join(p, k);
+    const Row r = finish(p, a.scale);
+    if (t == 0) put_row<T>(a, row, r);
+    if (!a.top) return;
+    for (int d = 1; d < 64; d <<= 1)
+        least = max(least, static_cast<uint64_t>(__shfl_xor(static_cast<unsigned long long>(least), d)));
+    __syncthreads();
+    for (uint32_t i = t; i < sp.parts * a.top; i += kThreads) {
+        const uint64_t key = reinterpret_cast<const uint64_t*>(part_at(a, sp, row, i / a.top) + kPartFloats)[i % a.top];
+        if (key == 0 || key < least) continue;
+        keys[atomicAdd(&count, 1u)] = key;
+    }
+    __syncthreads();
+    const uint32_t got = count;
+    for (uint32_t i = t; i < got; i += kThreads) {
+        const uint64_t key = keys[i];
+        int place = 0;
+        for (uint32_t j = 0; j < got; ++j) place += keys[j] > key ? 1 : 0;
+        if (place < a.top) put_top(a, row, place, key, r);
     }
 }
 
@@ -178,24 +406,54 @@ __global__ void __launch_bounds__(kThreads) logprob_bwd_kernel(LogprobBwd a, int
 
 constexpr int64_t kMaxBlocks = int64_t{1} << 22;  // of 256 threads: a grid's threads fit 32 bits
 
-}  // namespace
+// Runs of a row: a few long rows leave most compute units idle, so that they are cut into runs of at
+// least kRun columns.
+constexpr int64_t kRun = 16384, kFill = 256;
+Split plan_split(int64_t rows, int64_t cols) {
+    int64_t parts = std::min<int64_t>({cols / kRun, kFill / std::max<int64_t>(rows, 1), kMaxParts});
+    parts = std::max<int64_t>(parts, 1);
+    const int64_t per = ((cols + parts - 1) / parts + kV - 1) / kV * kV;
+    return {static_cast<uint32_t>((cols + per - 1) / per), per};
+}
 
-int64_t logprob_workspace_floats(int64_t, int64_t, int32_t) { return 0; }
+template <typename T, int kT, bool kNt>
+void forward(const LogprobFwd& a, const Split& sp, int64_t r0, uint32_t blocks, hipStream_t stream) {
+    if (a.entropy) {
+        if (a.top) logprob_fwd_kernel<T, kT, true, true, kNt><<<blocks, kT, 0, stream>>>(a, sp, r0);
+        else logprob_fwd_kernel<T, kT, true, false, kNt><<<blocks, kT, 0, stream>>>(a, sp, r0);
+    } else {
+        if (a.top) logprob_fwd_kernel<T, kT, false, true, kNt><<<blocks, kT, 0, stream>>>(a, sp, r0);
+        else logprob_fwd_kernel<T, kT, false, false, kNt><<<blocks, kT, 0, stream>>>(a, sp, r0);
+    }
+}
 
-hipError_t launch_logprob_forward(const LogprobFwd& a, hipStream_t stream) {
-    for (int64_t r0 = 0; r0 < a.rows; r0 += kMaxBlocks) {
-        const dim3 grid(static_cast<uint32_t>(std::min(a.rows - r0, kMaxBlocks)));
-        if (a.bf16) {
-            if (a.entropy) logprob_fwd_kernel<uint16_t, true><<<grid, kThreads, 0, stream>>>(a, r0);
-            else logprob_fwd_kernel<uint16_t, false><<<grid, kThreads, 0, stream>>>(a, r0);
-        } else {
-            if (a.entropy) logprob_fwd_kernel<float, true><<<grid, kThreads, 0, stream>>>(a, r0);
-            else logprob_fwd_kernel<float, false><<<grid, kThreads, 0, stream>>>(a, r0);
-        }
+template <typename T>
+hipError_t forward_rows(const LogprobFwd& a, hipStream_t stream) {
+    const Split sp = plan_split(a.rows, a.cols);
+    const int64_t most = kMaxBlocks / 4 / sp.parts;   // of up to 1024 threads
+    for (int64_t r0 = 0; r0 < a.rows; r0 += most) {
+        const int64_t rows = std::min(a.rows - r0, most);
+        const uint32_t blocks = static_cast<uint32_t>(rows * sp.parts);
+        if (sp.per <= 2048) forward<T, 64, false>(a, sp, r0, blocks, stream);
+        else if (blocks >= 512) forward<T, 256, false>(a, sp, r0, blocks, stream);
+        else forward<T, 1024, false>(a, sp, r0, blocks, stream);
+        if (sp.parts > 1) logprob_join_kernel<T><<<static_cast<uint32_t>(rows), kThreads, 0, stream>>>(a, sp, r0);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+}  // namespace
+
+int64_t logprob_workspace_floats(int64_t rows, int64_t cols, int32_t top) {
+    if (rows == 0 || cols == 0) return 0;
+    const Split sp = plan_split(rows, cols);
+    return sp.parts == 1 ? 0 : rows * sp.parts * (kPartFloats + 2 * top);
+}
+
+hipError_t launch_logprob_forward(const LogprobFwd& a, hipStream_t stream) {
+    return a.bf16 ? forward_rows<uint16_t>(a, stream) : forward_rows<float>(a, stream);
 }
 
 hipError_t launch_logprob_backward(const LogprobBwd& a, hipStream_t stream) {
