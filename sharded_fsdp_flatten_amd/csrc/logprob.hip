@@ -99,32 +99,47 @@ __device__ __forceinline__ Part wave_join(Part p, float k) {
     const float m = wave_max(p.m), d = shift(p.m, m, k), f = __builtin_amdgcn_exp2f(d);
     return Part{m, wave_sum(p.s * f), wave_sum(f * (p.t + d * p.s))};
 }
-// How many of the wave's keys are larger than the lane's.
-__device__ __forceinline__ int wave_rank(uint64_t key) {
-    int rank = 0;
-    const int hi = static_cast<int>(key >> 32), lo = static_cast<int>(key);
-#pragma unroll 8
-    for (int l = 0; l < 64; ++l) {
-        const uint64_t other = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, l))) << 32 |
-                               static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, l));
-        rank += other > key ? 1 : 0;
-    }
-    return rank;
+// The largest key of each group of kG neighbouring lanes (1, 2 or 4), in all of them.
+template <int kG>
+__device__ __forceinline__ uint64_t group_key(uint64_t key) {
+    const auto swapped = [](uint64_t x, auto ctrl) {
+        return static_cast<uint64_t>(dpp<decltype(ctrl)::value>(static_cast<uint32_t>(x >> 32))) << 32 |
+               dpp<decltype(ctrl)::value>(static_cast<uint32_t>(x));
+    };
+    if constexpr (kG >= 2) key = max(key, swapped(key, std::integral_constant<int, kQuadXor1>{}));
+    if constexpr (kG >= 4) key = max(key, swapped(key, std::integral_constant<int, kQuadXor2>{}));
+    return key;
 }
-// The key of that rank; 0 where the wave has none.
-__device__ __forceinline__ uint64_t key_at(uint64_t key, int rank, int want) {
-    const uint64_t has = __ballot(rank == want && key != 0);
-    if (!has) return 0;
-    const int l = __builtin_ctzll(has);
+__device__ __forceinline__ uint64_t lane_key(uint64_t key, int l) {
     return static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key >> 32), l))) << 32 |
            static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key), l));
+}
+// The key that `want` of the wave's groups' keys are larger than; 0 where there are no more than that.
+template <int kG>
+__device__ __forceinline__ uint64_t wave_key(uint64_t key, int want) {
+    int rank = 0;
+#pragma unroll
+    for (int l = 0; l < 64; l += kG) rank += lane_key(key, l) > key ? 1 : 0;
+    const uint64_t has = __ballot(rank == want && key != 0);
+    return has ? lane_key(key, __builtin_ctzll(has)) : 0;
+}
+// How many of the first n keys are larger; read in pairs, 16 bytes at a time.
+__device__ __forceinline__ int larger(const uint64_t* keys, uint32_t n, uint64_t key) {
+    int place = 0;
+    uint32_t j = 0;
+    for (; j + 8 <= n; j += 8) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) place += keys[j + q] > key ? 1 : 0;
+    }
+    for (; j < n; ++j) place += keys[j] > key ? 1 : 0;
+    return place;
 }
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-// Candidates for the alternatives that a workgroup gathers; more than that go the slow way.
-constexpr int kCandidates = 2560;
+// Candidates for the alternatives that a workgroup gathers; where there are more, the bound is found exactly.
+constexpr int kCandidates = 1024;
 
 // A row in `parts` runs of `per` columns, one workgroup each; with more than one the runs' results meet
 // in the workspace and logprob_join_kernel.
@@ -158,21 +173,75 @@ __device__ __forceinline__ void put_top(const LogprobFwd& a, int64_t row, int i,
     a.top_logprob[row * a.top + i] = r.logprob(ranked_value(static_cast<uint32_t>(key >> 32)), a.scale);
 }
 
+// The k largest keys of a run of n > k logits in `keys` (in any order).  Every pass
+// counts the next eight bits of the keys that begin as the k-th largest does.
+template <typename T, int kT>
+__device__ uint32_t select(const T* x, int64_t n, int64_t c0, int k, uint64_t* keys, uint32_t* count) {
+    uint32_t* const hist = reinterpret_cast<uint32_t*>(keys);
+    const int t = threadIdx.x;
+    uint64_t prefix = 0;
+    uint32_t left = static_cast<uint32_t>(k);   // the wanted key's place among those that begin with prefix
+    for (int bit = 56; bit >= 0; bit -= 8) {
+        for (int i = t; i < 256; i += kT) hist[i] = 0;
+        __syncthreads();
+        for (int64_t c = t; c < n; c += kT) {
+            const uint64_t key = key_of(rank_bits(value(x + c)), static_cast<uint32_t>(c0 + c));
+            if (bit == 56 || key >> (bit + 8) == prefix) atomicAdd(&hist[key >> bit & 255u], 1u);
+        }
+        __syncthreads();
+        // every wave: four digits a lane, the largest digits in the first lane
+        const int l = t & 63;
+        uint32_t each[4], sum = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum += each[q] = hist[255 - 4 * l - q];
+        uint32_t before = sum;
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t o = __shfl_up(before, d);
+            if (l >= d) before += o;
+        }
+        before -= sum;
+        uint32_t digit = 0, rest = 0;
+        bool here = false;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (!here && before < left && left <= before + each[q]) {
+                here = true;
+                digit = 255u - 4u * l - q;
+                rest = left - before;
+            }
+            if (!here) before += each[q];
+        }
+        const int from = __builtin_ctzll(__ballot(here));
+        prefix = prefix << 8 | static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(digit), from));
+        left = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(rest), from));
+        __syncthreads();
+    }
+    if (t == 0) *count = 0;
+    __syncthreads();
+    for (int64_t c = t; c < n; c += kT) {
+        const uint64_t key = key_of(rank_bits(value(x + c)), static_cast<uint32_t>(c0 + c));
+        if (key >= prefix) keys[atomicAdd(count, 1u)] = key;
+    }
+    __syncthreads();
+    return static_cast<uint32_t>(k);
+}
+
 // Lane t of a run takes its head's element t (the head ends at a 16-byte boundary), vectors t, t + kT, ...
 // of 8 columns, and its tail's element t - 8.
 //
 // Alternatives, in the pass over the logits: every lane remembers its largest logit and the first place
 // (vector) that held it.  The k-th largest of these keys bounds the k-th largest logit from below, for they
-// are of different logits; a bound that takes no sorting across waves is the larger of the lowest over the
-// waves of their (k / waves)-th key and the highest of their k-th.  Only lanes whose own key reaches it can
-// hold one of the k: they read their logits again (from the cache) and gather what reaches it, and the
-// place of a candidate is how many are larger.
+// are of different logits; a bound that takes no sorting across waves is the lowest over the waves of their
+// (k / waves)-th key (of groups of lanes, to rank fewer).  Only lanes whose own key reaches it can hold one of
+// the k: they read their logits again (from the cache) and gather what reaches it, and the place of a
+// candidate is how many are larger.  Where too many reach it (rows that allow fewer than k tokens, or whose
+// largest logits meet in one lane) the k-th largest key itself is found, eight bits a pass over the row.
 template <typename T, int kT, bool kEntropy, bool kTop, bool kNt>
 __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp, int64_t row0) {
-    constexpr int kW = kT / 64, kU = 4;
+    constexpr int kW = kT / 64, kU = 4, kG = kT == 64 ? 1 : kT == 256 ? 2 : 4;
     __shared__ Part parts[kW];
-    __shared__ uint64_t bound[kTop ? 2 * kW : 1];
-    __shared__ uint64_t keys[kTop ? kCandidates : 1];
+    __shared__ uint64_t bound[kTop ? kW : 1];
+    __shared__ alignas(16) uint64_t keys[kTop ? kCandidates : 2];
     __shared__ uint32_t count;
     const int64_t row = row0 + blockIdx.x / sp.parts;
     const uint32_t part = blockIdx.x % sp.parts;
@@ -238,12 +307,10 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
     const bool any = t < head || static_cast<uint32_t>(t) < nv || (t >= 8 && t - 8 < tail);
     const uint64_t mine = kTop && any ? key_of(rank_bits(p.m), place) : 0;
     if constexpr (kTop) {
-        const int rank = wave_rank(mine), share = (a.top + kW - 1) / kW;
-        const uint64_t low = key_at(mine, rank, share - 1), high = key_at(mine, rank, a.top - 1);
-        if ((t & 63) == 0) {
-            bound[t >> 6] = low;
-            bound[kW + (t >> 6)] = high;
-        }
+        // the first waves have keys in all of their lanes
+        const int full = max(1, static_cast<int>(min(nv / 64, static_cast<uint32_t>(kW))));
+        const uint64_t low = wave_key<kG>(group_key<kG>(mine), (a.top + full - 1) / full - 1);
+        if ((t & 63) == 0) bound[t >> 6] = (t >> 6) < full ? low : ~uint64_t{0};
     }
     p = wave_join(p, k);
     if ((t & 63) == 0) parts[t >> 6] = p;
@@ -264,13 +331,9 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
         }
     }
     if constexpr (kTop) {
-        uint64_t least = bound[0], most = bound[kW];
+        uint64_t reach = bound[0];
 #pragma unroll
-        for (int i = 1; i < kW; ++i) {
-            least = min(least, bound[i]);
-            most = max(most, bound[kW + i]);
-        }
-        const uint64_t reach = max(least, most);
+        for (int i = 1; i < kW; ++i) reach = min(reach, bound[i]);
         const auto put = [&](int i, uint64_t key) {
             if (whole) put_top(a, row, i, key, r);
             else reinterpret_cast<uint64_t*>(ws + kPartFloats)[i] = key;
@@ -297,39 +360,18 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
             }
         }
         __syncthreads();
-        const uint32_t got = count;
-        if (got <= kCandidates) {
-            for (uint32_t i = t; i < got; i += kT) {
-                const uint64_t key = keys[i];
-                int place_of = 0;
-                for (uint32_t j = 0; j < got; ++j) place_of += keys[j] > key ? 1 : 0;
-                if (place_of < a.top) put(place_of, key);
-            }
-            // a run shorter than the alternatives wanted
-            for (uint32_t i = got + t; i < static_cast<uint32_t>(a.top); i += kT) put(static_cast<int>(i), 0);
-            return;
-        }
-        // too many candidates (one lane's columns hold most of the largest logits): one by one, the
-        // largest key below the last one
-        uint64_t last = ~uint64_t{0};
-        for (int i = 0; i < a.top; ++i) {
-            uint64_t best = 0;
-            for (int64_t c = t; c < n; c += kT) {
-                const uint64_t key = key_of(rank_bits(value(x + c)), static_cast<uint32_t>(c0 + c));
-                if (key < last && key > best) best = key;
-            }
-            for (int d = 1; d < 64; d <<= 1) {
-                const uint64_t o = static_cast<uint64_t>(__shfl_xor(static_cast<unsigned long long>(best), d));
-                best = max(best, o);
-            }
+        uint32_t got = count;
+        if (got > kCandidates) {
             __syncthreads();
-            if ((t & 63) == 0) keys[t >> 6] = best;
-            __syncthreads();
-            best = keys[0];
-            for (int w = 1; w < kW; ++w) best = max(best, keys[w]);
-            last = best;
-            if (t == 0) put(i, best);
+            got = select<T, kT>(x, n, c0, a.top, keys, &count);
         }
+        for (uint32_t i = t; i < got; i += kT) {
+            const uint64_t key = keys[i];
+            const int place_of = larger(keys, got, key);
+            if (place_of < a.top) put(place_of, key);
+        }
+        // a run shorter than the alternatives wanted
+        for (uint32_t i = got + t; i < static_cast<uint32_t>(a.top); i += kT) put(static_cast<int>(i), 0);
     }
 }
 
@@ -337,7 +379,7 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
 constexpr int kMaxParts = 64;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) logprob_join_kernel(LogprobFwd a, Split sp, int64_t row0) {
-    __shared__ uint64_t keys[kMaxParts * kMaxTop];
+    __shared__ alignas(16) uint64_t keys[kMaxParts * kMaxTop];
     __shared__ uint32_t count;
     const int64_t row = row0 + blockIdx.x;
     const int t = threadIdx.x;
@@ -346,19 +388,20 @@ __global__ void __launch_bounds__(kThreads) logprob_join_kernel(LogprobFwd a, Sp
     // every wave joins all of them
     const int l = t & 63;
     Part p = {-INFINITY, 0.0f, 0.0f};
-    uint64_t least = 0;
+    uint64_t least = ~uint64_t{0};
     if (l < static_cast<int>(sp.parts)) {
         const float* ws = part_at(a, sp, row, l);
         p = Part{ws[0], ws[1], ws[2]};
-        // a run's last key: it has that many, all of them at least as large
-        if (a.top) least = reinterpret_cast<const uint64_t*>(ws + kPartFloats)[a.top - 1];
+        // the runs' shares of the alternatives: all runs together have that many at least as large as the
+        // lowest of these
+        if (a.top) least = reinterpret_cast<const uint64_t*>(ws + kPartFloats)[(a.top + sp.parts - 1) / sp.parts - 1];
     }
     p = wave_join(p, k);
     const Row r = finish(p, a.scale);
     if (t == 0) put_row<T>(a, row, r);
     if (!a.top) return;
     for (int d = 1; d < 64; d <<= 1)
-        least = max(least, static_cast<uint64_t>(__shfl_xor(static_cast<unsigned long long>(least), d)));
+        least = min(least, static_cast<uint64_t>(__shfl_xor(static_cast<unsigned long long>(least), d)));
     __syncthreads();
     for (uint32_t i = t; i < sp.parts * a.top; i += kThreads) {
         const uint64_t key = reinterpret_cast<const uint64_t*>(part_at(a, sp, row, i / a.top) + kPartFloats)[i % a.top];
@@ -369,8 +412,7 @@ __global__ void __launch_bounds__(kThreads) logprob_join_kernel(LogprobFwd a, Sp
     const uint32_t got = count;
     for (uint32_t i = t; i < got; i += kThreads) {
         const uint64_t key = keys[i];
-        int place = 0;
-        for (uint32_t j = 0; j < got; ++j) place += keys[j] > key ? 1 : 0;
+        const int place = larger(keys, got, key);
         if (place < a.top) put_top(a, row, place, key, r);
     }
 }
@@ -435,7 +477,7 @@ hipError_t forward_rows(const LogprobFwd& a, hipStream_t stream) {
         const int64_t rows = std::min(a.rows - r0, most);
         const uint32_t blocks = static_cast<uint32_t>(rows * sp.parts);
         if (sp.per <= 2048) forward<T, 64, false>(a, sp, r0, blocks, stream);
-        else if (blocks >= 512) forward<T, 256, false>(a, sp, r0, blocks, stream);
+        else if (blocks >= 512 || sp.per < 16384) forward<T, 256, false>(a, sp, r0, blocks, stream);
         else forward<T, 1024, false>(a, sp, r0, blocks, stream);
         if (sp.parts > 1) logprob_join_kernel<T><<<static_cast<uint32_t>(rows), kThreads, 0, stream>>>(a, sp, r0);
         const hipError_t e = hipGetLastError();
