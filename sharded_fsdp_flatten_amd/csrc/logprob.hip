@@ -6,6 +6,7 @@
 // maximum by one factor.  The lanes' triples join in a fixed order.  Bound by HBM: forward reads every
 // logit once, backward reads and writes each once.
 #include <algorithm>
+#include <type_traits>
 
 #include "layer_dev.h"
 #include "train.h"
@@ -15,19 +16,25 @@ namespace {
 
 constexpr double kLog2e = 1.4426950408889634074, kLn2 = 0.69314718055994530942;
 
-// Running sums of a part of a row, against its largest logit m: s = sum of e, t = sum of e u with
-// u = k (x - m), e = 2^u.  A part without logits above -infinity has m = -infinity, s = t = 0.
+// Running sums of a part of a row with the largest logit m, against r = anchor(m): s = sum of e, t = sum of
+// e u with u = k x - r (one rounding), e = 2^u.  A part without logits above -infinity has m = -infinity,
+// s = t = 0.
 struct Part {
     float m, s, t;
 };
-// Logits are taken against their difference from the maximum, not against k m: masks of the type's
-// lowest value would overflow in the product.  -infinity as a maximum would make NaN of masked logits.
-__device__ __forceinline__ float anchor(float m) { return m == -INFINITY ? 0.0f : m; }
+// k m, rounded, held within 2^24: against it -infinity gives e = 0 instead of NaN.  What its rounding
+// lacks, at most a half, is made up once for a row (finish).  Rows whose k m lies beyond (masks of the
+// type's lowest value and nothing else) are summed again, of differences from the maximum.
+constexpr float kFar = 0x1p24f;
+__device__ __forceinline__ float anchor(float m, float k) { return __builtin_amdgcn_fmed3f(m * k, -kFar, kFar); }
+__device__ __forceinline__ bool overflows(float r) { return fabsf(r) == kFar; }
 
-// How far the exponents of sums against `from` move when they are taken against `to`, the larger one;
-// never so far that 2^shift times a sum's weight could be infinity times 0.
+// How far the exponents of sums against `from`'s anchor move when they are taken against that of `to`, the
+// larger one; never so far that 2^shift times a sum's weight could be infinity times 0.
 __device__ __forceinline__ float shift(float from, float to, float k) {
-    return from == to ? 0.0f : fmaxf((from - to) * k, -1000.0f);
+    if (from == to) return 0.0f;
+    const float r = anchor(to, k);
+    return fmaxf(overflows(r) ? (from - to) * k : anchor(from, k) - r, -1000.0f);
 }
 __device__ __forceinline__ Part join(Part a, Part b, float k) {
     const float m = fmaxf(a.m, b.m);
@@ -47,13 +54,15 @@ struct Row {
         return empty() ? -INFINITY : fmaf(x, scale, -max) - logsum;
     }
 };
-__device__ __forceinline__ Row finish(const Part& p, float scale) {
+__device__ __forceinline__ Row finish(const Part& p, float scale, float k) {
     Row r;
     r.max = p.m * scale;
     if (r.max == -INFINITY && p.s == p.s) return Row{-INFINITY, 0.0f, 0.0f};  // nothing above -infinity
     if (r.max == INFINITY) return Row{INFINITY, NAN, NAN};
-    const float ls = logf(p.s);
-    r.logsum = ls + fmaf(p.m, scale, -r.max);   // of the rounded maximum, so that the two add up
+    const float ls = logf(p.s), a = anchor(p.m, k);
+    const float lacks = overflows(a) ? 0.0f : fmaf(p.m, k, -a);
+    // against the exact k m, and then of the rounded maximum, so that the two add up
+    r.logsum = ls - static_cast<float>(kLn2) * lacks + fmaf(p.m, scale, -r.max);
     r.entropy = ls - static_cast<float>(kLn2) * (p.t / p.s);
     return r;
 }
@@ -262,44 +271,76 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
     uint32_t place = t < head ? t : static_cast<uint32_t>(t) < nv ? t + 8u : nv + t;
     const auto one = [&](float v, uint32_t at) {
         const float m = fmaxf(p.m, v), d = shift(p.m, m, k), f = __builtin_amdgcn_exp2f(d);
-        const float u = (v - anchor(m)) * k, e = __builtin_amdgcn_exp2f(u);
+        const float u = fmaf(v, k, -anchor(m, k)), e = __builtin_amdgcn_exp2f(u);
         if (kEntropy) p.t = f * (p.t + d * p.s) + weighted(e, u);
         p.s = p.s * f + e;
         if (m > p.m) place = at;
         p.m = m;
     };
     if (t < head) one(value(x + t), t);
-    for (uint32_t i = t; i < nv; i += kU * kT) {
-        Vec<T> w[kU];
-#pragma unroll
-        for (int j = 0; j < kU; ++j) {
-            // a lane beyond the end reads the last vector again
-            const uint32_t at = min(i + j * kT, nv - 1);
-            w[j].template load<kNt>(body + static_cast<int64_t>(at) * kV);
-        }
-        float v[kU][kV], top = p.m;
+    const auto load = [&](Vec<T>& w, uint32_t i) {
+        w.template load<kNt>(reinterpret_cast<const T*>(reinterpret_cast<const char*>(body) + i * static_cast<uint32_t>(kV * sizeof(T))));
+    };
+    // kU vectors from place i on (those beyond the end were read from the last one)
+    const auto take = [&](const Vec<T>* w, uint32_t i, auto all) {
+        constexpr bool kAll = decltype(all)::value;
+        float v[kU][kV], g[kU], top = p.m;
 #pragma unroll
         for (int j = 0; j < kU; ++j) {
             w[j].get(v[j]);
-            float g = fmaxf(fmaxf(fmaxf(v[j][0], v[j][1]), fmaxf(v[j][2], v[j][3])), fmaxf(fmaxf(v[j][4], v[j][5]), fmaxf(v[j][6], v[j][7])));
-            if (i + j * kT >= nv) g = -INFINITY;
-            if (kTop && g > top) place = i + j * kT + 8u;
-            top = fmaxf(top, g);
+            // maxima that keep a NaN need no quieting of their operands
+            g[j] = v[j][0];
+#pragma unroll
+            for (int q = 1; q < kV; ++q) g[j] = __builtin_elementwise_maximum(g[j], v[j][q]);
+            if (!kAll && i + j * kT >= nv) g[j] = -INFINITY;
+            top = __builtin_elementwise_maximum(top, g[j]);
         }
-        const float d = shift(p.m, top, k), f = __builtin_amdgcn_exp2f(d), r = anchor(top);
+        if (top != top) {   // and where there is one are taken again without it
+            top = p.m;
+#pragma unroll
+            for (int j = 0; j < kU; ++j) {
+                g[j] = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < kV; ++q) g[j] = fmaxf(g[j], v[j][q]);
+                if (!kAll && i + j * kT >= nv) g[j] = -INFINITY;
+                top = fmaxf(top, g[j]);
+            }
+        }
+        if constexpr (kTop) {
+            float m = p.m;
+#pragma unroll
+            for (int j = 0; j < kU; ++j) {
+                if (g[j] > m) place = i + j * kT + 8u;
+                m = fmaxf(m, g[j]);
+            }
+        }
+        const float r = anchor(top, k), d = fmaxf(anchor(p.m, k) - r, -1000.0f), f = __builtin_amdgcn_exp2f(d);
         if (kEntropy) p.t = f * (p.t + d * p.s);
         p.s *= f;
         p.m = top;
 #pragma unroll
         for (int j = 0; j < kU; ++j) {
-            if (i + j * kT >= nv) break;
+            if (!kAll && i + j * kT >= nv) break;
 #pragma unroll
             for (int q = 0; q < kV; ++q) {
-                const float u = (v[j][q] - r) * k, e = __builtin_amdgcn_exp2f(u);
+                const float u = fmaf(v[j][q], k, -r), e = __builtin_amdgcn_exp2f(u);
                 p.s += e;
                 if (kEntropy) p.t += weighted(e, u);
             }
         }
+    };
+    uint32_t i = t;
+    for (; i + (kU - 1) * kT < nv; i += kU * kT) {
+        Vec<T> w[kU];
+#pragma unroll
+        for (int j = 0; j < kU; ++j) load(w[j], i + j * kT);
+        take(w, i, std::true_type{});
+    }
+    if (i < nv) {
+        Vec<T> w[kU];
+#pragma unroll
+        for (int j = 0; j < kU; ++j) load(w[j], min(i + j * kT, nv - 1));
+        take(w, i, std::false_type{});
     }
     if (t >= 8 && t - 8 < tail) one(value(body + static_cast<int64_t>(nv) * kV + (t - 8)), nv + t);
 
@@ -312,15 +353,32 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
         const uint64_t low = wave_key<kG>(group_key<kG>(mine), (a.top + full - 1) / full - 1);
         if ((t & 63) == 0) bound[t >> 6] = (t >> 6) < full ? low : ~uint64_t{0};
     }
-    p = wave_join(p, k);
-    if ((t & 63) == 0) parts[t >> 6] = p;
-    __syncthreads();
-    p = parts[0];
-#pragma unroll
-    for (int i = 1; i < kW; ++i) p = join(p, parts[i], k);
+    // the lanes' sums, then the waves'
+    const auto meet = [&](Part q) {
+        q = wave_join(q, k);
+        if constexpr (kW > 1) {
+            if ((t & 63) == 0) parts[t >> 6] = q;
+            __syncthreads();
+            q = wave_join((t & 63) < kW ? parts[t & 63] : Part{-INFINITY, 0.0f, 0.0f}, k);
+        } else {
+            __syncthreads();
+        }
+        return q;
+    };
+    p = meet(p);
+    if (p.m > -INFINITY && p.m < INFINITY && overflows(anchor(p.m, k))) {
+        Part q = {p.m, 0.0f, 0.0f};
+        for (int64_t c = t; c < n; c += kT) {
+            const float u = (value(x + c) - p.m) * k, e = __builtin_amdgcn_exp2f(u);
+            q.s += e;
+            q.t += weighted(e, u);
+        }
+        __syncthreads();
+        p = meet(q);
+    }
     const bool whole = sp.parts == 1;
     float* ws = whole ? nullptr : part_at(a, sp, row, part);
-    const Row r = finish(p, a.scale);
+    const Row r = finish(p, a.scale, k);
     if (t == 0) {
         if (whole) {
             put_row<T>(a, row, r);
@@ -397,7 +455,7 @@ __global__ void __launch_bounds__(kThreads) logprob_join_kernel(LogprobFwd a, Sp
         if (a.top) least = reinterpret_cast<const uint64_t*>(ws + kPartFloats)[(a.top + sp.parts - 1) / sp.parts - 1];
     }
     p = wave_join(p, k);
-    const Row r = finish(p, a.scale);
+    const Row r = finish(p, a.scale, k);
     if (t == 0) put_row<T>(a, row, r);
     if (!a.top) return;
     for (int d = 1; d < 64; d <<= 1)
