@@ -72,6 +72,25 @@ __device__ __forceinline__ float value(const uint16_t* p) {
 }
 __device__ __forceinline__ float value(const float* p) { return *p; }
 
+// 16 bytes of logits: neighbouring lanes read neighbouring vectors, so that every load of a wave takes whole
+// lines.
+template <typename T> constexpr int kE = 16 / sizeof(T);
+template <bool kNt>
+__device__ __forceinline__ u4 load16(const void* p) {
+    return kNt ? __builtin_nontemporal_load(static_cast<const u4*>(p)) : *static_cast<const u4*>(p);
+}
+__device__ __forceinline__ void values(u4 w, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __builtin_bit_cast(float, w[j] << 16);
+        v[2 * j + 1] = __builtin_bit_cast(float, w[j] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void values(u4 w, float (&v)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __builtin_bit_cast(float, static_cast<uint32_t>(w[j]));
+}
+
 // A logit's place in the order of alternatives: larger values first, then lower places; NaN as
 // -infinity.  Larger keys come first; no two of a row are equal; 0 is below every key.
 __device__ __forceinline__ uint32_t rank_bits(float x) {
@@ -108,22 +127,20 @@ __device__ __forceinline__ Part wave_join(Part p, float k) {
     const float m = wave_max(p.m), d = shift(p.m, m, k), f = __builtin_amdgcn_exp2f(d);
     return Part{m, wave_sum(p.s * f), wave_sum(f * (p.t + d * p.s))};
 }
-// The largest key of each group of kG neighbouring lanes (1, 2 or 4), in all of them.
-template <int kG>
-__device__ __forceinline__ uint64_t group_key(uint64_t key) {
+// The largest key of the lane's quad.
+__device__ __forceinline__ uint64_t quad_key(uint64_t key) {
     const auto swapped = [](uint64_t x, auto ctrl) {
         return static_cast<uint64_t>(dpp<decltype(ctrl)::value>(static_cast<uint32_t>(x >> 32))) << 32 |
                dpp<decltype(ctrl)::value>(static_cast<uint32_t>(x));
     };
-    if constexpr (kG >= 2) key = max(key, swapped(key, std::integral_constant<int, kQuadXor1>{}));
-    if constexpr (kG >= 4) key = max(key, swapped(key, std::integral_constant<int, kQuadXor2>{}));
-    return key;
+    key = max(key, swapped(key, std::integral_constant<int, kQuadXor1>{}));
+    return max(key, swapped(key, std::integral_constant<int, kQuadXor2>{}));
 }
 __device__ __forceinline__ uint64_t lane_key(uint64_t key, int l) {
     return static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key >> 32), l))) << 32 |
            static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key), l));
 }
-// The key that `want` of the wave's groups' keys are larger than; 0 where there are no more than that.
+// The key that `want` of the wave's keys are larger than, of every kG-th lane; 0 where there are no more.
 template <int kG>
 __device__ __forceinline__ uint64_t wave_key(uint64_t key, int want) {
     int rank = 0;
@@ -149,6 +166,7 @@ __device__ __forceinline__ int larger(const uint64_t* keys, uint32_t n, uint64_t
 // ---------------------------------------------------------------------------
 // Candidates for the alternatives that a workgroup gathers; where there are more, the bound is found exactly.
 constexpr int kCandidates = 1024;
+constexpr uint32_t kSegments = 2048;   // of a run; longer ones have larger segments
 
 // A row in `parts` runs of `per` columns, one workgroup each; with more than one the runs' results meet
 // in the workspace and logprob_join_kernel.
@@ -236,22 +254,28 @@ __device__ uint32_t select(const T* x, int64_t n, int64_t c0, int k, uint64_t* k
 }
 
 // Lane t of a run takes its head's element t (the head ends at a 16-byte boundary), vectors t, t + kT, ...
-// of 8 columns, and its tail's element t - 8.
+// of 16 bytes, and its tail's element t - 8.
 //
-// Alternatives, in the pass over the logits: every lane remembers its largest logit and the first place
-// (vector) that held it.  The k-th largest of these keys bounds the k-th largest logit from below, for they
-// are of different logits; a bound that takes no sorting across waves is the lowest over the waves of their
-// (k / waves)-th key (of groups of lanes, to rank fewer).  Only lanes whose own key reaches it can hold one of
-// the k: they read their logits again (from the cache) and gather what reaches it, and the place of a
-// candidate is how many are larger.  Where too many reach it (rows that allow fewer than k tokens, or whose
-// largest logits meet in one lane) the k-th largest key itself is found, eight bits a pass over the row.
+// Alternatives: the pass over the logits also leaves the largest logit of every segment in LDS (kSeg
+// neighbouring lanes' vectors, 128 bytes; one vector in short rows).  The k-th largest of them, with the lower
+// segment first among equals, bounds the k-th largest logit from below, for they are different logits, and
+// only the k best segments can hold one of the k.  A bound that takes no sorting across waves is the lowest over
+// the waves of the (k / waves)-th best of their lanes' segments (of quads', where enough are left).  The
+// segments that reach it are read again, all at once, what reaches it is gathered, and the place of a candidate is
+// how many are larger.  Where too many reach it (rows that allow fewer than k tokens, rows whose largest
+// logits meet in a few segments) the k-th largest key itself is found, eight bits a pass over the row.
+// Measured, top 20 with entropy of 2048 x 50257 fp32: lanes that read all of their own logits again 107 us (they
+// are 16 bytes in every 4 KB: as many lines as the row has), segments 78.
 template <typename T, int kT, bool kEntropy, bool kTop, bool kNt>
 __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp, int64_t row0) {
-    constexpr int kW = kT / 64, kU = 4, kG = kT == 64 ? 1 : kT == 256 ? 2 : 4;
+    constexpr int kW = kT / 64, kV = kE<T>, kU = 32 / kV;
+    constexpr uint32_t kSeg = kT == 64 ? 1 : 8;
     __shared__ Part parts[kW];
     __shared__ uint64_t bound[kTop ? kW : 1];
     __shared__ alignas(16) uint64_t keys[kTop ? kCandidates : 2];
-    __shared__ uint32_t count;
+    __shared__ uint32_t segs[kTop ? kSegments : 1];      // rank_bits of the segments' largest
+    __shared__ uint16_t chosen[kTop ? kCandidates : 1];  // segments that reach the bound
+    __shared__ uint32_t count, picked;
     const int64_t row = row0 + blockIdx.x / sp.parts;
     const uint32_t part = blockIdx.x % sp.parts;
     const int64_t c0 = part * sp.per;
@@ -259,35 +283,36 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
     const T* x = static_cast<const T*>(a.x.p) + row * a.x.pitch + c0;
     const float k = static_cast<float>(a.scale * kLog2e);
     const int t = threadIdx.x;
-    if (kTop && t == 0) count = 0;
     const int head = static_cast<int>(min(static_cast<int64_t>((16 - reinterpret_cast<uintptr_t>(x) % 16) % 16 / sizeof(T)), n));
     const uint32_t nv = static_cast<uint32_t>((n - head) / kV);
     const int tail = static_cast<int>(n - head - static_cast<int64_t>(nv) * kV);
     const T* body = x + head;
 
     Part p = {-INFINITY, 0.0f, 0.0f};
-    // places, in the columns' order: element t of the head t, vector i of the body i + 8, element j of
-    // the tail nv + 8 + j
-    uint32_t place = t < head ? t : static_cast<uint32_t>(t) < nv ? t + 8u : nv + t;
-    const auto one = [&](float v, uint32_t at) {
+    // segments of kSeg << wide vectors
+    const uint32_t all = (nv + kSeg - 1) / kSeg;
+    const int wide = kTop && all > kSegments ? 32 - __builtin_clz((all - 1) / kSegments) : 0;
+    if constexpr (kTop) {
+        if (t == 0) count = picked = 0;
+        for (uint32_t i = t; i < min(all, kSegments); i += kT) segs[i] = 0;
+        __syncthreads();
+    }
+    const auto one = [&](float v) {
         const float m = fmaxf(p.m, v), d = shift(p.m, m, k), f = __builtin_amdgcn_exp2f(d);
         const float u = fmaf(v, k, -anchor(m, k)), e = __builtin_amdgcn_exp2f(u);
         if (kEntropy) p.t = f * (p.t + d * p.s) + weighted(e, u);
         p.s = p.s * f + e;
-        if (m > p.m) place = at;
         p.m = m;
     };
-    if (t < head) one(value(x + t), t);
-    const auto load = [&](Vec<T>& w, uint32_t i) {
-        w.template load<kNt>(reinterpret_cast<const T*>(reinterpret_cast<const char*>(body) + i * static_cast<uint32_t>(kV * sizeof(T))));
-    };
+    if (t < head) one(value(x + t));
+    const auto load = [&](uint32_t i) { return load16<kNt>(reinterpret_cast<const char*>(body) + i * 16u); };
     // kU vectors from place i on (those beyond the end were read from the last one)
-    const auto take = [&](const Vec<T>* w, uint32_t i, auto all) {
+    const auto take = [&](const u4* w, uint32_t i, auto all) {
         constexpr bool kAll = decltype(all)::value;
         float v[kU][kV], g[kU], top = p.m;
 #pragma unroll
         for (int j = 0; j < kU; ++j) {
-            w[j].get(v[j]);
+            values(w[j], v[j]);
             // maxima that keep a NaN need no quieting of their operands
             g[j] = v[j][0];
 #pragma unroll
@@ -307,11 +332,17 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
             }
         }
         if constexpr (kTop) {
-            float m = p.m;
 #pragma unroll
             for (int j = 0; j < kU; ++j) {
-                if (g[j] > m) place = i + j * kT + 8u;
-                m = fmaxf(m, g[j]);
+                uint32_t b = __builtin_bit_cast(uint32_t, g[j] + 0.0f);
+                b ^= static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u;   // as rank_bits; no NaN is left
+                if constexpr (kSeg == 8) {
+                    b = max(b, dpp<kQuadXor1>(b));
+                    b = max(b, dpp<kQuadXor2>(b));
+                    b = max(b, dpp<kHalfMirror>(b));
+                }
+                // a segment's first lane has it; lanes beyond the end hold -infinity
+                if (t % kSeg == 0 && (kAll || i + j * kT < nv)) atomicMax(&segs[(i + j * kT) / kSeg >> wide], b);
             }
         }
         const float r = anchor(top, k), d = fmaxf(anchor(p.m, k) - r, -1000.0f), f = __builtin_amdgcn_exp2f(d);
@@ -331,28 +362,19 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
     };
     uint32_t i = t;
     for (; i + (kU - 1) * kT < nv; i += kU * kT) {
-        Vec<T> w[kU];
+        u4 w[kU];
 #pragma unroll
-        for (int j = 0; j < kU; ++j) load(w[j], i + j * kT);
+        for (int j = 0; j < kU; ++j) w[j] = load(i + j * kT);
         take(w, i, std::true_type{});
     }
     if (i < nv) {
-        Vec<T> w[kU];
+        u4 w[kU];
 #pragma unroll
-        for (int j = 0; j < kU; ++j) load(w[j], min(i + j * kT, nv - 1));
+        for (int j = 0; j < kU; ++j) w[j] = load(min(i + j * kT, nv - 1));
         take(w, i, std::false_type{});
     }
-    if (t >= 8 && t - 8 < tail) one(value(body + static_cast<int64_t>(nv) * kV + (t - 8)), nv + t);
+    if (t >= 8 && t - 8 < tail) one(value(body + static_cast<int64_t>(nv) * kV + (t - 8)));
 
-    // the wave's sums, and its bounds on the alternatives
-    const bool any = t < head || static_cast<uint32_t>(t) < nv || (t >= 8 && t - 8 < tail);
-    const uint64_t mine = kTop && any ? key_of(rank_bits(p.m), place) : 0;
-    if constexpr (kTop) {
-        // the first waves have keys in all of their lanes
-        const int full = max(1, static_cast<int>(min(nv / 64, static_cast<uint32_t>(kW))));
-        const uint64_t low = wave_key<kG>(group_key<kG>(mine), (a.top + full - 1) / full - 1);
-        if ((t & 63) == 0) bound[t >> 6] = (t >> 6) < full ? low : ~uint64_t{0};
-    }
     // the lanes' sums, then the waves'
     const auto meet = [&](Part q) {
         q = wave_join(q, k);
@@ -389,33 +411,71 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
         }
     }
     if constexpr (kTop) {
+        // (the sums' meeting was a barrier: the segments are complete)
+        const uint32_t n_segs = nv ? ((all - 1) >> wide) + 1 : 0;
+        uint64_t best = 0;
+        for (uint32_t i = t; i < n_segs; i += kT) best = max(best, key_of(segs[i], i));
+        // the first waves have a segment in each of their lanes
+        const int full = max(1, static_cast<int>(min(n_segs / 64, static_cast<uint32_t>(kW))));
+        const int share = (a.top + full - 1) / full - 1;
+        uint64_t low = ~uint64_t{0};
+        // ranks of quads where four times the alternatives are left of them, else of lanes
+        if ((t >> 6) < full)
+            low = 4 * a.top <= 16 * full ? wave_key<4>(quad_key(best), share) : wave_key<1>(best, share);
+        if ((t & 63) == 0) bound[t >> 6] = low;
+        __syncthreads();
         uint64_t reach = bound[0];
 #pragma unroll
         for (int i = 1; i < kW; ++i) reach = min(reach, bound[i]);
+        for (uint32_t i = t; i < n_segs; i += kT) {
+            if (key_of(segs[i], i) < reach) continue;
+            const uint32_t slot = atomicAdd(&picked, 1u);
+            if (slot < kCandidates) chosen[slot] = static_cast<uint16_t>(i);
+        }
+        __syncthreads();
         const auto put = [&](int i, uint64_t key) {
             if (whole) put_top(a, row, i, key, r);
             else reinterpret_cast<uint64_t*>(ws + kPartFloats)[i] = key;
         };
-        const auto gather = [&](float v, uint32_t at, int64_t col) {
+        // against the bound a logit counts as if it had its segment's place
+        const auto gather = [&](float v, uint32_t seg, int64_t col) {
             const uint32_t bits = rank_bits(v);
-            if (key_of(bits, at) < reach) return;
+            if (key_of(bits, seg) < reach) return;
             const uint32_t slot = atomicAdd(&count, 1u);
             if (slot < kCandidates) keys[slot] = key_of(bits, static_cast<uint32_t>(c0 + col));
         };
-        if (mine != 0 && mine >= reach) {
-            if (t < head) gather(value(x + t), t, t);
-            for (uint32_t i = t; i < nv; i += kT) {
-                Vec<T> w;
-                w.template load<false>(body + static_cast<int64_t>(i) * kV);
-                float v[kV];
-                w.get(v);
+        const uint32_t taken = picked;
+        if (taken <= kCandidates) {
+            const int vecs = __builtin_ctz(kSeg) + wide;
+            const uint32_t work = taken << vecs;
+            constexpr int kA = 4;   // read at once
+            for (uint32_t i = t; i < work; i += kA * kT) {
+                u4 w[kA];
+                uint32_t at[kA], seg[kA];
 #pragma unroll
-                for (int q = 0; q < kV; ++q) gather(v[q], i + 8u, head + static_cast<int64_t>(i) * kV + q);
+                for (int j = 0; j < kA; ++j) {
+                    const uint32_t item = min(i + j * kT, work - 1);
+                    seg[j] = chosen[item >> vecs];
+                    at[j] = (seg[j] << vecs) + (item & ((1u << vecs) - 1));
+                    w[j] = load16<false>(reinterpret_cast<const char*>(body) + min(at[j], nv - 1) * 16u);
+                }
+#pragma unroll
+                for (int j = 0; j < kA; ++j) {
+                    if (i + j * kT >= work || at[j] >= nv) continue;
+                    float v[kV];
+                    values(w[j], v);
+#pragma unroll
+                    for (int q = 0; q < kV; ++q) gather(v[q], seg[j], head + static_cast<int64_t>(at[j]) * kV + q);
+                }
             }
+            // the head comes before every segment, the tail behind all of them
+            if (t < head) gather(value(x + t), 0u, t);
             if (t >= 8 && t - 8 < tail) {
                 const int64_t col = head + static_cast<int64_t>(nv) * kV + (t - 8);
-                gather(value(x + col), nv + t, col);
+                gather(value(x + col), n_segs, col);
             }
+        } else if (t == 0) {
+            count = kCandidates + 1;
         }
         __syncthreads();
         uint32_t got = count;
@@ -531,11 +591,15 @@ template <typename T>
 hipError_t forward_rows(const LogprobFwd& a, hipStream_t stream) {
     const Split sp = plan_split(a.rows, a.cols);
     const int64_t most = kMaxBlocks / 4 / sp.parts;   // of up to 1024 threads
+    // Past the cache where a call's logits outgrow it, rows at any element: 4096 x 50257 bf16 (412 MB) cached 75.0,
+    // nt 68.4 us; 2048 x 50257 fp32 72.1 and 66.7.
+    const bool nt = a.rows * a.cols * static_cast<int64_t>(sizeof(T)) >= kNtBytes;
     for (int64_t r0 = 0; r0 < a.rows; r0 += most) {
         const int64_t rows = std::min(a.rows - r0, most);
         const uint32_t blocks = static_cast<uint32_t>(rows * sp.parts);
         if (sp.per <= 2048) forward<T, 64, false>(a, sp, r0, blocks, stream);
-        else if (blocks >= 512 || sp.per < 16384) forward<T, 256, false>(a, sp, r0, blocks, stream);
+        else if (blocks >= 512 || sp.per < 16384)
+            nt ? forward<T, 256, true>(a, sp, r0, blocks, stream) : forward<T, 256, false>(a, sp, r0, blocks, stream);
         else forward<T, 1024, false>(a, sp, r0, blocks, stream);
         if (sp.parts > 1) logprob_join_kernel<T><<<static_cast<uint32_t>(rows), kThreads, 0, stream>>>(a, sp, r0);
         const hipError_t e = hipGetLastError();
