@@ -91,6 +91,26 @@ __device__ __forceinline__ void values(u4 w, float (&v)[4]) {
     for (int j = 0; j < 4; ++j) v[j] = __builtin_bit_cast(float, static_cast<uint32_t>(w[j]));
 }
 
+__device__ __forceinline__ u4 packed(const float (&v)[8]) {
+    u4 w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v[2 * j], v[2 * j + 1]}), bf2));
+    return w;
+}
+__device__ __forceinline__ u4 packed(const float (&v)[4]) {
+    u4 w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __builtin_bit_cast(uint32_t, v[j]);
+    return w;
+}
+// stores at any element
+__device__ __forceinline__ void put16(void* p, u4 w) { __builtin_nontemporal_store(w, static_cast<u4e*>(p)); }
+__device__ __forceinline__ void put1(uint16_t* p, float v) {
+    *p = static_cast<uint16_t>(__builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v, 0.0f}), bf2)));
+}
+__device__ __forceinline__ void put1(float* p, float v) { *p = v; }
+
 // A logit's place in the order of alternatives: larger values first, then lower places; NaN as
 // -infinity.  Larger keys come first; no two of a row are equal; 0 is below every key.
 __device__ __forceinline__ uint32_t rank_bits(float x) {
@@ -164,9 +184,13 @@ __device__ __forceinline__ int larger(const uint64_t* keys, uint32_t n, uint64_t
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-// Candidates for the alternatives that a workgroup gathers; where there are more, the bound is found exactly.
-constexpr int kCandidates = 1024;
-constexpr uint32_t kSegments = 2048;   // of a run; longer ones have larger segments
+// Candidates for the alternatives that a workgroup of kT threads gathers (where there are more, the bound is
+// found exactly), and the segments of its run (longer ones have larger segments).  A wave's own rows, of
+// kShort columns at most, hold less, so that a compute unit holds more of them: top 20 of 16384 x 500 bf16 XX us, 47.0
+// with as much as the others.
+constexpr int64_t kShort = 4096;
+template <int kT> constexpr int kCandidates = kT == 64 ? 512 : 1024;
+template <typename T, int kT> constexpr uint32_t kSegments = kT == 64 ? kShort / kE<T> : 2048;
 
 // A row in `parts` runs of `per` columns, one workgroup each; with more than one the runs' results meet
 // in the workspace and logprob_join_kernel.
@@ -269,12 +293,13 @@ __device__ uint32_t select(const T* x, int64_t n, int64_t c0, int k, uint64_t* k
 template <typename T, int kT, bool kEntropy, bool kTop, bool kNt>
 __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp, int64_t row0) {
     constexpr int kW = kT / 64, kV = kE<T>, kU = 32 / kV;
-    constexpr uint32_t kSeg = kT == 64 ? 1 : 8;
+    constexpr uint32_t kSeg = kT == 64 ? 1 : 8, kAll = kSegments<T, kT>;
+    constexpr int kMost = kCandidates<kT>;
     __shared__ Part parts[kW];
     __shared__ uint64_t bound[kTop ? kW : 1];
-    __shared__ alignas(16) uint64_t keys[kTop ? kCandidates : 2];
-    __shared__ uint32_t segs[kTop ? kSegments : 1];      // rank_bits of the segments' largest
-    __shared__ uint16_t chosen[kTop ? kCandidates : 1];  // segments that reach the bound
+    __shared__ alignas(16) uint64_t keys[kTop ? kMost : 2];
+    __shared__ uint32_t segs[kTop ? kAll : 1];      // rank_bits of the segments' largest
+    __shared__ uint16_t chosen[kTop ? kMost : 1];  // segments that reach the bound
     __shared__ uint32_t count, picked;
     const int64_t row = row0 + blockIdx.x / sp.parts;
     const uint32_t part = blockIdx.x % sp.parts;
@@ -291,10 +316,10 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
     Part p = {-INFINITY, 0.0f, 0.0f};
     // segments of kSeg << wide vectors
     const uint32_t all = (nv + kSeg - 1) / kSeg;
-    const int wide = kTop && all > kSegments ? 32 - __builtin_clz((all - 1) / kSegments) : 0;
+    const int wide = kTop && all > kAll ? 32 - __builtin_clz((all - 1) / kAll) : 0;
     if constexpr (kTop) {
         if (t == 0) count = picked = 0;
-        for (uint32_t i = t; i < min(all, kSegments); i += kT) segs[i] = 0;
+        for (uint32_t i = t; i < min(all, kAll); i += kT) segs[i] = 0;
         __syncthreads();
     }
     const auto one = [&](float v) {
@@ -307,8 +332,8 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
     if (t < head) one(value(x + t));
     const auto load = [&](uint32_t i) { return load16<kNt>(reinterpret_cast<const char*>(body) + i * 16u); };
     // kU vectors from place i on (those beyond the end were read from the last one)
-    const auto take = [&](const u4* w, uint32_t i, auto all) {
-        constexpr bool kAll = decltype(all)::value;
+    const auto take = [&](const u4* w, uint32_t i, auto full) {
+        constexpr bool kWhole = decltype(full)::value;
         float v[kU][kV], g[kU], top = p.m;
 #pragma unroll
         for (int j = 0; j < kU; ++j) {
@@ -317,7 +342,7 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
             g[j] = v[j][0];
 #pragma unroll
             for (int q = 1; q < kV; ++q) g[j] = __builtin_elementwise_maximum(g[j], v[j][q]);
-            if (!kAll && i + j * kT >= nv) g[j] = -INFINITY;
+            if (!kWhole && i + j * kT >= nv) g[j] = -INFINITY;
             top = __builtin_elementwise_maximum(top, g[j]);
         }
         if (top != top) {   // and where there is one are taken again without it
@@ -327,7 +352,7 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
                 g[j] = -INFINITY;
 #pragma unroll
                 for (int q = 0; q < kV; ++q) g[j] = fmaxf(g[j], v[j][q]);
-                if (!kAll && i + j * kT >= nv) g[j] = -INFINITY;
+                if (!kWhole && i + j * kT >= nv) g[j] = -INFINITY;
                 top = fmaxf(top, g[j]);
             }
         }
@@ -342,7 +367,7 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
                     b = max(b, dpp<kHalfMirror>(b));
                 }
                 // a segment's first lane has it; lanes beyond the end hold -infinity
-                if (t % kSeg == 0 && (kAll || i + j * kT < nv)) atomicMax(&segs[(i + j * kT) / kSeg >> wide], b);
+                if (t % kSeg == 0 && (kWhole || i + j * kT < nv)) atomicMax(&segs[(i + j * kT) / kSeg >> wide], b);
             }
         }
         const float r = anchor(top, k), d = fmaxf(anchor(p.m, k) - r, -1000.0f), f = __builtin_amdgcn_exp2f(d);
@@ -351,7 +376,7 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
         p.m = top;
 #pragma unroll
         for (int j = 0; j < kU; ++j) {
-            if (!kAll && i + j * kT >= nv) break;
+            if (!kWhole && i + j * kT >= nv) break;
 #pragma unroll
             for (int q = 0; q < kV; ++q) {
                 const float u = fmaf(v[j][q], k, -r), e = __builtin_amdgcn_exp2f(u);
@@ -360,14 +385,16 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
             }
         }
     };
+    // a segment's lanes go together, so that its maximum meets
+    constexpr uint32_t kLast = kTop ? kSeg - 1 : 0;
     uint32_t i = t;
-    for (; i + (kU - 1) * kT < nv; i += kU * kT) {
+    for (; (i | kLast) + (kU - 1) * kT < nv; i += kU * kT) {
         u4 w[kU];
 #pragma unroll
         for (int j = 0; j < kU; ++j) w[j] = load(i + j * kT);
         take(w, i, std::true_type{});
     }
-    if (i < nv) {
+    if ((i & ~kLast) < nv) {
         u4 w[kU];
 #pragma unroll
         for (int j = 0; j < kU; ++j) w[j] = load(min(i + j * kT, nv - 1));
@@ -430,7 +457,7 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
         for (uint32_t i = t; i < n_segs; i += kT) {
             if (key_of(segs[i], i) < reach) continue;
             const uint32_t slot = atomicAdd(&picked, 1u);
-            if (slot < kCandidates) chosen[slot] = static_cast<uint16_t>(i);
+            if (slot < kMost) chosen[slot] = static_cast<uint16_t>(i);
         }
         __syncthreads();
         const auto put = [&](int i, uint64_t key) {
@@ -442,10 +469,10 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
             const uint32_t bits = rank_bits(v);
             if (key_of(bits, seg) < reach) return;
             const uint32_t slot = atomicAdd(&count, 1u);
-            if (slot < kCandidates) keys[slot] = key_of(bits, static_cast<uint32_t>(c0 + col));
+            if (slot < kMost) keys[slot] = key_of(bits, static_cast<uint32_t>(c0 + col));
         };
         const uint32_t taken = picked;
-        if (taken <= kCandidates) {
+        if (taken <= kMost) {
             const int vecs = __builtin_ctz(kSeg) + wide;
             const uint32_t work = taken << vecs;
             constexpr int kA = 4;   // read at once
@@ -475,11 +502,11 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
                 gather(value(x + col), n_segs, col);
             }
         } else if (t == 0) {
-            count = kCandidates + 1;
+            count = kMost + 1;
         }
         __syncthreads();
         uint32_t got = count;
-        if (got > kCandidates) {
+        if (got > kMost) {
             __syncthreads();
             got = select<T, kT>(x, n, c0, a.top, keys, &count);
         }
@@ -535,40 +562,86 @@ __global__ void __launch_bounds__(kThreads) logprob_join_kernel(LogprobFwd a, Sp
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) logprob_bwd_kernel(LogprobBwd a, int64_t row0, uint32_t across) {
-    const int64_t row = row0 + blockIdx.x / across;
-    const int64_t c = (static_cast<int64_t>(blockIdx.x % across) * kThreads + threadIdx.x) * kV;
-    const int n = static_cast<int>(max(min(a.cols - c, int64_t{kV}), int64_t{0}));
+// ---------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------
+// One shot: a workgroup takes kBwdVecs vectors a thread of one row (a wave a row where rows are short),
+// aligned as the logits are; block 0 of a row also takes its head and its tail.  A lane stores what it has read,
+// so that the gradient may take the logits' place.
+constexpr int kBwdVecs = 4;
+template <typename T, int kT, bool kEntropy, bool kNt>
+__global__ void __launch_bounds__(kThreads) logprob_bwd_kernel(LogprobBwd a, int64_t row0, int64_t rows, uint32_t across) {
+    constexpr int kV = kE<T>;
+    const int t = threadIdx.x % kT;
+    const uint32_t unit = blockIdx.x * (kThreads / kT) + (kT < kThreads ? __builtin_amdgcn_readfirstlane(threadIdx.x / kT) : 0);
+    const uint32_t down = unit / across, block = unit - down * across;
+    if (down >= rows) return;
+    const int64_t row = row0 + down;
     const T* x = static_cast<const T*>(a.x.p) + row * a.x.pitch;
     T* y = static_cast<T*>(a.dx.p) + row * a.dx.pitch;
     const float mx = a.max[row], logsum = a.logsum[row];
     const int64_t tok = a.dl ? a.tokens[row] : -1;
-    const float dl = tok >= 0 && tok < a.cols ? a.dl[row] : 0.0f, dh = a.dh ? a.dh[row] : 0.0f;
-    float v[kV] = {};
-    if ((dl != 0.0f || dh != 0.0f) && !(mx == -INFINITY && logsum == 0.0f)) {
-        const float H = a.dh ? a.entropy[row] : 0.0f;
-        Vec<T> t;
-        vload<false>(t, x + c, n);
-        t.get(v);
+    const bool has = tok >= 0 && tok < a.cols;
+    const float dl = has ? a.dl[row] : 0.0f, dh = kEntropy ? a.dh[row] : 0.0f;
+    const bool zero = (dl == 0.0f && dh == 0.0f) || (mx == -INFINITY && logsum == 0.0f);
+    const float H = kEntropy ? a.entropy[row] : 0.0f;
+    constexpr float c2 = static_cast<float>(kLog2e);
+    const float l2 = logsum * c2, base = dl + dh * H, back = -a.scale, up = dl * a.scale;
+    const int64_t n = a.cols;
+    const int head = static_cast<int>(min(static_cast<int64_t>((16 - reinterpret_cast<uintptr_t>(x) % 16) % 16 / sizeof(T)), n));
+    const int64_t nv = (n - head) / kV;
+    const auto grad = [&](float v) {
+        const float d = fmaf(v, a.scale, -mx), p = __builtin_amdgcn_exp2f(fmaf(d, c2, -l2));
+        // log p far below its place in p is 0 times infinity
+        if constexpr (kEntropy) return back * p * fmaf(dh, fmaxf(d - logsum, -1e4f), base);
+        else return back * dl * p;
+    };
+    const int64_t first = static_cast<int64_t>(block) * (kT * kBwdVecs) + t;
+    if (zero) {
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            const float lp = fmaf(v[j], a.scale, -mx) - logsum;
-            const float p = __builtin_amdgcn_exp2f(lp * static_cast<float>(kLog2e));
-            float d = -dl * p;
-            if (a.dh) d -= dh * (weighted(p, lp) + p * H);
-            if (c + j == tok) d += dl;
-            v[j] = d * a.scale;
+        for (int j = 0; j < kBwdVecs; ++j) {
+            const int64_t i = first + j * kT;
+            if (i < nv) put16(y + head + i * kV, u4{0u, 0u, 0u, 0u});
+        }
+    } else {
+        u4 w[kBwdVecs];
+#pragma unroll
+        for (int j = 0; j < kBwdVecs; ++j) {
+            const int64_t i = first + j * kT;
+            w[j] = u4{0u, 0u, 0u, 0u};
+            if (i < nv) w[j] = load16<kNt>(x + head + i * kV);
+        }
+#pragma unroll
+        for (int j = 0; j < kBwdVecs; ++j) {
+            const int64_t i = first + j * kT;
+            if (i >= nv) break;
+            float v[kV];
+            values(w[j], v);
+#pragma unroll
+            for (int q = 0; q < kV; ++q) v[q] = grad(v[q]);
+            const int64_t at = tok - (head + i * kV);
+            if (has && at >= 0 && at < kV) {
+#pragma unroll
+                for (int q = 0; q < kV; ++q) v[q] += q == at ? up : 0.0f;
+            }
+            put16(y + head + i * kV, packed(v));
         }
     }
-    put8(y + c, v, n);
+    if (block == 0) {
+        const int64_t tail = n - head - nv * kV;
+        const int64_t c = t < head ? t : t >= 8 && t - 8 < tail ? head + nv * kV + (t - 8) : -1;
+        if (c >= 0) {
+            const float g = zero ? 0.0f : grad(value(x + c)) + (has && c == tok ? up : 0.0f);
+            put1(y + c, g);
+        }
+    }
 }
 
 constexpr int64_t kMaxBlocks = int64_t{1} << 22;  // of 256 threads: a grid's threads fit 32 bits
 
 // Runs of a row: a few long rows leave most compute units idle, so that they are cut into runs of at
 // least kRun columns.
-constexpr int64_t kRun = 16384, kFill = 256;
+constexpr int64_t kRun = 32768, kFill = 256;
 Split plan_split(int64_t rows, int64_t cols) {
     int64_t parts = std::min<int64_t>({cols / kRun, kFill / std::max<int64_t>(rows, 1), kMaxParts});
     parts = std::max<int64_t>(parts, 1);
@@ -597,7 +670,7 @@ hipError_t forward_rows(const LogprobFwd& a, hipStream_t stream) {
     for (int64_t r0 = 0; r0 < a.rows; r0 += most) {
         const int64_t rows = std::min(a.rows - r0, most);
         const uint32_t blocks = static_cast<uint32_t>(rows * sp.parts);
-        if (sp.per <= 2048) forward<T, 64, false>(a, sp, r0, blocks, stream);
+        if (sp.per <= kShort) forward<T, 64, false>(a, sp, r0, blocks, stream);
         else if (blocks >= 512 || sp.per < 16384)
             nt ? forward<T, 256, true>(a, sp, r0, blocks, stream) : forward<T, 256, false>(a, sp, r0, blocks, stream);
         else forward<T, 1024, false>(a, sp, r0, blocks, stream);
@@ -620,17 +693,40 @@ hipError_t launch_logprob_forward(const LogprobFwd& a, hipStream_t stream) {
     return a.bf16 ? forward_rows<uint16_t>(a, stream) : forward_rows<float>(a, stream);
 }
 
-hipError_t launch_logprob_backward(const LogprobBwd& a, hipStream_t stream) {
-    const int64_t across = (a.cols + kThreads * kV - 1) / (kThreads * kV);
-    const int64_t rows = std::max<int64_t>(1, kMaxBlocks / across);
-    for (int64_t r0 = 0; r0 < a.rows; r0 += rows) {
-        const dim3 grid(static_cast<uint32_t>(std::min(a.rows - r0, rows) * across));
-        if (a.bf16) logprob_bwd_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(a, r0, static_cast<uint32_t>(across));
-        else logprob_bwd_kernel<float><<<grid, kThreads, 0, stream>>>(a, r0, static_cast<uint32_t>(across));
+namespace {
+
+template <typename T, int kT>
+hipError_t backward_rows(const LogprobBwd& a, hipStream_t stream) {
+    constexpr int kRows = kThreads / kT;
+    const int64_t across = std::max<int64_t>(1, (a.cols / kE<T> + kT * kBwdVecs - 1) / (kT * kBwdVecs));
+    const int64_t most = std::max<int64_t>(1, kMaxBlocks / across) * kRows;
+    const bool nt = a.rows * a.cols * static_cast<int64_t>(2 * sizeof(T)) >= kNtBytes;
+    for (int64_t r0 = 0; r0 < a.rows; r0 += most) {
+        const int64_t rows = std::min(a.rows - r0, most);
+        const dim3 grid(static_cast<uint32_t>((rows * across + kRows - 1) / kRows));
+        const uint32_t c = static_cast<uint32_t>(across);
+        if (a.dh) {
+            if (nt) logprob_bwd_kernel<T, kT, true, true><<<grid, kThreads, 0, stream>>>(a, r0, rows, c);
+            else logprob_bwd_kernel<T, kT, true, false><<<grid, kThreads, 0, stream>>>(a, r0, rows, c);
+        } else {
+            if (nt) logprob_bwd_kernel<T, kT, false, true><<<grid, kThreads, 0, stream>>>(a, r0, rows, c);
+            else logprob_bwd_kernel<T, kT, false, false><<<grid, kThreads, 0, stream>>>(a, r0, rows, c);
+        }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_logprob_backward(const LogprobBwd& a, hipStream_t stream) {
+    // a wave a row where its vectors are one shot of it
+    if (a.bf16)
+        return a.cols <= 64 * kBwdVecs * kE<uint16_t> ? backward_rows<uint16_t, 64>(a, stream)
+                                                      : backward_rows<uint16_t, kThreads>(a, stream);
+    return a.cols <= 64 * kBwdVecs * kE<float> ? backward_rows<float, 64>(a, stream)
+                                               : backward_rows<float, kThreads>(a, stream);
 }
 
 }  // namespace fsdp

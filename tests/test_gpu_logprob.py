@@ -110,6 +110,19 @@ def test_top(cols, top):
     check_forward(x, tok, 1.3, top, cols + 1, 3)
 
 
+@pytest.mark.parametrize("dtype,cols", [("bf16", 70000), ("bf16", 4900), ("bf16", 33000), ("f32", 33000), ("f32", 4900), ("f32", 2000)])
+def test_top_in_every_column(cols, dtype):
+    """The largest logits at every place of the last vectors and around the ends of whole steps, rows at any
+    element: none of them is lost where lanes part."""
+    n = 128
+    x = torch.zeros(n, cols)
+    for r in range(n):
+        x[r, cols - 1 - 9 * r % 1100] = 3.0
+        x[r, r * 37 % cols] = 2.0
+        x[r, (cols // 2 + r * 61) % cols] = 4.0
+    check_forward(x.to(T[dtype]), torch.zeros(n, dtype=torch.int64), top=3, pitch=cols + 1)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("cols", [64, 100, 2051, 50257, 200003])
 def test_ties(cols, dtype):
