@@ -186,8 +186,8 @@ __device__ __forceinline__ int larger(const uint64_t* keys, uint32_t n, uint64_t
 // ---------------------------------------------------------------------------
 // Candidates for the alternatives that a workgroup of kT threads gathers (where there are more, the bound is
 // found exactly), and the segments of its run (longer ones have larger segments).  A wave's own rows, of
-// kShort columns at most, hold less, so that a compute unit holds more of them: top 20 of 16384 x 500 bf16 XX us, 47.0
-// with as much as the others.
+// kShort columns at most, hold less, so that a compute unit holds more of them: top 20 with entropy of 16384 x 500 bf16
+// 30 us, with as much as the others 47; of 16384 x 3000 41 and 68.
 constexpr int64_t kShort = 4096;
 template <int kT> constexpr int kCandidates = kT == 64 ? 512 : 1024;
 template <typename T, int kT> constexpr uint32_t kSegments = kT == 64 ? kShort / kE<T> : 2048;
@@ -565,15 +565,22 @@ __global__ void __launch_bounds__(kThreads) logprob_join_kernel(LogprobFwd a, Sp
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
-// One shot: a workgroup takes kBwdVecs vectors a thread of one row (a wave a row where rows are short),
-// aligned as the logits are; block 0 of a row also takes its head and its tail.  A lane stores what it has read,
+// One shot: a workgroup takes two vectors a thread of one row (where rows are short a wave takes a row, four
+// vectors a thread), aligned as the logits are; block 0 of a row also takes its head and its tail.  A lane stores what it has read,
 // so that the gradient may take the logits' place.
-constexpr int kBwdVecs = 4;
+// Vectors a thread, 4096 x 50257 bf16 with a tenth of the rows padded: 1 / 2 / 3 / 4 / 8 163 / 127.5 / 133 / 137 / 147 us; 2048 x
+// 50257 fp32 with entropy 181 / 132 / 138 / 138 / 406.  Cached loads 2-7% slower there, cached stores 5-20% everywhere.
+template <int kT> constexpr int kBwdVecs = kT == 64 ? 4 : 2;
 template <typename T, int kT, bool kEntropy, bool kNt>
 __global__ void __launch_bounds__(kThreads) logprob_bwd_kernel(LogprobBwd a, int64_t row0, int64_t rows, uint32_t across) {
-    constexpr int kV = kE<T>;
+    constexpr int kV = kE<T>, kN = kBwdVecs<kT>;
     const int t = threadIdx.x % kT;
-    const uint32_t unit = blockIdx.x * (kThreads / kT) + (kT < kThreads ? __builtin_amdgcn_readfirstlane(threadIdx.x / kT) : 0);
+    // each XCD takes runs of 16 neighbouring blocks: 128.5 -> 126 us (4096 x 50257 bf16; runs of 64 / 128 / 256 / 512 126.0 /
+    // 127.0 / 127.5 / 131)
+    constexpr uint32_t kXcds = 8, kRunOf = 16, kPer = kXcds * kRunOf;
+    uint32_t at = blockIdx.x;
+    if (at < gridDim.x / kPer * kPer) at = at / kPer * kPer + at % kXcds * kRunOf + at % kPer / kXcds;
+    const uint32_t unit = at * (kThreads / kT) + (kT < kThreads ? __builtin_amdgcn_readfirstlane(threadIdx.x / kT) : 0);
     const uint32_t down = unit / across, block = unit - down * across;
     if (down >= rows) return;
     const int64_t row = row0 + down;
@@ -596,23 +603,23 @@ __global__ void __launch_bounds__(kThreads) logprob_bwd_kernel(LogprobBwd a, int
         if constexpr (kEntropy) return back * p * fmaf(dh, fmaxf(d - logsum, -1e4f), base);
         else return back * dl * p;
     };
-    const int64_t first = static_cast<int64_t>(block) * (kT * kBwdVecs) + t;
+    const int64_t first = static_cast<int64_t>(block) * (kT * kN) + t;
     if (zero) {
 #pragma unroll
-        for (int j = 0; j < kBwdVecs; ++j) {
+        for (int j = 0; j < kN; ++j) {
             const int64_t i = first + j * kT;
             if (i < nv) put16(y + head + i * kV, u4{0u, 0u, 0u, 0u});
         }
     } else {
-        u4 w[kBwdVecs];
+        u4 w[kN];
 #pragma unroll
-        for (int j = 0; j < kBwdVecs; ++j) {
+        for (int j = 0; j < kN; ++j) {
             const int64_t i = first + j * kT;
             w[j] = u4{0u, 0u, 0u, 0u};
             if (i < nv) w[j] = load16<kNt>(x + head + i * kV);
         }
 #pragma unroll
-        for (int j = 0; j < kBwdVecs; ++j) {
+        for (int j = 0; j < kN; ++j) {
             const int64_t i = first + j * kT;
             if (i >= nv) break;
             float v[kV];
@@ -698,7 +705,7 @@ namespace {
 template <typename T, int kT>
 hipError_t backward_rows(const LogprobBwd& a, hipStream_t stream) {
     constexpr int kRows = kThreads / kT;
-    const int64_t across = std::max<int64_t>(1, (a.cols / kE<T> + kT * kBwdVecs - 1) / (kT * kBwdVecs));
+    const int64_t across = std::max<int64_t>(1, (a.cols / kE<T> + kT * kBwdVecs<kT> - 1) / (kT * kBwdVecs<kT>));
     const int64_t most = std::max<int64_t>(1, kMaxBlocks / across) * kRows;
     const bool nt = a.rows * a.cols * static_cast<int64_t>(2 * sizeof(T)) >= kNtBytes;
     for (int64_t r0 = 0; r0 < a.rows; r0 += most) {
@@ -723,9 +730,9 @@ hipError_t backward_rows(const LogprobBwd& a, hipStream_t stream) {
 hipError_t launch_logprob_backward(const LogprobBwd& a, hipStream_t stream) {
     // a wave a row where its vectors are one shot of it
     if (a.bf16)
-        return a.cols <= 64 * kBwdVecs * kE<uint16_t> ? backward_rows<uint16_t, 64>(a, stream)
+        return a.cols <= 64 * kBwdVecs<64> * kE<uint16_t> ? backward_rows<uint16_t, 64>(a, stream)
                                                       : backward_rows<uint16_t, kThreads>(a, stream);
-    return a.cols <= 64 * kBwdVecs * kE<float> ? backward_rows<float, 64>(a, stream)
+    return a.cols <= 64 * kBwdVecs<64> * kE<float> ? backward_rows<float, 64>(a, stream)
                                                : backward_rows<float, kThreads>(a, stream);
 }
 
