@@ -329,7 +329,6 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
         p.s = p.s * f + e;
         p.m = m;
     };
-    if (t < head) one(value(x + t));
     const auto load = [&](uint32_t i) { return load16<kNt>(reinterpret_cast<const char*>(body) + i * 16u); };
     // kU vectors from place i on (those beyond the end were read from the last one)
     const auto take = [&](const u4* w, uint32_t i, auto full) {
@@ -388,19 +387,24 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
     // a segment's lanes go together, so that its maximum meets
     constexpr uint32_t kLast = kTop ? kSeg - 1 : 0;
     uint32_t i = t;
-    for (; (i | kLast) + (kU - 1) * kT < nv; i += kU * kT) {
-        u4 w[kU];
+    if constexpr (kT < 1024) {   // (few rows take few steps: one path, for its instructions are fetched once)
+        for (; (i | kLast) + (kU - 1) * kT < nv; i += kU * kT) {
+            u4 w[kU];
 #pragma unroll
-        for (int j = 0; j < kU; ++j) w[j] = load(i + j * kT);
-        take(w, i, std::true_type{});
+            for (int j = 0; j < kU; ++j) w[j] = load(i + j * kT);
+            take(w, i, std::true_type{});
+        }
     }
-    if ((i & ~kLast) < nv) {
+    for (; (i & ~kLast) < nv; i += kU * kT) {
         u4 w[kU];
 #pragma unroll
         for (int j = 0; j < kU; ++j) w[j] = load(min(i + j * kT, nv - 1));
         take(w, i, std::false_type{});
     }
-    if (t >= 8 && t - 8 < tail) one(value(body + static_cast<int64_t>(nv) * kV + (t - 8)));
+    // head and tail: lane t's element t and t - 8 of them
+    const bool in_tail = t >= 8 && t - 8 < tail;
+    const int64_t edge = t < head ? t : in_tail ? n - tail + (t - 8) : -1;
+    if (edge >= 0) one(value(x + edge));
 
     // the lanes' sums, then the waves'
     const auto meet = [&](Part q) {
@@ -475,32 +479,17 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
         if (taken <= kMost) {
             const int vecs = __builtin_ctz(kSeg) + wide;
             const uint32_t work = taken << vecs;
-            constexpr int kA = 4;   // read at once
-            for (uint32_t i = t; i < work; i += kA * kT) {
-                u4 w[kA];
-                uint32_t at[kA], seg[kA];
+            // (one vector a thread reads what is usually chosen)
+            for (uint32_t i = t; i < work; i += kT) {
+                const uint32_t seg = chosen[i >> vecs], at = (seg << vecs) + (i & ((1u << vecs) - 1));
+                if (at >= nv) continue;
+                float v[kV];
+                values(load16<false>(reinterpret_cast<const char*>(body) + at * 16u), v);
 #pragma unroll
-                for (int j = 0; j < kA; ++j) {
-                    const uint32_t item = min(i + j * kT, work - 1);
-                    seg[j] = chosen[item >> vecs];
-                    at[j] = (seg[j] << vecs) + (item & ((1u << vecs) - 1));
-                    w[j] = load16<false>(reinterpret_cast<const char*>(body) + min(at[j], nv - 1) * 16u);
-                }
-#pragma unroll
-                for (int j = 0; j < kA; ++j) {
-                    if (i + j * kT >= work || at[j] >= nv) continue;
-                    float v[kV];
-                    values(w[j], v);
-#pragma unroll
-                    for (int q = 0; q < kV; ++q) gather(v[q], seg[j], head + static_cast<int64_t>(at[j]) * kV + q);
-                }
+                for (int q = 0; q < kV; ++q) gather(v[q], seg, head + static_cast<int64_t>(at) * kV + q);
             }
             // the head comes before every segment, the tail behind all of them
-            if (t < head) gather(value(x + t), 0u, t);
-            if (t >= 8 && t - 8 < tail) {
-                const int64_t col = head + static_cast<int64_t>(nv) * kV + (t - 8);
-                gather(value(x + col), n_segs, col);
-            }
+            if (edge >= 0) gather(value(x + edge), in_tail ? n_segs : 0u, edge);
         } else if (t == 0) {
             count = kMost + 1;
         }
