@@ -21,6 +21,7 @@ constexpr int kTile = kThreads * 8;   // elements of a workgroup
 constexpr int kLaunch = 50;           // tensors of a launch (kernel-argument budget)
 constexpr int64_t kMaxTiles = int64_t{1} << 22;
 
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u2e __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u1e __attribute__((aligned(1)));
 typedef float f4 __attribute__((ext_vector_type(4)));
@@ -53,15 +54,29 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
     // 2^(byte - 127); 255: NaN; 0 (a state of zeros): 0
     return __builtin_bit_cast(float, byte == 255u ? 0x7FC00000u : byte << 23);
 }
-// x, scaled by 1 / 2^s, rounded at random to a code's value.
+// Four values, scaled by inv = 1 / 2^s and rounded at random to codes' values: n = floor(|y| / q + r / 2^16) of
+// steps q, an eighth of the power of two below y, but no less than 2^(kMinExp - 3).  Above 2^kMinExp that is
+// adding r below the three mantissa bits that stay and cutting off what is left of them (20 bits; the sum is
+// exact either way); smaller values, and zeros, take the sum itself.
 template <typename F>
-__device__ __forceinline__ float round_code(float x, float inv, uint32_t r16) {
-    const float y = fabsf(x) * inv;
-    // an eighth of the power of two below y, and its inverse
-    const uint32_t e = max(__builtin_bit_cast(uint32_t, y) & 0x7F800000u, static_cast<uint32_t>(F::kMinExp + 127) << 23);
-    const float q = __builtin_bit_cast(float, e - (3u << 23)), iq = __builtin_bit_cast(float, (257u << 23) - e);
-    const float n = floorf(y * iq + static_cast<float>(r16) * 0x1p-16f);
-    return copysignf(n * q, x);
+__device__ __forceinline__ void round_codes(const float* x, float inv, const uint32_t* r16, float* c) {
+    uint32_t y[4], low = 0xFFFFFFFFu;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        y[j] = __builtin_bit_cast(uint32_t, x[j] * inv);
+        low = min(low, y[j] & 0x7FFFFFFFu);
+        c[j] = __builtin_bit_cast(float, (y[j] + (r16[j] << 4)) & 0xFFF00000u);
+    }
+    constexpr uint32_t kNormal = static_cast<uint32_t>(F::kMinExp + 127) << 23;
+    if (low < kNormal) {
+        constexpr float q = __builtin_bit_cast(float, kNormal - (3u << 23)), iq = __builtin_bit_cast(float, (257u << 23) - kNormal);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float v = __builtin_bit_cast(float, y[j]);
+            const float n = floorf(fabsf(v) * iq + static_cast<float>(r16[j]) * 0x1p-16f) * q;
+            if ((y[j] & 0x7FFFFFFFu) < kNormal) c[j] = copysignf(n, v);
+        }
+    }
 }
 // Four codes of a word, and back.  Values that are codes convert exactly.
 __device__ __forceinline__ uint32_t pack_m(const float* v) {
@@ -94,13 +109,18 @@ __device__ __forceinline__ void unpack_v(uint32_t w, float scale, float* v) {
 }
 // Random bits of an element: a xor-shift-multiply hash of its number and the tensor's key (multipliers
 // next to 2^32 times the golden ratio, and the square roots of 2 and 3); m takes the upper 16, v the lower.
-__device__ __forceinline__ uint32_t random_bits(uint64_t element, uint32_t key) {
-    uint32_t x = static_cast<uint32_t>(element) * 0x9E3779B1u + key + static_cast<uint32_t>(element >> 32) * 0xDDB3D743u;
-    x ^= x >> 15;
-    x *= 0xB504F333u;
-    x ^= x >> 13;
-    x *= 0xDDB3D743u;
-    return x ^ (x >> 16);
+__device__ __forceinline__ void random_bits(uint64_t element, uint32_t key, uint32_t* r) {
+    // four neighbouring elements, the first a multiple of 4
+    const uint32_t first = static_cast<uint32_t>(element) * 0x9E3779B1u + key + static_cast<uint32_t>(element >> 32) * 0xDDB3D743u;
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) {
+        uint32_t x = first + j * 0x9E3779B1u;
+        x ^= x >> 15;
+        x *= 0xB504F333u;
+        x ^= x >> 13;
+        x *= 0xDDB3D743u;
+        r[j] = x ^ (x >> 16);
+    }
 }
 // The largest of a group's eight lanes.
 __device__ __forceinline__ float group_max(float x) {
@@ -121,87 +141,120 @@ __device__ __forceinline__ float largest(const float* v) {
     for (int j = 0; j < 4; ++j) a = max(a, __builtin_bit_cast(uint32_t, v[j]) & 0x7FFFFFFFu);
     return __builtin_bit_cast(float, a);
 }
-// Four elements of a state (n of them inside the tensor), element `at` its first.
-template <typename F>
-__device__ __forceinline__ void load8(const uint8_t* s, int64_t at, int n, int64_t scales, float* v) {
-    uint32_t w = 0;
-    if (n >= 4) {
-        w = *(const u1e*)(s + at);
+template <bool kWhole>
+__device__ __forceinline__ void put4(float* p, int n, const float* v) {
+    if (kWhole || n >= 4) {
+        __builtin_nontemporal_store((f4{v[0], v[1], v[2], v[3]}), (f4e*)p);
     } else {
+#pragma unroll
         for (int j = 0; j < 3; ++j)
-            if (j < n) w |= static_cast<uint32_t>(s[at + j]) << (8 * j);
-    }
-    const float scale = n > 0 ? scale_value(s[scales + at / kStateGroup]) : 0.0f;
-    if constexpr (F::kTopExp == 8) unpack_m(w, scale, v);
-    else unpack_v(w, scale, v);
-}
-// Every lane of a group calls it; values behind the tensor's end are 0.
-template <typename F>
-__device__ __forceinline__ void store8(uint8_t* s, int64_t at, int n, int64_t scales, const float* v, const uint32_t* r, bool high) {
-    const uint32_t byte = scale_byte<F>(group_max(largest(v)));
-    uint32_t w = 0;
-    if (byte != 255u) {
-        const float inv = __builtin_bit_cast(float, (254u - byte) << 23);
-        float c[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[j] = round_code<F>(v[j], inv, high ? r[j] >> 16 : r[j] & 0xFFFFu);
-        w = F::kTopExp == 8 ? pack_m(c) : pack_v(c);
-    }
-    if (n >= 4) {
-        *(u1e*)(s + at) = w;
-    } else {
-        for (int j = 0; j < 3; ++j)
-            if (j < n) s[at + j] = static_cast<uint8_t>(w >> (8 * j));
-    }
-    if (n > 0 && (threadIdx.x & 7) == 0) s[scales + at / kStateGroup] = static_cast<uint8_t>(byte);
-}
-
-// ---------------------------------------------------------------------------
-// four elements of an fp32 or bf16 array
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ void load4(const float* p, int n, float* v) {
-    if (n >= 4) {
-        const f4 t = *(const f4e*)p;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = t[j];
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = j < n ? p[j] : 0.0f;
-    }
-}
-__device__ __forceinline__ void load4(const uint16_t* p, int n, float* v) {
-    uint32_t w[2] = {0u, 0u};
-    if (n >= 4) {
-        const u2e t = *(const u2e*)p;
-        w[0] = t[0];
-        w[1] = t[1];
-    } else {
-        for (int j = 0; j < 3; ++j)
-            if (j < n) w[j >> 1] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = __builtin_bit_cast(float, j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
-}
-__device__ __forceinline__ void store4(float* p, int n, const float* v) {
-    if (n >= 4) {
-        *(f4e*)p = f4{v[0], v[1], v[2], v[3]};
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
             if (j < n) p[j] = v[j];
     }
 }
-__device__ __forceinline__ void store4(uint16_t* p, int n, const float* v) {
-    u2e w;
+template <bool kWhole>
+__device__ __forceinline__ void put4(uint16_t* p, int n, const float* v) {
+    u2 w;
     w[0] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v[0], v[1]}), bf2));
     w[1] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v[2], v[3]}), bf2));
-    if (n >= 4) {
-        *(u2e*)p = w;
+    if (kWhole || n >= 4) {
+        __builtin_nontemporal_store(w, (u2e*)p);
     } else {
         for (int j = 0; j < 3; ++j)
             if (j < n) p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
     }
 }
+// Raw loads of four elements, n of them inside the tensor (kWhole: all), so that a tile's loads are all issued
+// before the first is used.
+template <bool kWhole>
+__device__ __forceinline__ uint32_t raw_codes(const uint8_t* s, int64_t at, int n) {
+    if (kWhole || n >= 4) return *(const u1e*)(s + at);
+    uint32_t w = 0;
+    for (int j = 0; j < 3; ++j)
+        if (j < n) w |= static_cast<uint32_t>(s[at + j]) << (8 * j);
+    return w;
+}
+template <bool kWhole>
+__device__ __forceinline__ uint32_t raw_scale(const uint8_t* s, int64_t at, int n, int64_t scales) {
+    return kWhole || n > 0 ? s[scales + at / kStateGroup] : 0u;
+}
+template <bool kWhole>
+__device__ __forceinline__ f4 raw4(const float* p, int n) {
+    if (kWhole || n >= 4) return *(const f4e*)p;
+    f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+        if (j < n) v[j] = p[j];
+    return v;
+}
+template <bool kWhole>
+__device__ __forceinline__ u2 raw4(const uint16_t* p, int n) {
+    if (kWhole || n >= 4) return *(const u2e*)p;
+    u2 v = {0u, 0u};
+    for (int j = 0; j < 3; ++j)
+        if (j < n) v[j >> 1] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
+    return v;
+}
+__device__ __forceinline__ void values(f4 w, float* v) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = w[j];
+}
+__device__ __forceinline__ void values(u2 w, float* v) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __builtin_bit_cast(float, j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+}
+// A state in its format: raw words of four elements, their values, and the way back.
+template <State kState, typename F> struct Held;
+template <typename F> struct Held<State::k8Bit, F> {
+    uint32_t codes, scale;
+    template <bool kWhole> __device__ void load(const void* s, int64_t at, int n, int64_t scales) {
+        codes = raw_codes<kWhole>(static_cast<const uint8_t*>(s), at, n);
+        scale = raw_scale<kWhole>(static_cast<const uint8_t*>(s), at, n, scales);
+    }
+    __device__ void get(float* v) const {
+        if constexpr (F::kTopExp == 8) unpack_m(codes, scale_value(scale), v);
+        else unpack_v(codes, scale_value(scale), v);
+    }
+    // every lane of a group calls it; values behind the tensor's end are 0
+    template <bool kWhole> __device__ static void put(void* to, int64_t at, int n, int64_t scales, const float* v, const uint32_t* r) {
+        uint8_t* s = static_cast<uint8_t*>(to);
+        const uint32_t byte = scale_byte<F>(group_max(largest(v)));
+        const float inv = __builtin_bit_cast(float, (254u - byte) << 23);
+        uint32_t r16[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r16[j] = F::kTopExp == 8 ? r[j] >> 16 : r[j] & 0xFFFFu;
+        float c[4];
+        round_codes<F>(v, inv, r16, c);
+        uint32_t w = F::kTopExp == 8 ? pack_m(c) : pack_v(c);
+        if (byte == 255u) w = 0;
+        if (kWhole || n >= 4) {
+            *(u1e*)(s + at) = w;
+        } else {
+            for (int j = 0; j < 3; ++j)
+                if (j < n) s[at + j] = static_cast<uint8_t>(w >> (8 * j));
+        }
+        if ((kWhole || n > 0) && (threadIdx.x & 7) == 0) s[scales + at / kStateGroup] = static_cast<uint8_t>(byte);
+    }
+};
+template <typename F> struct Held<State::kF32, F> {
+    f4 raw;
+    template <bool kWhole> __device__ void load(const void* s, int64_t at, int n, int64_t) {
+        raw = raw4<kWhole>(static_cast<const float*>(s) + at, n);
+    }
+    __device__ void get(float* v) const { values(raw, v); }
+    template <bool kWhole> __device__ static void put(void* to, int64_t at, int n, int64_t, const float* v, const uint32_t*) {
+        put4<kWhole>(static_cast<float*>(to) + at, n, v);
+    }
+};
+template <typename F> struct Held<State::kBF16, F> {
+    u2 raw;
+    template <bool kWhole> __device__ void load(const void* s, int64_t at, int n, int64_t) {
+        raw = raw4<kWhole>(static_cast<const uint16_t*>(s) + at, n);
+    }
+    __device__ void get(float* v) const { values(raw, v); }
+    template <bool kWhole> __device__ static void put(void* to, int64_t at, int n, int64_t, const float* v, const uint32_t*) {
+        put4<kWhole>(static_cast<uint16_t*>(to) + at, n, v);
+    }
+};
 
 // ---------------------------------------------------------------------------
 // the step
@@ -233,48 +286,65 @@ __device__ __forceinline__ void adam1(float& p, float g, float& m, float& v, con
     p = p - s.step_size * (m / den);
 }
 
-template <typename G, bool k8>
+template <typename G, State kState, bool kWhole>
+__device__ __forceinline__ void adam_tile(const Table& t, const Entry& e, int64_t base) {
+    constexpr int kN = kTile / kThreads / 4;
+    const AdamScalars s = t.sc[e.group];
+    const float gs = t.grad_scale ? *t.grad_scale : 1.0f;
+    const int64_t scales = (e.n + 15) / 16 * 16;
+    f4 p[kN];
+    decltype(raw4<true>(static_cast<const G*>(nullptr), 0)) g[kN];
+    Held<kState, FormatM> m[kN];
+    Held<kState, FormatV> v[kN];
+    const auto place = [&](int h, int64_t* at) {
+        *at = base + 4 * (threadIdx.x + h * kThreads);
+        return kWhole ? 4 : static_cast<int>(max(min(e.n - *at, int64_t{4}), int64_t{0}));
+    };
+#pragma unroll
+    for (int h = 0; h < kN; ++h) {
+        int64_t at;
+        const int n = place(h, &at);
+        p[h] = raw4<kWhole>(e.p + at, n);
+        g[h] = raw4<kWhole>(static_cast<const G*>(e.g) + at, n);
+        m[h].template load<kWhole>(e.m, at, n, scales);
+        v[h].template load<kWhole>(e.v, at, n, scales);
+    }
+#pragma unroll
+    for (int h = 0; h < kN; ++h) {
+        int64_t at;
+        const int n = place(h, &at);
+        float pp[4], gg[4], mm[4], vv[4];
+        values(p[h], pp);
+        values(g[h], gg);
+        m[h].get(mm);
+        v[h].get(vv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) adam1(pp[j], t.grad_scale ? gg[j] * gs : gg[j], mm[j], vv[j], s);
+        put4<kWhole>(e.p + at, n, pp);
+        if (e.pb) put4<kWhole>(e.pb + at, n, pp);
+        uint32_t r[4];
+        if constexpr (kState == State::k8Bit) {
+            random_bits(static_cast<uint64_t>(at), e.key, r);
+            if constexpr (!kWhole) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j >= n) mm[j] = vv[j] = 0.0f;
+            }
+        }
+        Held<kState, FormatM>::template put<kWhole>(e.m, at, n, scales, mm, r);
+        Held<kState, FormatV>::template put<kWhole>(e.v, at, n, scales, vv, r);
+    }
+}
+
+template <typename G, State kState>
 __global__ void __launch_bounds__(kThreads) adam_tensors_kernel(Table t) {
     if (t.skip && *t.skip != 0.0f) return;
     uint32_t k = 0;
     for (int i = 1; i < kLaunch; ++i) k += t.start[i] <= blockIdx.x ? 1u : 0u;
     const Entry& e = t.e[k];
-    const AdamScalars s = t.sc[e.group];
-    const float gs = t.grad_scale ? *t.grad_scale : 1.0f;
     const int64_t base = (static_cast<int64_t>(blockIdx.x - t.start[k]) + e.bias) * kTile;
-    const int64_t scales = (e.n + 15) / 16 * 16;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int64_t at = base + 4 * (threadIdx.x + h * kThreads);
-        const int n = static_cast<int>(max(min(e.n - at, int64_t{4}), int64_t{0}));
-        float p[4], g[4], m[4], v[4];
-        load4(e.p + at, n, p);
-        load4(static_cast<const G*>(e.g) + at, n, g);
-        if constexpr (k8) {
-            load8<FormatM>(static_cast<const uint8_t*>(e.m), at, n, scales, m);
-            load8<FormatV>(static_cast<const uint8_t*>(e.v), at, n, scales, v);
-        } else {
-            load4(static_cast<const float*>(e.m) + at, n, m);
-            load4(static_cast<const float*>(e.v) + at, n, v);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) adam1(p[j], t.grad_scale ? g[j] * gs : g[j], m[j], v[j], s);
-        store4(e.p + at, n, p);
-        if (e.pb) store4(e.pb + at, n, p);
-        if constexpr (k8) {
-            uint32_t r[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                r[j] = random_bits(static_cast<uint64_t>(at + j), e.key);
-                if (j >= n) m[j] = v[j] = 0.0f;
-            }
-            store8<FormatM>(static_cast<uint8_t*>(e.m), at, n, scales, m, r, true);
-            store8<FormatV>(static_cast<uint8_t*>(e.v), at, n, scales, v, r, false);
-        } else {
-            store4(static_cast<float*>(e.m) + at, n, m);
-            store4(static_cast<float*>(e.v) + at, n, v);
-        }
-    }
+    if (base + kTile <= e.n) adam_tile<G, kState, true>(t, e, base);
+    else adam_tile<G, kState, false>(t, e, base);
 }
 
 struct CopyEntry {
@@ -288,42 +358,45 @@ struct CopyTable {
     CopyEntry e[kLaunch];
 };
 
+template <State kFrom, State kTo, bool kWhole>
+__device__ __forceinline__ void convert_tile(const CopyEntry& e, int64_t base) {
+    constexpr int kN = kTile / kThreads / 4;
+    const int64_t scales = (e.n + 15) / 16 * 16;
+    Held<kFrom, FormatM> m[kN];
+    Held<kFrom, FormatV> v[kN];
+    const auto place = [&](int h, int64_t* at) {
+        *at = base + 4 * (threadIdx.x + h * kThreads);
+        return kWhole ? 4 : static_cast<int>(max(min(e.n - *at, int64_t{4}), int64_t{0}));
+    };
+#pragma unroll
+    for (int h = 0; h < kN; ++h) {
+        int64_t at;
+        const int n = place(h, &at);
+        m[h].template load<kWhole>(e.m, at, n, scales);
+        v[h].template load<kWhole>(e.v, at, n, scales);
+    }
+#pragma unroll
+    for (int h = 0; h < kN; ++h) {
+        int64_t at;
+        const int n = place(h, &at);
+        float mm[4], vv[4];
+        m[h].get(mm);
+        v[h].get(vv);
+        uint32_t r[4];
+        if constexpr (kTo == State::k8Bit) random_bits(static_cast<uint64_t>(at), e.key, r);
+        Held<kTo, FormatM>::template put<kWhole>(e.m_to, at, n, scales, mm, r);
+        Held<kTo, FormatV>::template put<kWhole>(e.v_to, at, n, scales, vv, r);
+    }
+}
+
 template <State kFrom, State kTo>
 __global__ void __launch_bounds__(kThreads) adam_convert_kernel(CopyTable t) {
     uint32_t k = 0;
     for (int i = 1; i < kLaunch; ++i) k += t.start[i] <= blockIdx.x ? 1u : 0u;
     const CopyEntry& e = t.e[k];
     const int64_t base = (static_cast<int64_t>(blockIdx.x - t.start[k]) + e.bias) * kTile;
-    const int64_t scales = (e.n + 15) / 16 * 16;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int64_t at = base + 4 * (threadIdx.x + h * kThreads);
-        const int n = static_cast<int>(max(min(e.n - at, int64_t{4}), int64_t{0}));
-        float m[4], v[4];
-        if constexpr (kFrom == State::k8Bit) {
-            load8<FormatM>(static_cast<const uint8_t*>(e.m), at, n, scales, m);
-            load8<FormatV>(static_cast<const uint8_t*>(e.v), at, n, scales, v);
-        } else if constexpr (kFrom == State::kBF16) {
-            load4(static_cast<const uint16_t*>(e.m) + at, n, m);
-            load4(static_cast<const uint16_t*>(e.v) + at, n, v);
-        } else {
-            load4(static_cast<const float*>(e.m) + at, n, m);
-            load4(static_cast<const float*>(e.v) + at, n, v);
-        }
-        if constexpr (kTo == State::k8Bit) {
-            uint32_t r[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) r[j] = random_bits(static_cast<uint64_t>(at + j), e.key);
-            store8<FormatM>(static_cast<uint8_t*>(e.m_to), at, n, scales, m, r, true);
-            store8<FormatV>(static_cast<uint8_t*>(e.v_to), at, n, scales, v, r, false);
-        } else if constexpr (kTo == State::kBF16) {
-            store4(static_cast<uint16_t*>(e.m_to) + at, n, m);
-            store4(static_cast<uint16_t*>(e.v_to) + at, n, v);
-        } else {
-            store4(static_cast<float*>(e.m_to) + at, n, m);
-            store4(static_cast<float*>(e.v_to) + at, n, v);
-        }
-    }
+    if (base + kTile <= e.n) convert_tile<kFrom, kTo, true>(e, base);
+    else convert_tile<kFrom, kTo, false>(e, base);
 }
 
 int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
@@ -359,14 +432,14 @@ hipError_t in_launches(const List& list, TableT& t, Fill&& fill, Launch&& launch
     return flush();
 }
 
-template <typename G, bool k8>
+template <typename G, State kState>
 hipError_t step(const std::vector<AdamTensor>& list, Table& t, hipStream_t stream) {
     return in_launches(
         list, t,
         [&](int i, const AdamTensor& a, uint32_t bias) {
             t.e[i] = {a.p, a.g, a.m, a.v, a.pb, a.n, bias, a.key, static_cast<uint32_t>(a.group), 0};
         },
-        [&](uint32_t tiles) { adam_tensors_kernel<G, k8><<<dim3(tiles), kThreads, 0, stream>>>(t); });
+        [&](uint32_t tiles) { adam_tensors_kernel<G, kState><<<dim3(tiles), kThreads, 0, stream>>>(t); });
 }
 
 template <State kFrom, State kTo>
@@ -399,8 +472,8 @@ hipError_t launch_adam_tensors(const std::vector<AdamTensor>& list, const AdamSc
     std::copy(groups, groups + n_groups, t.sc);
     t.grad_scale = grad_scale;
     t.skip = skip;
-    if (state8) return grad_bf16 ? step<uint16_t, true>(list, t, stream) : step<float, true>(list, t, stream);
-    return grad_bf16 ? step<uint16_t, false>(list, t, stream) : step<float, false>(list, t, stream);
+    if (state8) return grad_bf16 ? step<uint16_t, State::k8Bit>(list, t, stream) : step<float, State::k8Bit>(list, t, stream);
+    return grad_bf16 ? step<uint16_t, State::kF32>(list, t, stream) : step<float, State::kF32>(list, t, stream);
 }
 
 hipError_t launch_adam_convert(const std::vector<StateCopy>& list, State from, State to, hipStream_t stream) {
