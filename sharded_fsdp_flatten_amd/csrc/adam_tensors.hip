@@ -8,6 +8,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "train.h"
 
@@ -17,7 +18,9 @@ namespace fsdp {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = kThreads * 8;   // elements of a workgroup
+// Elements of a workgroup: 14.2 M elements with fp32 states, tiles of 1024 / 2048 / 4096 72.1 / 74.0 / 73.9 us; 25 M with 8-bit
+// ones XX.
+template <State kState> constexpr int kTile = kThreads * (kState == State::kF32 ? 4 : 8);
 constexpr int kLaunch = 50;           // tensors of a launch (kernel-argument budget)
 constexpr int64_t kMaxTiles = int64_t{1} << 22;
 
@@ -163,6 +166,13 @@ __device__ __forceinline__ void put4(uint16_t* p, int n, const float* v) {
             if (j < n) p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
     }
 }
+// Arrays are read past the cache (kNt) where a call's operands outgrow it, as the layer operators' are.  Steps
+// queued one after another over three sets of operands, cached / nt, us: fp32 states 75 MB 14.3 / 16.0, 150 MB 27.1 /
+// 28.8, 425 MB 82.9 / 73.9, 900 MB 168 / 152; 8-bit ones 91 MB 18.6 / 18.9, 257 MB 51.6 / 44.6, 544 MB 103 / 86.  (Alone after a
+// read of 1 GiB cached loads look better, 69.6 against 77.8 us for 425 MB: then up to 256 MB of what was written
+// is still on its way when the kernel ends, and the next one pays.)  Codes and scales are always cached.
+constexpr int64_t kNtBytes = int64_t{192} << 20;
+
 // Raw loads of four elements, n of them inside the tensor (kWhole: all), so that a tile's loads are all issued
 // before the first is used.
 template <bool kWhole>
@@ -177,18 +187,18 @@ template <bool kWhole>
 __device__ __forceinline__ uint32_t raw_scale(const uint8_t* s, int64_t at, int n, int64_t scales) {
     return kWhole || n > 0 ? s[scales + at / kStateGroup] : 0u;
 }
-template <bool kWhole>
+template <bool kWhole, bool kNt>
 __device__ __forceinline__ f4 raw4(const float* p, int n) {
-    if (kWhole || n >= 4) return *(const f4e*)p;
+    if (kWhole || n >= 4) return kNt ? __builtin_nontemporal_load((const f4e*)p) : *(const f4e*)p;
     f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < 3; ++j)
         if (j < n) v[j] = p[j];
     return v;
 }
-template <bool kWhole>
+template <bool kWhole, bool kNt>
 __device__ __forceinline__ u2 raw4(const uint16_t* p, int n) {
-    if (kWhole || n >= 4) return *(const u2e*)p;
+    if (kWhole || n >= 4) return kNt ? __builtin_nontemporal_load((const u2e*)p) : *(const u2e*)p;
     u2 v = {0u, 0u};
     for (int j = 0; j < 3; ++j)
         if (j < n) v[j >> 1] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
@@ -206,7 +216,7 @@ __device__ __forceinline__ void values(u2 w, float* v) {
 template <State kState, typename F> struct Held;
 template <typename F> struct Held<State::k8Bit, F> {
     uint32_t codes, scale;
-    template <bool kWhole> __device__ void load(const void* s, int64_t at, int n, int64_t scales) {
+    template <bool kWhole, bool kNt> __device__ void load(const void* s, int64_t at, int n, int64_t scales) {
         codes = raw_codes<kWhole>(static_cast<const uint8_t*>(s), at, n);
         scale = raw_scale<kWhole>(static_cast<const uint8_t*>(s), at, n, scales);
     }
@@ -237,8 +247,8 @@ template <typename F> struct Held<State::k8Bit, F> {
 };
 template <typename F> struct Held<State::kF32, F> {
     f4 raw;
-    template <bool kWhole> __device__ void load(const void* s, int64_t at, int n, int64_t) {
-        raw = raw4<kWhole>(static_cast<const float*>(s) + at, n);
+    template <bool kWhole, bool kNt> __device__ void load(const void* s, int64_t at, int n, int64_t) {
+        raw = raw4<kWhole, kNt>(static_cast<const float*>(s) + at, n);
     }
     __device__ void get(float* v) const { values(raw, v); }
     template <bool kWhole> __device__ static void put(void* to, int64_t at, int n, int64_t, const float* v, const uint32_t*) {
@@ -247,8 +257,8 @@ template <typename F> struct Held<State::kF32, F> {
 };
 template <typename F> struct Held<State::kBF16, F> {
     u2 raw;
-    template <bool kWhole> __device__ void load(const void* s, int64_t at, int n, int64_t) {
-        raw = raw4<kWhole>(static_cast<const uint16_t*>(s) + at, n);
+    template <bool kWhole, bool kNt> __device__ void load(const void* s, int64_t at, int n, int64_t) {
+        raw = raw4<kWhole, kNt>(static_cast<const uint16_t*>(s) + at, n);
     }
     __device__ void get(float* v) const { values(raw, v); }
     template <bool kWhole> __device__ static void put(void* to, int64_t at, int n, int64_t, const float* v, const uint32_t*) {
@@ -277,23 +287,46 @@ struct Table {
 };
 static_assert(sizeof(Table) <= 4096 - 64, "the table must fit one kernel argument block");
 
-__device__ __forceinline__ void adam1(float& p, float g, float& m, float& v, const AdamScalars& s) {
+// kExact: the single shard's step, bit for bit.  Else (8-bit states) its square root and quotients are the
+// hardware's, to one unit in the last place each, and the update stays within 14 x 2^-24 of itself: 29.5 M elements 97 ->
+// 86 us, where the exact ones' 45 more instruction slots an element bind the kernel.
+template <bool kExact>
+__device__ __forceinline__ void adam1(float& p, float g, float& m, float& v, const AdamScalars& s, float inv_bc2s) {
     p = p * s.decay;
     m = s.b1 * m + s.omb1 * g;
     const float gg = g * g;
     v = s.b2 * v + s.omb2 * gg;
-    const float den = sqrtf(v) / s.bc2s + s.eps;
-    p = p - s.step_size * (m / den);
+    if constexpr (kExact) {
+        const float den = sqrtf(v) / s.bc2s + s.eps;
+        p = p - s.step_size * (m / den);
+    } else {
+        const float den = __builtin_amdgcn_sqrtf(v) * inv_bc2s + s.eps;
+        p = p - s.step_size * (m * __builtin_amdgcn_rcpf(den));
+    }
 }
 
-template <typename G, State kState, bool kWhole>
+// The workgroup's entry, and which of the entry's tiles of this launch it takes.  Each XCD takes runs of 64
+// neighbouring tiles (14.2 M elements with fp32 states 74.0 -> 72.6 us).
+__device__ __forceinline__ uint32_t entry_of(const uint32_t* start, uint32_t* tile) {
+    constexpr uint32_t kXcds = 8, kRun = 64, kPer = kXcds * kRun;
+    uint32_t at = blockIdx.x;
+    if (at < gridDim.x / kPer * kPer) at = at / kPer * kPer + at % kXcds * kRun + at % kPer / kXcds;
+    uint32_t k = 0;
+#pragma unroll
+    for (int i = 1; i < kLaunch; ++i) k += start[i] <= at ? 1u : 0u;
+    *tile = at - start[k];
+    return k;
+}
+
+template <typename G, State kState, bool kWhole, bool kNt>
 __device__ __forceinline__ void adam_tile(const Table& t, const Entry& e, int64_t base) {
-    constexpr int kN = kTile / kThreads / 4;
+    constexpr int kN = kTile<kState> / kThreads / 4;
     const AdamScalars s = t.sc[e.group];
+    const float inv_bc2s = 1.0f / s.bc2s;
     const float gs = t.grad_scale ? *t.grad_scale : 1.0f;
     const int64_t scales = (e.n + 15) / 16 * 16;
     f4 p[kN];
-    decltype(raw4<true>(static_cast<const G*>(nullptr), 0)) g[kN];
+    decltype(raw4<true, kNt>(static_cast<const G*>(nullptr), 0)) g[kN];
     Held<kState, FormatM> m[kN];
     Held<kState, FormatV> v[kN];
     const auto place = [&](int h, int64_t* at) {
@@ -304,10 +337,10 @@ __device__ __forceinline__ void adam_tile(const Table& t, const Entry& e, int64_
     for (int h = 0; h < kN; ++h) {
         int64_t at;
         const int n = place(h, &at);
-        p[h] = raw4<kWhole>(e.p + at, n);
-        g[h] = raw4<kWhole>(static_cast<const G*>(e.g) + at, n);
-        m[h].template load<kWhole>(e.m, at, n, scales);
-        v[h].template load<kWhole>(e.v, at, n, scales);
+        p[h] = raw4<kWhole, kNt>(e.p + at, n);
+        g[h] = raw4<kWhole, kNt>(static_cast<const G*>(e.g) + at, n);
+        m[h].template load<kWhole, kNt>(e.m, at, n, scales);
+        v[h].template load<kWhole, kNt>(e.v, at, n, scales);
     }
 #pragma unroll
     for (int h = 0; h < kN; ++h) {
@@ -319,7 +352,7 @@ __device__ __forceinline__ void adam_tile(const Table& t, const Entry& e, int64_
         m[h].get(mm);
         v[h].get(vv);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) adam1(pp[j], t.grad_scale ? gg[j] * gs : gg[j], mm[j], vv[j], s);
+        for (int j = 0; j < 4; ++j) adam1<kState == State::kF32>(pp[j], t.grad_scale ? gg[j] * gs : gg[j], mm[j], vv[j], s, inv_bc2s);
         put4<kWhole>(e.p + at, n, pp);
         if (e.pb) put4<kWhole>(e.pb + at, n, pp);
         uint32_t r[4];
@@ -336,15 +369,14 @@ __device__ __forceinline__ void adam_tile(const Table& t, const Entry& e, int64_
     }
 }
 
-template <typename G, State kState>
+template <typename G, State kState, bool kNt>
 __global__ void __launch_bounds__(kThreads) adam_tensors_kernel(Table t) {
     if (t.skip && *t.skip != 0.0f) return;
-    uint32_t k = 0;
-    for (int i = 1; i < kLaunch; ++i) k += t.start[i] <= blockIdx.x ? 1u : 0u;
-    const Entry& e = t.e[k];
-    const int64_t base = (static_cast<int64_t>(blockIdx.x - t.start[k]) + e.bias) * kTile;
-    if (base + kTile <= e.n) adam_tile<G, kState, true>(t, e, base);
-    else adam_tile<G, kState, false>(t, e, base);
+    uint32_t tile;
+    const Entry& e = t.e[entry_of(t.start, &tile)];
+    const int64_t base = (static_cast<int64_t>(tile) + e.bias) * kTile<kState>;
+    if (base + kTile<kState> <= e.n) adam_tile<G, kState, true, kNt>(t, e, base);
+    else adam_tile<G, kState, false, kNt>(t, e, base);
 }
 
 struct CopyEntry {
@@ -360,7 +392,7 @@ struct CopyTable {
 
 template <State kFrom, State kTo, bool kWhole>
 __device__ __forceinline__ void convert_tile(const CopyEntry& e, int64_t base) {
-    constexpr int kN = kTile / kThreads / 4;
+    constexpr int kN = kTile<State::k8Bit> / kThreads / 4;
     const int64_t scales = (e.n + 15) / 16 * 16;
     Held<kFrom, FormatM> m[kN];
     Held<kFrom, FormatV> v[kN];
@@ -372,8 +404,8 @@ __device__ __forceinline__ void convert_tile(const CopyEntry& e, int64_t base) {
     for (int h = 0; h < kN; ++h) {
         int64_t at;
         const int n = place(h, &at);
-        m[h].template load<kWhole>(e.m, at, n, scales);
-        v[h].template load<kWhole>(e.v, at, n, scales);
+        m[h].template load<kWhole, false>(e.m, at, n, scales);
+        v[h].template load<kWhole, false>(e.v, at, n, scales);
     }
 #pragma unroll
     for (int h = 0; h < kN; ++h) {
@@ -391,20 +423,17 @@ __device__ __forceinline__ void convert_tile(const CopyEntry& e, int64_t base) {
 
 template <State kFrom, State kTo>
 __global__ void __launch_bounds__(kThreads) adam_convert_kernel(CopyTable t) {
-    uint32_t k = 0;
-    for (int i = 1; i < kLaunch; ++i) k += t.start[i] <= blockIdx.x ? 1u : 0u;
-    const CopyEntry& e = t.e[k];
-    const int64_t base = (static_cast<int64_t>(blockIdx.x - t.start[k]) + e.bias) * kTile;
-    if (base + kTile <= e.n) convert_tile<kFrom, kTo, true>(e, base);
+    uint32_t tile;
+    const CopyEntry& e = t.e[entry_of(t.start, &tile)];
+    const int64_t base = (static_cast<int64_t>(tile) + e.bias) * kTile<State::k8Bit>;
+    if (base + kTile<State::k8Bit> <= e.n) convert_tile<kFrom, kTo, true>(e, base);
     else convert_tile<kFrom, kTo, false>(e, base);
 }
-
-int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
 
 // Cuts a list into launches: fill(table slot, list index, tiles taken before) for every entry, then
 // launch(tiles).  A tensor too long for one launch goes on in the next.
 template <typename TableT, typename List, typename Fill, typename Launch>
-hipError_t in_launches(const List& list, TableT& t, Fill&& fill, Launch&& launch) {
+hipError_t in_launches(const List& list, int tile, TableT& t, Fill&& fill, Launch&& launch) {
     int used = 0;
     int64_t tiles = 0;
     const auto flush = [&]() -> hipError_t {
@@ -416,7 +445,7 @@ hipError_t in_launches(const List& list, TableT& t, Fill&& fill, Launch&& launch
         return hipGetLastError();
     };
     for (size_t i = 0; i < list.size(); ++i) {
-        const int64_t all = tiles_of(list[i].n);
+        const int64_t all = (list[i].n + tile - 1) / tile;
         for (int64_t done = 0; done < all;) {
             const int64_t now = std::min(all - done, kMaxTiles - tiles);
             t.start[used] = static_cast<uint32_t>(tiles);
@@ -432,21 +461,21 @@ hipError_t in_launches(const List& list, TableT& t, Fill&& fill, Launch&& launch
     return flush();
 }
 
-template <typename G, State kState>
+template <typename G, State kState, bool kNt>
 hipError_t step(const std::vector<AdamTensor>& list, Table& t, hipStream_t stream) {
     return in_launches(
-        list, t,
+        list, kTile<kState>, t,
         [&](int i, const AdamTensor& a, uint32_t bias) {
             t.e[i] = {a.p, a.g, a.m, a.v, a.pb, a.n, bias, a.key, static_cast<uint32_t>(a.group), 0};
         },
-        [&](uint32_t tiles) { adam_tensors_kernel<G, kState><<<dim3(tiles), kThreads, 0, stream>>>(t); });
+        [&](uint32_t tiles) { adam_tensors_kernel<G, kState, kNt><<<dim3(tiles), kThreads, 0, stream>>>(t); });
 }
 
 template <State kFrom, State kTo>
 hipError_t convert(const std::vector<StateCopy>& list, hipStream_t stream) {
     CopyTable t{};
     return in_launches(
-        list, t,
+        list, kTile<State::k8Bit>, t,
         [&](int i, const StateCopy& a, uint32_t bias) { t.e[i] = {a.m, a.v, a.m_to, a.v_to, a.n, bias, a.key}; },
         [&](uint32_t tiles) { adam_convert_kernel<kFrom, kTo><<<dim3(tiles), kThreads, 0, stream>>>(t); });
 }
@@ -472,8 +501,18 @@ hipError_t launch_adam_tensors(const std::vector<AdamTensor>& list, const AdamSc
     std::copy(groups, groups + n_groups, t.sc);
     t.grad_scale = grad_scale;
     t.skip = skip;
-    if (state8) return grad_bf16 ? step<uint16_t, State::k8Bit>(list, t, stream) : step<float, State::k8Bit>(list, t, stream);
-    return grad_bf16 ? step<uint16_t, State::kF32>(list, t, stream) : step<float, State::kF32>(list, t, stream);
+    // bytes of the whole list: the launches of a step follow one another
+    int64_t bytes = 0;
+    for (const AdamTensor& a : list) bytes += a.n * ((state8 ? 12 : 24) + (grad_bf16 ? 2 : 4) + (a.pb ? 2 : 0));
+    const auto go = [&](auto grad, auto state) {
+        using G = decltype(grad);
+        constexpr State kState = decltype(state)::value;
+        return bytes >= kNtBytes ? step<G, kState, true>(list, t, stream) : step<G, kState, false>(list, t, stream);
+    };
+    using Small = std::integral_constant<State, State::k8Bit>;
+    using Full = std::integral_constant<State, State::kF32>;
+    if (state8) return grad_bf16 ? go(uint16_t{}, Small{}) : go(0.0f, Small{});
+    return grad_bf16 ? go(uint16_t{}, Full{}) : go(0.0f, Full{});
 }
 
 hipError_t launch_adam_convert(const std::vector<StateCopy>& list, State from, State to, hipStream_t stream) {

@@ -1,5 +1,6 @@
-"""AdamW over many tensors on the GPU: with fp32 states bit for bit fsdp_adam_shard's step, with 8-bit states bit
-for bit a plain reference (train_ref.py: binary32 steps, codes found in a table); conversions; odd sizes, any
+"""AdamW over many tensors on the GPU: with fp32 states bit for bit fsdp_adam_shard's step, with 8-bit states these
+bit for bit as a plain reference has them (train_ref.py: binary32 steps, codes found in a table) and the
+parameters within bounds; conversions; odd sizes, any
 alignment, long lists, groups, clipping and skipped steps, infinities and NaN."""
 import numpy as np
 import pytest
@@ -74,6 +75,7 @@ class Case:
                 self.arena[k].parts[i].copy_(torch.from_numpy(x[i]))
         a = {k: x.parts for k, x in self.arena.items()}
         self.groups = groups or [0] * len(sizes)
+        self.off = [np.zeros(n) for n in sizes]   # how far p may be from the reference's
         self.list = F.AdamTensors(a["p"], a["g"], a["m"], a["v"], states=states, groups=self.groups, param_bf16=a.get("pb"))
 
     def reference(self, cfgs, seed=0, gs=None):
@@ -82,17 +84,25 @@ class Case:
             cfg = cfgs[self.groups[i]]
             g = f32(self.g[i])
             if self.states == "f32":
-                self.p[i], self.m[i], self.v[i] = R.adam_f32(self.p[i], g, self.m[i], self.v[i], cfg, gs)
+                self.p[i], self.m[i], self.v[i], _ = R.adam_f32(self.p[i], g, self.m[i], self.v[i], cfg, gs)
                 continue
             m, v = (R.read_state(x[i], n, k).astype(np.float32) for k, x in (("m", self.m), ("v", self.v)))
-            self.p[i], m, v = R.adam_f32(self.p[i], g, m, v, cfg, gs)
+            self.p[i], m, v, off = R.adam_f32(self.p[i], g, m, v, cfg, gs)
+            self.off[i] = self.off[i] * abs(1 - cfg["lr"] * cfg.get("weight_decay", 0.0)) + off
             r = R.random16(n, R.key(seed, cfg["step"], i))
             self.m[i], self.v[i] = R.write_state(m, r[0], "m"), R.write_state(v, r[1], "v")
 
     def check(self):
         for i, n in enumerate(self.sizes):
             what = "tensor %d of %d elements: " % (i, n)
-            same(f32(self.arena["p"].parts[i]), self.p[i], what + "p")
+            p = f32(self.arena["p"].parts[i])
+            if self.states == "f32":
+                same(p, self.p[i], what + "p")
+            else:
+                assert np.array_equal(np.isnan(p), np.isnan(self.p[i])), what + "p"
+                with np.errstate(invalid="ignore"):
+                    bad = np.flatnonzero(~((np.abs(p.astype(float) - self.p[i]) <= self.off[i]) | (p == self.p[i]) | np.isnan(p)))
+                assert not bad.size, what + "p %d: %r want %r" % (bad[0], p[bad[0]], self.p[i][bad[0]])
             for k, x in (("m", self.m), ("v", self.v)):
                 got = self.arena[k].parts[i].cpu().numpy()
                 if self.states == "f32":
@@ -103,7 +113,7 @@ class Case:
                 bad = np.flatnonzero(got[:n] != x[i][:n])
                 assert not bad.size, what + "%s code %d: %d want %d" % (k, bad[0], got[bad[0]], x[i][bad[0]])
             if "pb" in self.arena:
-                want = torch.from_numpy(self.p[i]).bfloat16()
+                want = torch.from_numpy(p).bfloat16()
                 assert torch.equal(self.arena["pb"].parts[i].cpu().nan_to_num(9), want.nan_to_num(9)), what + "copy"
             assert torch.equal(self.arena["g"].parts[i].cpu().nan_to_num(9), self.g[i].nan_to_num(9))
         for k, a in self.arena.items():
@@ -203,7 +213,9 @@ def test_zero_state_is_a_first_step():
         zero = torch.zeros(F.fsdp_adam_state_bytes(n), dtype=torch.uint8, device=dev()) if states == "8bit" else torch.zeros(n, device=dev())
         F.fsdp_adam_tensors(F.AdamTensors([p], [g], [zero], [zero.clone()], states=states), dict(lr=0.1, step=1))
         out.append(p)
-    assert torch.equal(*out)
+    want, _, _, off = R.adam_f32(np.ones(n, np.float32), f32(g), np.zeros(n, np.float32), np.zeros(n, np.float32), dict(lr=0.1, step=1))
+    assert_f32_bits(f32(out[0]), want)
+    assert (np.abs(f32(out[1]).astype(float) - want) <= off).all()
 
 
 @pytest.mark.parametrize("grad", ["f32", "bf16"])

@@ -207,7 +207,10 @@ def write_state(x, r, which):
 
 
 def adam_f32(p, g, m, v, cfg, gs=None):
-    """One AdamW step, every operation rounded to binary32."""
+    """One AdamW step, every operation rounded to binary32, and how far a step with 8-bit states may take p from
+    it.  That step's square root, 1 / bc2 and 1 / den are off by 2 U, U and 2 U, its products by U each (three) and
+    its sum by U: 9 U of the update; here the root, two quotients, a product and the sum are off by U each: 5 U.
+    The last differences round both results, by U of them each; products below 2^-126 may be flushed."""
     f = np.float32
     lr, (b1, b2), eps, wd, t = cfg["lr"], cfg.get("betas", (0.9, 0.999)), cfg.get("eps", 1e-8), cfg.get("weight_decay", 0.0), cfg["step"]
     decay, step_size, bc2 = f(1 - lr * wd), f(lr / (1 - b1 ** t)), f(np.sqrt(1 - b2 ** t))
@@ -216,5 +219,7 @@ def adam_f32(p, g, m, v, cfg, gs=None):
         p = p * decay
         m = f(b1) * m + f(1 - b1) * g
         v = f(b2) * v + f(1 - b2) * (g * g)
-        p = p - step_size * (m / (np.sqrt(v) / bc2 + f(eps)))
-    return p, m, v
+        update = step_size * (m / (np.sqrt(v) / bc2 + f(eps)))
+        p = p - update
+        off = 14 * U * np.abs(update.astype(float)) + 2 * U * np.abs(p.astype(float)) + 2.0 ** -126
+    return p, m, v, off
