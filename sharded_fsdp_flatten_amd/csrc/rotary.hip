@@ -1,9 +1,9 @@
 // rotary.hip -- rotary positions of queries and keys, forward and backward.
 //
-// Pair i of a head at position x turns by w = x f_i: (a, b) -> (a cos w - b sin w, a sin w + b cos w).
-// The cosine and sine of a (token, pair) serve every head, so a lane owns eight pairs of a token and walks
-// its heads with sixteen numbers in registers; q and k share them in one launch.  Bound by HBM: every
-// element is read and written once.
+// Pair i of a head at position x turns by w = x f_i: (a, b) -> (a cos w - b sin w, a sin w + b cos w).  The
+// cosine and sine of a (token, pair) serve every head: a workgroup takes a few tokens, computes theirs once into
+// LDS, one a thread, and then walks the tokens' heads of q and k with them.  Bound by HBM: every element is
+// read and written once.
 #include <algorithm>
 
 #include "layer_dev.h"
@@ -13,119 +13,207 @@ namespace fsdp {
 namespace {
 
 constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
+constexpr int kPairs = 2048;                      // cosines and sines of a workgroup (16 KB of LDS)
 
-// Lanes of a workgroup: `lanes` of them own a head (its vectors of 8 pairs, then the vectors of 8
-// elements behind the rotated ones), `slots` heads side by side, `per` tokens a workgroup.
+// 16 bytes, at any element
+template <typename T> constexpr int kE = 16 / sizeof(T);
+template <bool kNt>
+__device__ __forceinline__ u4 load16(const void* p) {
+    return kNt ? __builtin_nontemporal_load(static_cast<const u4e*>(p)) : *static_cast<const u4e*>(p);
+}
+__device__ __forceinline__ void put16(void* p, u4 w) { __builtin_nontemporal_store(w, static_cast<u4e*>(p)); }
+__device__ __forceinline__ void values(u4 w, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __builtin_bit_cast(float, w[j] << 16);
+        v[2 * j + 1] = __builtin_bit_cast(float, w[j] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void values(u4 w, float (&v)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __builtin_bit_cast(float, static_cast<uint32_t>(w[j]));
+}
+__device__ __forceinline__ u4 packed(const float (&v)[8]) {
+    u4 w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v[2 * j], v[2 * j + 1]}), bf2));
+    return w;
+}
+__device__ __forceinline__ u4 packed(const float (&v)[4]) {
+    u4 w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __builtin_bit_cast(uint32_t, v[j]);
+    return w;
+}
+// the first n elements of a vector (kWhole: all of them)
+template <bool kWhole, bool kNt, typename T>
+__device__ __forceinline__ u4 load_some(const T* p, int n) {
+    if (kWhole || n >= kE<T>) return load16<kNt>(p);
+    u4 w = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < kE<T>; ++j) {
+        if (j >= n) break;
+        if constexpr (sizeof(T) == 2) w[j >> 1] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
+        else w[j] = __builtin_bit_cast(uint32_t, static_cast<float>(p[j]));
+    }
+    return w;
+}
+template <bool kWhole, typename T>
+__device__ __forceinline__ void put_some(T* p, u4 w, int n) {
+    if (kWhole || n >= kE<T>) return put16(p, w);
+#pragma unroll
+    for (int j = 0; j < kE<T>; ++j) {
+        if (j >= n) break;
+        if constexpr (sizeof(T) == 2) p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+        else p[j] = __builtin_bit_cast(float, static_cast<uint32_t>(w[j]));
+    }
+}
+
+// kP cosines or sines; kWhole: aligned to as many.
+template <bool kWhole, int kP>
+__device__ __forceinline__ void angles(const float* p, float (&v)[kP]) {
+    if constexpr (kWhole && kP >= 4) {
+#pragma unroll
+        for (int j = 0; j < kP; j += 4) {
+            const f4 w = *reinterpret_cast<const f4*>(p + j);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[j + q] = w[q];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kP; ++j) v[j] = p[j];
+    }
+}
+
+// `lanes` threads take a head: first those of its pairs (kE pairs each in the half layout, whose two vectors lie
+// half apart, kE / 2 in the interleaved one, whose pairs are one vector), then one a vector behind the rotated
+// elements; `across` of them are there (a head may need more than a workgroup has).  `slots` heads go side by
+// side, `per` tokens a workgroup.
 struct RotaryShape {
-    int pair_vecs, lanes, slots, per;
+    int pair_lanes, lanes, across, slots, per;
 };
 
-template <typename T, bool kInter>
+template <typename T, bool kInter, bool kWhole, bool kNt>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(Rotary a, RotaryShape s, int64_t token0) {
-    const int lane = threadIdx.x % s.lanes, slot = threadIdx.x / s.lanes;
-    if (slot >= s.slots) return;
-    const int all = static_cast<int>(a.heads + a.kv_heads);
-    const int across = s.per > 1 ? slot / all : 0;           // which of the workgroup's tokens
-    if (across >= s.per) return;
-    const int64_t token = token0 + static_cast<int64_t>(blockIdx.x) * s.per + across;
-    if (token >= a.batch * a.tokens) return;
-    const int64_t b = token / a.tokens, t = token - b * a.tokens;
+    constexpr int kV = kE<T>, kP = kInter ? kV / 2 : kV;   // elements of a vector, pairs of a lane
+    __shared__ alignas(16) float cs[kPairs + 16], sn[kPairs + 16];
     const int half = a.rot / 2;
-    const bool rotates = lane < s.pair_vecs;
-    const int first = rotates ? lane * kV : a.rot + (lane - s.pair_vecs) * kV;  // pair, or element
-    const int n = min(kV, rotates ? half - first : a.head_dim - first);
-    float c[kV], sn[kV];
-    if (rotates) {
-        const double x = static_cast<double>(a.positions ? a.positions[token] : a.start + t);
-#pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            c[j] = sn[j] = 0.0f;
-            if (j < n) {
-                const double turns = x * a.freqs[first + j] * kTurn;
-                const float r = static_cast<float>(turns - __builtin_rint(turns));
-                float si, co;
-                sincospif(2.0f * r, &si, &co);
-                c[j] = co * a.scale;
-                sn[j] = si * a.scale * a.sign;
-            }
-        }
-    }
-    const int step = s.per > 1 ? all : s.slots;
-    for (int h = s.per > 1 ? slot - across * all : slot; h < all; h += step) {
-        const bool is_q = h < a.heads;
-        const Heads& from = is_q ? a.q : a.k;
-        const Heads& to = is_q ? a.q_out : a.k_out;
-        const int64_t hh = is_q ? h : h - a.heads;
-        const T* x = static_cast<const T*>(from.p) + b * from.batch + t * from.token + hh * from.head;
-        T* y = static_cast<T*>(to.p) + b * to.batch + t * to.token + hh * to.head;
-        if (!rotates) {
-            if (x == y) continue;
-            Vec<T> v;
-            vload<false>(v, x + first, n);
-            vstore(v, y + first, n);
-            continue;
-        }
-        // a pair's elements are `half` apart, or next to each other
-        Vec<T> u, w;
-        float p[kV], q[kV];
-        if constexpr (kInter) {
-            vload<false>(u, x + 2 * first, 2 * n);
-            vload<false>(w, x + 2 * first + kV, 2 * n - kV);
-            float e[2 * kV];
-            u.get(e);
-            w.get(e + kV);
-#pragma unroll
-            for (int j = 0; j < kV; ++j) {
-                const float A = e[2 * j], B = e[2 * j + 1];
-                e[2 * j] = A * c[j] - B * sn[j];
-                e[2 * j + 1] = A * sn[j] + B * c[j];
-            }
-            put8(y + 2 * first, e, 2 * n);
-            put8(y + 2 * first + kV, e + kV, 2 * n - kV);
+    const int64_t first = token0 + static_cast<int64_t>(blockIdx.x) * s.per;
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(s.per), a.batch * a.tokens - first));
+    // sequence and token of the workgroup's first, the same in every lane; the others count on from it
+    const int64_t b0 = first / a.tokens, t0 = first - b0 * a.tokens;
+    for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
+        const int tok = i / half, pair = i - tok * half;
+        int64_t x;
+        if (a.positions) {
+            x = a.positions[first + tok];
         } else {
-            vload<false>(u, x + first, n);
-            vload<false>(w, x + half + first, n);
-            u.get(p);
-            w.get(q);
+            for (x = t0 + tok; x >= a.tokens;) x -= a.tokens;
+            x += a.start;
+        }
+        const double turns = static_cast<double>(x) * a.freqs[pair] * kTurn;
+        float si, co;
+        sincospif(2.0f * static_cast<float>(turns - __builtin_rint(turns)), &si, &co);
+        cs[i] = co * a.scale;
+        sn[i] = si * a.scale * a.sign;
+    }
+    __syncthreads();
+    const int lane0 = threadIdx.x % s.across, slot = threadIdx.x / s.across;
+    if (slot >= s.slots) return;
+    const int heads = static_cast<int>(a.heads), all = heads + static_cast<int>(a.kv_heads);
+    for (int lane = lane0; lane < s.lanes; lane += s.across) {
+        const bool rotates = lane < s.pair_lanes;
+        // where the lane's (first) vector starts, and how many pairs or elements are left from there
+        const int pair = lane * kP;
+        const int at = rotates ? (kInter ? 2 * pair : pair) : a.rot + (lane - s.pair_lanes) * kV;
+        const int n = rotates ? min(half - pair, kP) : min(a.head_dim - at, kV);
+        int tok = slot / all, h = slot - tok * all;
+        int64_t b = b0, t = t0 + tok;
+        while (tok < tokens) {
+            for (; t >= a.tokens; t -= a.tokens) ++b;
+            const Heads& from = h < heads ? a.q : a.k;
+            const Heads& to = h < heads ? a.q_out : a.k_out;
+            const int hh = h < heads ? h : h - heads;
+            const T* x = static_cast<const T*>(from.p) + b * from.batch + t * from.token + hh * from.head + at;
+            T* y = static_cast<T*>(to.p) + b * to.batch + t * to.token + hh * to.head + at;
+            if (rotates) {
+                const u4 u = load_some<kWhole, kNt>(x, kInter ? 2 * n : n);
+                u4 w;
+                if constexpr (!kInter) w = load_some<kWhole, kNt>(x + half, n);
+                float c[kP], z[kP], p[kV];
+                angles<kWhole>(cs + tok * half + pair, c);
+                angles<kWhole>(sn + tok * half + pair, z);
+                values(u, p);
+                if constexpr (kInter) {
 #pragma unroll
-            for (int j = 0; j < kV; ++j) {
-                const float A = p[j], B = q[j];
-                p[j] = A * c[j] - B * sn[j];
-                q[j] = A * sn[j] + B * c[j];
+                    for (int j = 0; j < kP; ++j) {
+                        const float A = p[2 * j], B = p[2 * j + 1];
+                        p[2 * j] = A * c[j] - B * z[j];
+                        p[2 * j + 1] = A * z[j] + B * c[j];
+                    }
+                    put_some<kWhole>(y, packed(p), 2 * n);
+                } else {
+                    float q[kV];
+                    values(w, q);
+#pragma unroll
+                    for (int j = 0; j < kP; ++j) {
+                        const float A = p[j], B = q[j];
+                        p[j] = A * c[j] - B * z[j];
+                        q[j] = A * z[j] + B * c[j];
+                    }
+                    put_some<kWhole>(y, packed(p), n);
+                    put_some<kWhole>(y + half, packed(q), n);
+                }
+            } else if (x != y) {
+                put_some<kWhole>(y, load_some<kWhole, kNt>(x, n), n);
             }
-            put8(y + first, p, n);
-            put8(y + half + first, q, n);
+            for (h += s.slots; h >= all; h -= all) {
+                ++tok;
+                ++t;
+            }
         }
     }
 }
 
 constexpr int64_t kMaxBlocks = int64_t{1} << 22;  // of 256 threads: a grid's threads fit 32 bits
 
-}  // namespace
-
-hipError_t launch_rotary(const Rotary& a, hipStream_t stream) {
+template <typename T, bool kInter>
+hipError_t rotate(const Rotary& a, hipStream_t stream) {
+    constexpr int kV = kE<T>, kP = kInter ? kV / 2 : kV;
     RotaryShape s;
-    s.pair_vecs = (a.rot / 2 + kV - 1) / kV;
-    s.lanes = s.pair_vecs + (a.head_dim - a.rot + kV - 1) / kV;
-    // heads longer than a workgroup's lanes are cut by the caller's limit on head_dim
-    s.slots = std::max(1, kThreads / s.lanes);
-    const int64_t all = a.heads + a.kv_heads;
-    s.per = static_cast<int>(std::max<int64_t>(1, s.slots / all));
-    const int64_t tokens = a.batch * a.tokens;
-    for (int64_t t0 = 0; t0 < tokens; t0 += kMaxBlocks * s.per) {
-        const int64_t blocks = (std::min(tokens - t0, kMaxBlocks * s.per) + s.per - 1) / s.per;
-        const dim3 grid(static_cast<uint32_t>(blocks));
-        if (a.bf16) {
-            if (a.interleaved) rotary_kernel<uint16_t, true><<<grid, kThreads, 0, stream>>>(a, s, t0);
-            else rotary_kernel<uint16_t, false><<<grid, kThreads, 0, stream>>>(a, s, t0);
+    const int half = a.rot / 2, rest = a.head_dim - a.rot;
+    s.pair_lanes = (half + kP - 1) / kP;
+    s.lanes = s.pair_lanes + (rest + kV - 1) / kV;
+    s.across = std::min(s.lanes, kThreads);
+    s.slots = kThreads / s.across;
+    const bool whole = half % kP == 0 && rest % kV == 0;
+    const int64_t all = a.heads + a.kv_heads, tokens = a.batch * a.tokens;
+    // about four vectors a thread, but workgroups for the whole device
+    int64_t per = std::max<int64_t>(1, 4 * kThreads / (all * s.lanes));
+    per = std::min({per, std::max<int64_t>(1, tokens / 512), static_cast<int64_t>(kPairs / half)});
+    s.per = static_cast<int>(per);
+    const bool nt = 2 * tokens * all * a.head_dim * static_cast<int64_t>(sizeof(T)) >= kNtBytes;
+    for (int64_t t0 = 0; t0 < tokens; t0 += kMaxBlocks * per) {
+        const dim3 grid(static_cast<uint32_t>((std::min(tokens - t0, kMaxBlocks * per) + per - 1) / per));
+        if (whole) {
+            if (nt) rotary_kernel<T, kInter, true, true><<<grid, kThreads, 0, stream>>>(a, s, t0);
+            else rotary_kernel<T, kInter, true, false><<<grid, kThreads, 0, stream>>>(a, s, t0);
         } else {
-            if (a.interleaved) rotary_kernel<float, true><<<grid, kThreads, 0, stream>>>(a, s, t0);
-            else rotary_kernel<float, false><<<grid, kThreads, 0, stream>>>(a, s, t0);
+            if (nt) rotary_kernel<T, kInter, false, true><<<grid, kThreads, 0, stream>>>(a, s, t0);
+            else rotary_kernel<T, kInter, false, false><<<grid, kThreads, 0, stream>>>(a, s, t0);
         }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_rotary(const Rotary& a, hipStream_t stream) {
+    if (a.bf16) return a.interleaved ? rotate<uint16_t, true>(a, stream) : rotate<uint16_t, false>(a, stream);
+    return a.interleaved ? rotate<float, true>(a, stream) : rotate<float, false>(a, stream);
 }
 
 }  // namespace fsdp
