@@ -80,7 +80,7 @@ def test_head_sizes(D, rot, dtype, layout):
     check((2, 5, 3, D), 2, rot, dtype, layout, seed=D + rot)
 
 
-@pytest.mark.parametrize("H,kv", [(1, 0), (1, 1), (2, 1), (5, 3), (8, 8), (31, 2), (40, 0), (96, 96), (130, 1)])
+@pytest.mark.parametrize("H,kv", [(1, 0), (1, 1), (2, 1), (5, 3), (8, 8), (31, 2), (40, 0), (96, 96), (130, 1), (200, 57)])
 @pytest.mark.parametrize("n", [1, 2, 33])
 def test_heads_and_tokens(H, kv, n):
     check((3, n, H, 64), kv, 64, "bf16", seed=H)
