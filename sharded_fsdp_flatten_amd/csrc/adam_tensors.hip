@@ -22,7 +22,7 @@ constexpr int kThreads = 256;
 // ones and fp32 gradients 67.3 / 62.8 / 65.8.
 template <State kState> constexpr int kTile = kThreads * (kState == State::kF32 ? 4 : 8);
 constexpr int kLaunch = 50;           // tensors of a launch (kernel-argument budget)
-constexpr int64_t kMaxTiles = int64_t{1} << 22;
+constexpr int64_t kMaxTiles = int64_t{1} << 20;   // of a launch
 
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u2e __attribute__((ext_vector_type(2), aligned(2)));

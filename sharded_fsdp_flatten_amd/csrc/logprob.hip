@@ -370,19 +370,21 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
             }
         }
         const float r = anchor(top, k), d = fmaxf(anchor(p.m, k) - r, -1000.0f), f = __builtin_amdgcn_exp2f(d);
-        if (kEntropy) p.t = f * (p.t + d * p.s);
-        p.s *= f;
-        p.m = top;
+        // the step's own sums first: 32 terms, then one sum a step, instead of one long chain of roundings
+        float sum = 0.0f, sum_u = 0.0f;
 #pragma unroll
         for (int j = 0; j < kU; ++j) {
             if (!kWhole && i + j * kT >= nv) break;
 #pragma unroll
             for (int q = 0; q < kV; ++q) {
                 const float u = fmaf(v[j][q], k, -r), e = __builtin_amdgcn_exp2f(u);
-                p.s += e;
-                if (kEntropy) p.t += weighted(e, u);
+                sum += e;
+                if (kEntropy) sum_u += weighted(e, u);
             }
         }
+        if (kEntropy) p.t = f * (p.t + d * p.s) + sum_u;
+        p.s = p.s * f + sum;
+        p.m = top;
     };
     // a segment's lanes go together, so that its maximum meets
     constexpr uint32_t kLast = kTop ? kSeg - 1 : 0;

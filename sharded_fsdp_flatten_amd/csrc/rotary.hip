@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(Rotary a, RotaryShape 
     }
 }
 
-constexpr int64_t kMaxBlocks = int64_t{1} << 22;  // of 256 threads: a grid's threads fit 32 bits
+constexpr int64_t kMaxBlocks = int64_t{1} << 20;  // of a launch
 
 template <typename T, bool kInter>
 hipError_t rotate(const Rotary& a, hipStream_t stream) {

@@ -143,22 +143,21 @@ def fsdp_rotary_freqs(rot: int, base: float = 10000.0, *, scaling: str = "none",
     return out
 
 
-def _heads(t, name: str, batch: int, tokens: int, heads: int, dim: int, dtype, device: int):
-    """(address, batch, token and head pitch) of [batch, tokens, heads, dim] or [tokens, heads, dim]."""
-    if not isinstance(t, L._Tensor) or t.get_device() != device or not t.is_cuda:
+def _heads(t, name: str, shape, dtype, device: int):
+    """(address, batch, token and head pitch) of a tensor of heads of this shape."""
+    if not isinstance(t, L._Tensor) or t.get_device() != device:
         L._refuse(t, name, device)
     if t.dtype is not dtype:
         raise TypeError("%s is %s, the others are %s" % (name, t.dtype, dtype))
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 3:
-        shape, stride = (1, *shape), (0, *stride)
-    if tuple(shape) != (batch, tokens, heads, dim):
-        raise ValueError("%s has shape %s, %s is needed"
-                         % (name, tuple(t.shape), (batch, tokens, heads, dim)))
-    if dim > 1 and stride[3] != 1:
-        raise ValueError("the elements of a head of %s must be next to each other, got stride %d"
-                         % (name, stride[3]))
-    return t.data_ptr(), stride[0], stride[1], stride[2]
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, %s is needed" % (name, tuple(t.shape), tuple(shape)))
+    if len(shape) == 4:
+        b, n, h, e = t.stride()
+    else:
+        b, (n, h, e) = 0, t.stride()
+    if e != 1 and shape[-1] > 1:
+        raise ValueError("the elements of a head of %s must be next to each other, got stride %d" % (name, e))
+    return t.data_ptr(), b, n, h
 
 
 def _rotary(fn, q, q_out, freqs, k, k_out, positions, start, layout, scale, stream):
@@ -167,28 +166,34 @@ def _rotary(fn, q, q_out, freqs, k, k_out, positions, start, layout, scale, stre
     code = L._dtype_code(q, "q")
     if not q.is_cuda:
         L._refuse(q, "q", 0)
-    if q.dim() not in (3, 4):
+    shape, t, dev = q.shape, q.dtype, q.get_device()
+    if len(shape) == 4:
+        batch, tokens, heads, dim = shape
+    elif len(shape) == 3:
+        batch, (tokens, heads, dim) = 1, shape
+    else:
         raise ValueError("q must be [batch, tokens, heads, head_dim] or [tokens, heads, head_dim]")
-    batch, tokens, heads, dim = q.shape if q.dim() == 4 else (1, *q.shape)
-    t, dev = q.dtype, q.get_device()
-    if (k is None) != (k_out is None):
-        raise TypeError("k and k_out must be given together")
-    kv, kin, kout = 0, _NO_HEADS, _NO_HEADS
-    if k is not None:
-        if not isinstance(k, L._Tensor) or k.dim() != q.dim():
-            raise ValueError("k must have as many dimensions as q")
-        kv = k.shape[-2]
-        kin = _heads(k, "k", batch, tokens, kv, dim, t, dev)
-        kout = _heads(k_out, "k_out", batch, tokens, kv, dim, t, dev)
-    rot = 2 * freqs.numel() if isinstance(freqs, L._Tensor) else 0
-    f = L._vector(freqs, "freqs", rot // 2, dev, _f64)
-    if not f:
+    if k is None:
+        if k_out is not None:
+            raise TypeError("k and k_out must be given together")
+        kv, kin, kout = 0, _NO_HEADS, _NO_HEADS
+    else:
+        if k_out is None:
+            raise TypeError("k and k_out must be given together")
+        kshape = getattr(k, "shape", ())
+        if len(kshape) != len(shape) or kshape[:-2] != shape[:-2] or kshape[-1] != dim:
+            raise ValueError("k must have the shape of q but for the number of heads, got %s" % (tuple(kshape),))
+        kv = kshape[-2]
+        kin = _heads(k, "k", kshape, t, dev)
+        kout = _heads(k_out, "k_out", kshape, t, dev)
+    if not isinstance(freqs, L._Tensor):
         raise TypeError("freqs must be a tensor, got %r" % type(freqs))
-    cfg = _ROTARY_CFG.pack(batch, tokens, heads, kv, dim, rot, start, code,
+    pairs = freqs.numel()
+    cfg = _ROTARY_CFG.pack(batch, tokens, heads, kv, dim, 2 * pairs, start, code,
                            L._kind(layout, _LAYOUTS, "layout"), scale, 0)
-    io = _ROTARY_IO.pack(*_heads(q, "q", batch, tokens, heads, dim, t, dev),
-                         *_heads(q_out, "q_out", batch, tokens, heads, dim, t, dev), *kin, *kout,
-                         L._vector(positions, "positions", batch * tokens, dev, _i64), f)
+    io = _ROTARY_IO.pack(*_heads(q, "q", shape, t, dev), *_heads(q_out, "q_out", shape, t, dev), *kin, *kout,
+                         0 if positions is None else L._vector(positions, "positions", batch * tokens, dev, _i64),
+                         L._vector(freqs, "freqs", pairs, dev, _f64))
     L._call(fn, dev, stream, cfg, io)
 
 
@@ -197,13 +202,13 @@ def fsdp_rotary_forward(q, q_out, freqs, *, k=None, k_out=None, positions=None, 
     """Rotate the first 2 len(freqs) elements of every head of q, and of k where given, by their positions.
     Heads are [batch, tokens, heads, head_dim] or [tokens, heads, head_dim], of any strides but the last;
     the outputs may be the inputs.  positions: int64, one a token (else start + the token's number)."""
-    _rotary(_lib().fsdp_rotary_forward, q, q_out, freqs, k, k_out, positions, start, layout, scale, stream)
+    _rotary((_fn or _lib()).fsdp_rotary_forward, q, q_out, freqs, k, k_out, positions, start, layout, scale, stream)
 
 
 def fsdp_rotary_backward(dq, dq_out, freqs, *, k=None, k_out=None, positions=None, start: int = 0,
                          layout: str = "half", scale: float = 1.0, stream=None) -> None:
     """Gradients of fsdp_rotary_forward's inputs from those of its outputs, with the same arguments."""
-    _rotary(_lib().fsdp_rotary_backward, dq, dq_out, freqs, k, k_out, positions, start, layout, scale,
+    _rotary((_fn or _lib()).fsdp_rotary_backward, dq, dq_out, freqs, k, k_out, positions, start, layout, scale,
             stream)
 
 
