@@ -731,16 +731,16 @@ FSDP_API fsdp_status fsdp_rotary_freqs(int64_t rot, double base, int32_t scaling
 /*
  * Rotate pair (a, b) of every head of q and k at position x by the angle w = x f_i:
  *   (a, b) -> scale (a cos w - b sin w, a sin w + b cos w)
- * The angle is reduced in binary64: with |x f_i| up to 2^30 it is within 2^-21 of a
- * turn's radian even at the end of a long context; cosine and sine are
- * binary32, results rounded once.  Elements behind the rotated ones are copied bit for
- * bit (in place: left alone).  In place, no other operand may overlap.
+ * w is computed and reduced to a turn in binary64 (within |w| 2^-51), its fraction of a turn rounded to
+ * binary32 (2^-26 of a turn); cosine and sine are binary32, results rounded once.  Elements behind the
+ * rotated ones are copied bit for bit (in place: left alone).  In place, no other operand may overlap.
  * An output's heads, tokens and sequences must not overlap: of the pitches with more than one
  * entry, each from the smallest up must pass the extent of those before it.
  * batch, tokens or heads + kv_heads == 0: nothing is done.
  * Errors: FSDP_E_ARG (NULL cfg or io; with elements, a NULL buffer or freqs),
  * FSDP_E_RANGE (sizes negative, rot, head_dim, dtype, layout, scale, pitches),
- * FSDP_E_ALIGN, FSDP_E_OVERFLOW (an extent or the number of elements beyond int64), FSDP_E_HIP.
+ * FSDP_E_ALIGN, FSDP_E_OVERFLOW (an extent, a position from start or the number of elements beyond
+ * int64), FSDP_E_HIP.
  */
 FSDP_API fsdp_status fsdp_rotary_forward(const fsdp_rotary_cfg* cfg, const fsdp_rotary_io* io,
                                          void* stream);
@@ -761,7 +761,7 @@ typedef struct {
     int64_t rows, cols;        /* cols: the vocabulary, <= 2^30                             */
     int32_t dtype;             /* of the logits and their gradient                          */
     int32_t top;               /* forward: alternatives wanted, 0..FSDP_LOGPROB_MAX_TOP, <= cols */
-    float scale;               /* finite, > 0: the logits are multiplied by it (1 / temperature) */
+    float scale;               /* > 0, at most 2^127: the logits are multiplied by it (1 / temperature) */
     int32_t reserved;          /* ignored; set it to 0                                      */
 } fsdp_logprob_cfg;
 
@@ -805,10 +805,11 @@ FSDP_API fsdp_status fsdp_logprob_workspace(int64_t rows, int64_t cols, int32_t 
  * max is rounded, and logsum is of the rounded one: their sum is the logarithm of the sum of
  * e^z_j.  Sums are binary32.
  * A token outside [0, cols) is none (a padded position): its logprob is 0.
- * Logits of -infinity are masked: their probability is 0, and their logprob -infinity.  A
- * row that holds nothing else (or only logits whose product with scale is -infinity in binary32) has max -infinity, logsum 0, entropy 0 and every logprob
- * -infinity.  A row that holds a NaN or +infinity (or a product that is) has NaN for logsum, entropy and every logprob
- * (tokens that are none apart); a NaN is ranked as -infinity.
+ * Logits of -infinity are masked: their probability is 0, and their logprob -infinity.  A row that holds
+ * nothing else (or only logits whose product with scale is -infinity in binary32) has max -infinity,
+ * logsum 0, entropy 0 and every logprob -infinity.  A row that holds a NaN or +infinity (or a product that
+ * is) has NaN for logsum, entropy and every logprob (tokens that are none apart); a NaN is ranked as
+ * -infinity.
  * Every partial result read was written by the same call: the workspace needs no clearing,
  * and calls that share one must be ordered.
  * rows or cols == 0: nothing is written.
@@ -898,8 +899,9 @@ FSDP_API fsdp_status fsdp_adam_state_bytes(int64_t numel, int64_t* bytes);
  *   tensors : host array of n_tensors, groups : host array of n_groups; both are read during
  *             the call.
  * No two tensors may overlap.  The list is cut into as many launches as its table needs (50
- * tensors a launch).
- * Errors: FSDP_E_ARG (NULL list; NULL tensors or groups with tensors; a NULL buffer of a tensor
+ * tensors a launch).  A captured call keeps its step numbers, on which bias corrections and random numbers
+ * rest, so that only a replay of the same step repeats it rightly.
+ * Errors: FSDP_E_ARG (NULL list or groups; NULL tensors with n_tensors; a NULL buffer of a tensor
  * with elements), FSDP_E_RANGE (n_tensors negative, n_groups outside
  * 1..FSDP_ADAM_MAX_GROUPS, state_format, grad_dtype, a numel negative, a tensor's group, a group's
  * values as for fsdp_adam_shard), FSDP_E_ALIGN, FSDP_E_OVERFLOW (numel > 2^40), FSDP_E_HIP.
@@ -912,7 +914,7 @@ FSDP_API fsdp_status fsdp_adam_tensors(const fsdp_adam_list* list, const fsdp_ad
  * FSDP_STATE_8BIT: to save 8-bit states, or to start from others.  From 8 bits the values are exact
  * (in bf16 as well); to 8 bits they are rounded as by a step of the number `step` with the
  * same seed.  Only numel, exp_avg and exp_avg_sq of the tensors are read; exp_avg_sq must hold
- * no negative values.  numel has to be the same in both lists.
+ * no negative values.  numel has to be the same in both lists, and no buffer of one may overlap another.
  * Errors: FSDP_E_ARG (NULL arrays or buffers), FSDP_E_RANGE (n_tensors, the formats, numel, step < 1),
  * FSDP_E_ALIGN, FSDP_E_OVERFLOW, FSDP_E_HIP.
  */

@@ -4,7 +4,8 @@
 // A launch carries a table of tensors in its arguments; a workgroup takes one tile of one tensor.  With
 // fp32 states every element takes the operations of the single shard's step, each rounded on its own.
 // 8-bit states (m: e4m3, v: e5m3, a power-of-two scale for 32 elements) are read, updated in fp32, and
-// rounded at random to codes again.  Bound by HBM: 28 bytes an element with fp32 states, 16.1 with 8-bit ones.
+// rounded at random to codes again.  Bound by HBM: 28 bytes an element with fp32 states and
+// gradients, 16.1 with 8-bit states (2 less with bf16 gradients, 2 more with a bf16 copy).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -170,7 +171,8 @@ __device__ __forceinline__ void put4(uint16_t* p, int n, const float* v) {
 // queued one after another over three sets of operands, cached / nt, us: fp32 states 75 MB 14.3 / 16.0, 150 MB 27.1 /
 // 28.8, 425 MB 82.9 / 73.9, 900 MB 168 / 152; 8-bit ones 91 MB 18.6 / 18.9, 257 MB 51.6 / 44.6, 544 MB 103 / 86.  (Alone after a
 // read of 1 GiB cached loads look better, 69.6 against 77.8 us for 425 MB: then up to 256 MB of what was written
-// is still on its way when the kernel ends, and the next one pays.)  Codes and scales are always read through the cache (nt 8% slower).
+// is still on its way when the kernel ends, and the next one pays.)  Codes and scales
+// are always read through the cache (nt 8% slower).
 constexpr int64_t kNtBytes = int64_t{192} << 20;
 
 // Raw loads of four elements, n of them inside the tensor (kWhole: all), so that a tile's loads are all issued

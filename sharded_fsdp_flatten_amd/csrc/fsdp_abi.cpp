@@ -330,6 +330,9 @@ fsdp_status rotary_impl(const fsdp_rotary_cfg* c, const fsdp_rotary_io* io, floa
     if (c->batch == 0 || c->tokens == 0 || heads == 0) return ok();
     if (c->tokens > INT64_MAX / 8 / c->batch / heads / c->head_dim)
         return fail(FSDP_E_OVERFLOW, "batch x tokens x heads x head_dim overflows int64");
+    int64_t last;
+    if (!io->positions && __builtin_add_overflow(c->start, c->tokens - 1, &last))
+        return fail(FSDP_E_OVERFLOW, "start + tokens overflows int64");
     const size_t e = elem_size(c->dtype);
     const auto check = [&](const fsdp_heads& x, int64_t n, bool out, const char* name) {
         return n == 0 ? FSDP_OK : check_heads(x, c->batch, c->tokens, n, c->head_dim, e, out, name);
@@ -369,8 +372,9 @@ fsdp_status check_logprob(const fsdp_logprob_cfg* c) {
     fsdp_status s;
     if ((s = check_extent(c->rows, c->cols)) != FSDP_OK || (s = check_dtype(c->dtype, "dtype")) != FSDP_OK)
         return s;
-    if (!std::isfinite(c->scale) || c->scale <= 0.0f)
-        return fail(FSDP_E_RANGE, "scale must be finite and above 0");
+    // (the kernels' scale log2 e is finite then)
+    if (!(c->scale > 0.0f && c->scale <= 0x1p127f))
+        return fail(FSDP_E_RANGE, "scale must be above 0 and at most 2^127");
     return FSDP_OK;
 }
 

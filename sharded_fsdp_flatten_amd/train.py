@@ -278,8 +278,9 @@ def fsdp_adam_state_bytes(numel: int) -> int:
 
 
 class AdamTensors:
-    """A list of tensors with their gradients and states, as the C ABI takes it; it keeps the tensors, whose
-    addresses must stay.  params (fp32), grads (all fp32 or all bf16), exp_avgs and exp_avg_sqs by `states`:
+    """A list of tensors with their gradients and states, as the C ABI takes it.  It holds the tensors' memory
+    as it was when the list was made: where a parameter or gradient is replaced by another tensor, make a new
+    list.  In a list that a call writes no two params, states or copies may overlap.  params (fp32), grads (all fp32 or all bf16), exp_avgs and exp_avg_sqs by `states`:
     "f32" and "bf16" tensors of as many elements, "8bit" uint8 tensors of fsdp_adam_state_bytes.  groups:
     each tensor's index into the hyper-parameters of a step (default 0).  param_bf16: a list, entries may
     be None.  For fsdp_adam_convert params and grads may be None."""
@@ -319,7 +320,11 @@ class AdamTensors:
             if not isinstance(exp_avgs[0], L._Tensor) or not exp_avgs[0].is_cuda:
                 L._refuse(exp_avgs[0], "exp_avgs[0]", 0)
             self.device = exp_avgs[0].get_device()
-        self.numels = [t.numel() for t in (lists["params"] if self.steps else exp_avgs)]
+        sized = "params" if self.steps else "exp_avgs"
+        for i, t in enumerate(lists[sized]):
+            if not isinstance(t, L._Tensor):
+                L._refuse(t, "%s[%d]" % (sized, i), 0)
+        self.numels = [t.numel() for t in lists[sized]]
         dev = self.device
         table = (fsdp_adam_tensor * max(1, n))()
         for i in range(n):
@@ -334,7 +339,13 @@ class AdamTensors:
                 e.grad = L._vector(lists["grads"][i], "grads[%d]" % i, k, dev, gdtype)
             if param_bf16 is not None and lists["param_bf16"][i] is not None:
                 e.param_bf16 = L._vector(lists["param_bf16"][i], "param_bf16[%d]" % i, k, dev, torch.bfloat16)
-        self._keep = lists
+        spans = sorted((t.data_ptr(), t.numel() * t.element_size(), "%s[%d]" % (name, i))
+                       for name, v in lists.items() if name not in ("grads", "groups")
+                       for i, t in enumerate(v) if t is not None and t.numel())
+        self._overlap = next(("%s and %s overlap" % (first, second)
+                              for (a, size, first), (b, _, second) in zip(spans, spans[1:]) if a + size > b), None)
+        # aliases keep the memory where the caller's tensors are given other storage
+        self._keep = [t.detach() for name, v in lists.items() if name != "groups" for t in v if t is not None]
         self._table = table
         self._address = ctypes.addressof(table)
 
@@ -348,15 +359,20 @@ def fsdp_adam_tensors(tensors: AdamTensors, groups, *, seed: int = 0, grad_scale
         raise TypeError("tensors must be an AdamTensors, got %r" % type(tensors))
     if not tensors.steps:
         raise ValueError("the list has no params and grads")
+    if tensors._overlap:
+        raise ValueError(tensors._overlap)
     if isinstance(groups, dict):
         groups = (groups,)
     cfg = b"".join([_adam_cfg(**g) for g in groups])
     dev = tensors.device
     if dev is None:
-        return
+        grad_scale = skip = None
     head = _ADAM_LIST.pack(tensors.n, len(groups), tensors.format, tensors.grad_dtype,
                            seed & 0xFFFFFFFFFFFFFFFF, L._vector(grad_scale, "grad_scale", 1, dev, L._f32),
                            L._vector(skip, "skip", 1, dev, L._f32))
+    if dev is None:   # an empty list: its arguments are checked
+        B._check(_fn.fsdp_adam_tensors(head, tensors._address, cfg, None))
+        return
     L._call(_fn.fsdp_adam_tensors, dev, stream, head, tensors._address, cfg)
 
 
@@ -372,6 +388,8 @@ def fsdp_adam_convert(src: AdamTensors, dst: AdamTensors, *, seed: int = 0, step
             raise TypeError("%s must be an AdamTensors, got %r" % (name, type(t)))
     if src.numels != dst.numels:
         raise ValueError("the lists hold tensors of different sizes")
+    if dst._overlap:
+        raise ValueError(dst._overlap)
     dev = src.device
     if dst.device != dev:
         raise ValueError("the lists are on different GPUs")

@@ -368,3 +368,59 @@ def test_rotary_of_several_launches_and_far_offsets():
     F.fsdp_rotary_forward(x, x, f)
     want, bound = R.rotary(src[None].double().cpu().numpy(), f.cpu().numpy(), np.array([some]), "half", 1.0, 1, "bf16")
     assert (np.abs(x[some][None].double().cpu().numpy() - want) <= bound).all()
+
+
+# ---------------------------------------------------------------------------
+# lists of tensors
+# ---------------------------------------------------------------------------
+def test_a_list_refuses_what_is_there_twice():
+    p, m, v = (torch.zeros(100, device=dev()) for _ in range(3))
+    q, r = torch.zeros(200, device=dev()), torch.zeros(200, device=dev())
+    good = ([p, q[:100]], [p, q[:100]], [m, r[:100]], [v, r[100:]])
+    F.AdamTensors(*good)
+    F.AdamTensors([p, p[:0]], [p, p[:0]], [m, m[:0]], [v, v[:0]])                    # nothing overlaps nothing
+    one = torch.zeros(1, device=dev())
+    for bad in (([p, p], *good[1:]), ([p, p[99:]], [p, one], [m, one], [v, one.clone()]), (*good[:2], [m, m], good[3]),
+                (*good[:3], [v, r[99:199]]), (*good[:2], [m, p], good[3])):
+        with pytest.raises(ValueError, match="overlap"):
+            F.fsdp_adam_tensors(F.AdamTensors(*bad), dict(lr=1e-3, step=1))
+    copy = F.AdamTensors([p], [m], [q[:100]], [v], param_bf16=[q[50:100].view(torch.bfloat16)])
+    with pytest.raises(ValueError, match="overlap"):
+        F.fsdp_adam_tensors(copy, dict(lr=1e-3, step=1))
+    state = torch.zeros(F.fsdp_adam_state_bytes(100), dtype=torch.uint8, device=dev())
+    small = F.AdamTensors([p], [p], [state], [state], states="8bit")
+    F.fsdp_adam_convert(small, F.AdamTensors(None, None, [m], [v]))           # read twice
+    with pytest.raises(ValueError, match="overlap"):
+        F.fsdp_adam_convert(F.AdamTensors(None, None, [m], [v]), small)
+    with pytest.raises(TypeError, match=r"params\[1\]"):
+        F.AdamTensors([p, None], [p, p], [m, r[:100]], [v, r[100:]])
+
+
+@pytest.mark.parametrize("states", ["f32", "8bit"])
+def test_a_list_holds_its_memory(states):
+    """Where a parameter is given other storage after the list was made, a step writes what the list holds."""
+    n = 1 << 20
+    held = F.fsdp_adam_state_bytes(n) if states == "8bit" else n
+    kind = torch.uint8 if states == "8bit" else torch.float32
+    p, g = torch.ones(n, device=dev()), torch.ones(n, device=dev())
+    m, v = torch.zeros(held, dtype=kind, device=dev()), torch.zeros(held, dtype=kind, device=dev())
+    t = F.AdamTensors([p], [g], [m], [v], states=states)
+    for x in (p, g, m, v):
+        x.data = torch.zeros(1, dtype=x.dtype, device=dev())
+    others = [torch.full((n,), 7.0, device=dev()) for _ in range(8)]    # would take freed memory
+    F.fsdp_adam_tensors(t, dict(lr=0.1, step=1))
+    torch.cuda.synchronize()
+    assert all(bool((x == 7).all()) for x in others) and float(p.sum()) == 0.0
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 127, 2.0 ** -100])
+def test_logprob_at_the_ends_of_the_scale(scale):
+    x = normal(1, 5, 700)
+    if scale > 1:
+        x = x.sign() * 2.0 ** -120 * x.abs()
+    tok = torch.arange(5, device=dev())
+    o = [torch.empty(5, device=dev()) for _ in range(4)]
+    F.fsdp_logprob_forward(x, tok, o[0], o[1], o[2], scale=scale, entropy=o[3])
+    want = R.logprob(x.double().cpu().numpy(), tok.cpu().numpy(), scale)
+    for got, k, e in ((o[0], "logprob", "elogprob"), (o[2], "logsum", "elogsum"), (o[3], "entropy", "eentropy")):
+        assert (np.abs(got.double().cpu().numpy() - want[k]) <= want[e]).all(), k

@@ -332,3 +332,32 @@ def test_random_numbers_are_spread():
     c, d = R.random16(n, R.key(0, 2, 0))
     for x, y in ((a, b), (a, c), (b, d)):
         assert abs(np.corrcoef(x, y)[0, 1]) < 5 / n ** 0.5
+
+
+# ---------------------------------------------------------------------------
+# ends of the ranges
+# ---------------------------------------------------------------------------
+def test_logprob_scale_whose_product_with_log2_e_overflows(lib):
+    big = float(np.float32(3e38))
+    for f in (lp_fwd, lp_bwd):
+        assert f(lib, dict(scale=big)) == RANGE
+        assert f(lib, dict(scale=2.0 ** 127, rows=0)) == OK
+        assert f(lib, dict(scale=2.0 ** -149, rows=0)) == OK
+
+
+def test_rotary_positions_from_start_stay_in_int64(lib):
+    last = (1 << 63) - 1
+    for f in ("fsdp_rotary_forward", "fsdp_rotary_backward"):
+        assert rotary(lib, dict(start=last - 6), dict(positions=None), f=f) == OVERFLOW   # 8 tokens
+        assert rotary(lib, dict(start=last - 6, tokens=0), f=f) == OK
+
+
+def test_an_empty_list_of_tensors_is_checked(lib):
+    t = T.AdamTensors([], [], [], [])
+    T.fsdp_adam_tensors(t, dict(lr=1e-3, step=1))
+    with pytest.raises(B.FsdpError, match="step"):
+        T.fsdp_adam_tensors(t, dict(lr=1e-3, step=0))
+    with pytest.raises(B.FsdpError, match="n_groups"):
+        T.fsdp_adam_tensors(t, [])
+    with pytest.raises(TypeError, match="positional|unexpected|missing"):
+        T.fsdp_adam_tensors(t, dict(lr=1e-3))
