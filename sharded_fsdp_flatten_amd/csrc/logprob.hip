@@ -669,10 +669,16 @@ hipError_t forward_rows(const LogprobFwd& a, hipStream_t stream) {
     // Threads of a workgroup.  A wave a row, against 256 threads: 16384 x 3000 bf16 19.6 and 32 us; 16384 x 6000 37.8 and 40.5, but
     // 99 and 85 with 20 alternatives.  1024, against 256, where workgroups are few: 200 x 262144 21 and 33.7, 200 x 50257 7.1 and
     // 8.2; not of 600 x 50257, 14.6 and 13.4 (27.6 and 22.6 with alternatives), nor of 200 x 12000 with alternatives, 9.5 and 8.8.
+    // 512, against 256, where many long rows keep the chip full: 4096 x 50257 bf16 64.8 and 67.2, 8192 x 33000 84.1 and 88.1, fp32 2048 x 50257
+    // with 20 alternatives 76.8 and 80.7; not of 16384 x 20000 bf16, 119 and 103, 1024 x 131072, 47.0 and 43.7, nor of 4096 x 50257
+    // with 20 alternatives, 91.5 and 86.7.
+    const int64_t long_row = int64_t{a.top ? 128 : 64} << 10;
     for (int64_t r0 = 0; r0 < a.rows; r0 += most) {
         const int64_t rows = std::min(a.rows - r0, most);
         const uint32_t blocks = static_cast<uint32_t>(rows * sp.parts);
         if (sp.per <= kShort) forward<T, 64, false>(a, sp, r0, blocks, stream);
+        else if (nt && blocks >= 2048 && sp.per * static_cast<int64_t>(sizeof(T)) >= long_row)
+            forward<T, 512, true>(a, sp, r0, blocks, stream);
         else if (blocks >= 512 || sp.per < 16384)
             nt ? forward<T, 256, true>(a, sp, r0, blocks, stream) : forward<T, 256, false>(a, sp, r0, blocks, stream);
         else forward<T, 1024, false>(a, sp, r0, blocks, stream);

@@ -318,3 +318,36 @@ def test_refusals():
         F.fsdp_logprob_backward(x, tok, None, v, v, x)
     with pytest.raises(TypeError):
         F.fsdp_logprob_backward(x, tok, v, v, v, x.bfloat16())
+
+
+@pytest.mark.parametrize("rows,cols,dtype,top,start", [(2048, 50257, "f32", 20, 1), (2051, 50257, "bf16", 0, 3), (2050, 66001, "bf16", 64, 7),
+                                                       (2048, 32768, "f32", 7, 0)])
+def test_many_long_rows(rows, cols, dtype, top, start):
+    """Rows that fill the chip; a few of them hold masks, infinities, NaN, one value throughout and rising values."""
+    m = Matrix(rows, cols, T[dtype], cols + 2, start)
+    g = torch.Generator(device=dev()).manual_seed(rows)
+    m.t.copy_((torch.randn(rows, cols, generator=g, device=dev()) * 3).to(T[dtype]))
+    low = torch.finfo(T[dtype]).min
+    m.t[1] = 0.25
+    m.t[2] = -float("inf")
+    m.t[3] = low
+    m.t[4, 70:] = -float("inf")
+    m.t[5, 100] = float("nan")
+    m.t[6, 9] = float("inf")
+    m.t[7] = torch.arange(cols, device=dev()).to(T[dtype])
+    m.t[8, :cols - 30] = low
+    tok = torch.randint(-1, cols, (rows,))
+    got = forward(m, tok, 1.0, top)
+    some = [*range(12), rows // 2, rows - 2, rows - 1]
+    x = f64(m.t[some])
+    want = R.logprob(x, tok[some].numpy(), 1.0)
+    for k in ("logsum", "entropy", "logprob"):
+        close(got[k][some], want[k], want["e" + k], k)
+    if top:
+        order = R.top(x, top)
+        assert np.array_equal(got["top_token"][some].cpu().numpy(), order)
+        r = np.arange(len(some))[:, None]
+        close(got["top_logprob"][some], want["lp"][r, order], want["elp"][r, order], "top_logprob")
+    again = forward(m, tok, 1.0, top)
+    for k in got:
+        assert torch.equal(got[k].nan_to_num(9), again[k].nan_to_num(9)), k
