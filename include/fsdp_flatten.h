@@ -898,8 +898,8 @@ FSDP_API fsdp_status fsdp_adam_state_bytes(int64_t numel, int64_t* bytes);
  * of fsdp_adam_shard's update.
  *   tensors : host array of n_tensors, groups : host array of n_groups; both are read during
  *             the call.
- * No two tensors may overlap.  The list is cut into as many launches as its table needs (50
- * tensors a launch).  A captured call keeps its step numbers, on which bias corrections and random numbers
+ * No two tensors may overlap.  The list is cut into as many launches as its tables need (about 80 tensors
+ * a launch; addresses of 48 bits).  A captured call keeps its step numbers, on which bias corrections and random numbers
  * rest, so that only a replay of the same step repeats it rightly.
  * Errors: FSDP_E_ARG (NULL list or groups; NULL tensors with n_tensors; a NULL buffer of a tensor
  * with elements), FSDP_E_RANGE (n_tensors negative, n_groups outside

@@ -22,7 +22,6 @@ constexpr int kThreads = 256;
 // Elements of a workgroup: 14.2 M elements with fp32 states, tiles of 1024 / 2048 / 4096 72.1 / 74.0 / 73.9 us; 25 M with 8-bit
 // ones and fp32 gradients 67.3 / 62.8 / 65.8.
 template <State kState> constexpr int kTile = kThreads * (kState == State::kF32 ? 4 : 8);
-constexpr int kLaunch = 50;           // tensors of a launch (kernel-argument budget)
 constexpr int64_t kMaxTiles = int64_t{1} << 20;   // of a launch
 
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
@@ -271,23 +270,69 @@ template <typename F> struct Held<State::kBF16, F> {
 // ---------------------------------------------------------------------------
 // the step
 // ---------------------------------------------------------------------------
-struct Entry {
+// A tensor in a launch's table, in 32-bit words: addresses and sizes take 48 bits each.  Where no tensor has a copy,
+// or the states need no key, those words are left out, so that more tensors go in a launch (96 short ones in one instead
+// of two of 50: 10.9 -> 7.4 us; 144 with 8-bit states in two instead of three: 119 -> 109).
+template <bool kKey, bool kCopy> struct Entry {
+    uint32_t low[kCopy ? 6 : 5];   // of p, g, m, v, n and the copy
+    uint32_t high[3];              // the upper 16 bits in pairs: p and g, m and v, n (with the group, from bit 12 on) and the copy
+    uint32_t key[kKey ? 1 : 0];
+};
+constexpr int kArguments = 4096 - 64;   // bytes of a table: the budget of a kernel's arguments, less what launches add
+constexpr int kTableHead = kAdamGroups * sizeof(AdamScalars) + 2 * sizeof(void*) + 8;
+template <bool kKey, bool kCopy> struct Table {
+    static constexpr int kLaunch = (kArguments - kTableHead) / (4 + sizeof(Entry<kKey, kCopy>));
+    AdamScalars sc[kAdamGroups];
+    const float *grad_scale, *skip;
+    uint32_t bias;             // the first entry's tiles that earlier launches took
+    uint32_t start[kLaunch];   // first tile of each entry; beyond the last entry: UINT32_MAX
+    Entry<kKey, kCopy> e[kLaunch];
+};
+static_assert(sizeof(Table<true, true>) <= kArguments && sizeof(Table<false, false>) <= kArguments,
+              "the table must fit one kernel argument block");
+// The same, read by a kernel.
+struct Tensor {
     float* p;
     const void* g;
     void *m, *v;
     uint16_t* pb;
     int64_t n;
-    uint32_t bias;      // the tensor's tiles that earlier launches took
-    uint32_t key;
-    uint32_t group, unused;
+    uint32_t key, group;
 };
-struct Table {
-    uint32_t start[kLaunch];   // first tile of each entry; beyond the last entry: all tiles
-    Entry e[kLaunch];
-    AdamScalars sc[kAdamGroups];
-    const float *grad_scale, *skip;
-};
-static_assert(sizeof(Table) <= 4096 - 64, "the table must fit one kernel argument block");
+template <bool kKey, bool kCopy>
+__device__ __forceinline__ Tensor tensor_of(const Entry<kKey, kCopy>& e) {
+    const auto at = [](uint32_t low, uint32_t high) { return static_cast<uint64_t>(high & 0xFFFFu) << 32 | low; };
+    Tensor t;
+    t.p = reinterpret_cast<float*>(at(e.low[0], e.high[0]));
+    t.g = reinterpret_cast<const void*>(at(e.low[1], e.high[0] >> 16));
+    t.m = reinterpret_cast<void*>(at(e.low[2], e.high[1]));
+    t.v = reinterpret_cast<void*>(at(e.low[3], e.high[1] >> 16));
+    t.n = static_cast<int64_t>(at(e.low[4], e.high[2] & 0xFFFu));
+    t.group = e.high[2] >> 12 & 15u;
+    t.pb = nullptr;
+    if constexpr (kCopy) t.pb = reinterpret_cast<uint16_t*>(at(e.low[5], e.high[2] >> 16));
+    t.key = 0;
+    if constexpr (kKey) t.key = e.key[0];
+    return t;
+}
+template <bool kKey, bool kCopy>
+Entry<kKey, kCopy> entry_of_tensor(const AdamTensor& a) {
+    const auto word = [](const void* p) { return reinterpret_cast<uint64_t>(p); };
+    const auto pair = [](uint64_t x, uint64_t y) { return static_cast<uint32_t>(x >> 32 & 0xFFFFu) | static_cast<uint32_t>(y >> 32 << 16); };
+    const uint64_t size = static_cast<uint64_t>(a.n) | static_cast<uint64_t>(a.group) << 44;
+    Entry<kKey, kCopy> e;
+    e.low[0] = static_cast<uint32_t>(word(a.p));
+    e.low[1] = static_cast<uint32_t>(word(a.g));
+    e.low[2] = static_cast<uint32_t>(word(a.m));
+    e.low[3] = static_cast<uint32_t>(word(a.v));
+    e.low[4] = static_cast<uint32_t>(size);
+    if constexpr (kCopy) e.low[5] = static_cast<uint32_t>(word(a.pb));
+    e.high[0] = pair(word(a.p), word(a.g));
+    e.high[1] = pair(word(a.m), word(a.v));
+    e.high[2] = pair(size, word(a.pb));
+    if constexpr (kKey) e.key[0] = a.key;
+    return e;
+}
 
 // kExact: the single shard's step, bit for bit.  Else (8-bit states) its square root and quotients are the
 // hardware's, to one unit in the last place each, and the update stays within 14 x 2^-24 of itself: 29.5 M elements 97 ->
@@ -309,23 +354,25 @@ __device__ __forceinline__ void adam1(float& p, float g, float& m, float& v, con
 
 // The workgroup's entry, and which of the entry's tiles of this launch it takes.  Each XCD takes runs of 64
 // neighbouring tiles (14.2 M elements with fp32 states 74.0 -> 72.6 us).
-__device__ __forceinline__ uint32_t entry_of(const uint32_t* start, uint32_t* tile) {
+template <int kLaunch>
+__device__ __forceinline__ uint32_t entry_of(const uint32_t (&start)[kLaunch], uint32_t* tile) {
     constexpr uint32_t kXcds = 8, kRun = 64, kPer = kXcds * kRun;
     uint32_t at = blockIdx.x;
     if (at < gridDim.x / kPer * kPer) at = at / kPer * kPer + at % kXcds * kRun + at % kPer / kXcds;
-    uint32_t k = 0;
-#pragma unroll
-    for (int i = 1; i < kLaunch; ++i) k += start[i] <= at ? 1u : 0u;
+    // an entry a lane
+    static_assert(kLaunch <= 128);
+    const uint32_t l = threadIdx.x & 63u;
+    const uint32_t k = __popcll(__ballot(start[min(l, kLaunch - 1u)] <= at && l < kLaunch)) +
+                       (kLaunch > 64 ? __popcll(__ballot(start[min(l + 64u, kLaunch - 1u)] <= at && l + 64u < kLaunch)) : 0) - 1u;
     *tile = at - start[k];
     return k;
 }
 
 template <typename G, State kState, bool kWhole, bool kNt>
-__device__ __forceinline__ void adam_tile(const Table& t, const Entry& e, int64_t base) {
+__device__ __forceinline__ void adam_tile(const AdamScalars& s, const float* grad_scale, const Tensor& e, int64_t base) {
     constexpr int kN = kTile<kState> / kThreads / 4;
-    const AdamScalars s = t.sc[e.group];
     const float inv_bc2s = 1.0f / s.bc2s;
-    const float gs = t.grad_scale ? *t.grad_scale : 1.0f;
+    const float gs = grad_scale ? *grad_scale : 1.0f;
     const int64_t scales = (e.n + 15) / 16 * 16;
     f4 p[kN];
     decltype(raw4<true, kNt>(static_cast<const G*>(nullptr), 0)) g[kN];
@@ -354,7 +401,7 @@ __device__ __forceinline__ void adam_tile(const Table& t, const Entry& e, int64_
         m[h].get(mm);
         v[h].get(vv);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) adam1<kState == State::kF32>(pp[j], t.grad_scale ? gg[j] * gs : gg[j], mm[j], vv[j], s, inv_bc2s);
+        for (int j = 0; j < 4; ++j) adam1<kState == State::kF32>(pp[j], grad_scale ? gg[j] * gs : gg[j], mm[j], vv[j], s, inv_bc2s);
         put4<kWhole>(e.p + at, n, pp);
         if (e.pb) put4<kWhole>(e.pb + at, n, pp);
         uint32_t r[4];
@@ -371,26 +418,31 @@ __device__ __forceinline__ void adam_tile(const Table& t, const Entry& e, int64_
     }
 }
 
-template <typename G, State kState, bool kNt>
-__global__ void __launch_bounds__(kThreads) adam_tensors_kernel(Table t) {
+template <typename G, State kState, bool kCopy, bool kNt>
+__global__ void __launch_bounds__(kThreads) adam_tensors_kernel(Table<kState == State::k8Bit, kCopy> t) {
     if (t.skip && *t.skip != 0.0f) return;
     uint32_t tile;
-    const Entry& e = t.e[entry_of(t.start, &tile)];
-    const int64_t base = (static_cast<int64_t>(tile) + e.bias) * kTile<kState>;
-    if (base + kTile<kState> <= e.n) adam_tile<G, kState, true, kNt>(t, e, base);
-    else adam_tile<G, kState, false, kNt>(t, e, base);
+    const uint32_t k = entry_of(t.start, &tile);
+    const Tensor e = tensor_of(t.e[k]);
+    const AdamScalars s = t.sc[e.group];
+    const int64_t base = (static_cast<int64_t>(tile) + (k == 0 ? t.bias : 0u)) * kTile<kState>;
+    if (base + kTile<kState> <= e.n) adam_tile<G, kState, true, kNt>(s, t.grad_scale, e, base);
+    else adam_tile<G, kState, false, kNt>(s, t.grad_scale, e, base);
 }
 
 struct CopyEntry {
     const void *m, *v;
     void *m_to, *v_to;
     int64_t n;
-    uint32_t bias, key;
+    uint32_t key, unused;
 };
 struct CopyTable {
+    static constexpr int kLaunch = 75;
+    uint32_t bias;
     uint32_t start[kLaunch];
     CopyEntry e[kLaunch];
 };
+static_assert(sizeof(CopyTable) <= kArguments, "the table must fit one kernel argument block");
 
 template <State kFrom, State kTo, bool kWhole>
 __device__ __forceinline__ void convert_tile(const CopyEntry& e, int64_t base) {
@@ -426,16 +478,18 @@ __device__ __forceinline__ void convert_tile(const CopyEntry& e, int64_t base) {
 template <State kFrom, State kTo>
 __global__ void __launch_bounds__(kThreads) adam_convert_kernel(CopyTable t) {
     uint32_t tile;
-    const CopyEntry& e = t.e[entry_of(t.start, &tile)];
-    const int64_t base = (static_cast<int64_t>(tile) + e.bias) * kTile<State::k8Bit>;
+    const uint32_t k = entry_of(t.start, &tile);
+    const CopyEntry& e = t.e[k];
+    const int64_t base = (static_cast<int64_t>(tile) + (k == 0 ? t.bias : 0u)) * kTile<State::k8Bit>;
     if (base + kTile<State::k8Bit> <= e.n) convert_tile<kFrom, kTo, true>(e, base);
     else convert_tile<kFrom, kTo, false>(e, base);
 }
 
-// Cuts a list into launches: fill(table slot, list index, tiles taken before) for every entry, then
-// launch(tiles).  A tensor too long for one launch goes on in the next.
+// Cuts a list into launches: fill(table slot, tensor) for every entry, then launch(tiles).  A tensor too long for one
+// launch goes on as the first of the next.
 template <typename TableT, typename List, typename Fill, typename Launch>
 hipError_t in_launches(const List& list, int tile, TableT& t, Fill&& fill, Launch&& launch) {
+    constexpr int kLaunch = TableT::kLaunch;
     int used = 0;
     int64_t tiles = 0;
     const auto flush = [&]() -> hipError_t {
@@ -451,7 +505,8 @@ hipError_t in_launches(const List& list, int tile, TableT& t, Fill&& fill, Launc
         for (int64_t done = 0; done < all;) {
             const int64_t now = std::min(all - done, kMaxTiles - tiles);
             t.start[used] = static_cast<uint32_t>(tiles);
-            fill(used++, list[i], static_cast<uint32_t>(done));
+            if (used == 0) t.bias = static_cast<uint32_t>(done);
+            fill(used++, list[i]);
             done += now;
             tiles += now;
             if (used == kLaunch || tiles == kMaxTiles) {
@@ -463,14 +518,17 @@ hipError_t in_launches(const List& list, int tile, TableT& t, Fill&& fill, Launc
     return flush();
 }
 
-template <typename G, State kState, bool kNt>
-hipError_t step(const std::vector<AdamTensor>& list, Table& t, hipStream_t stream) {
+template <typename G, State kState, bool kCopy, bool kNt>
+hipError_t step(const std::vector<AdamTensor>& list, const AdamScalars* groups, int n_groups, const float* grad_scale,
+                const float* skip, hipStream_t stream) {
+    constexpr bool kKey = kState == State::k8Bit;
+    Table<kKey, kCopy> t{};
+    std::copy(groups, groups + n_groups, t.sc);
+    t.grad_scale = grad_scale;
+    t.skip = skip;
     return in_launches(
-        list, kTile<kState>, t,
-        [&](int i, const AdamTensor& a, uint32_t bias) {
-            t.e[i] = {a.p, a.g, a.m, a.v, a.pb, a.n, bias, a.key, static_cast<uint32_t>(a.group), 0};
-        },
-        [&](uint32_t tiles) { adam_tensors_kernel<G, kState, kNt><<<dim3(tiles), kThreads, 0, stream>>>(t); });
+        list, kTile<kState>, t, [&](int i, const AdamTensor& a) { t.e[i] = entry_of_tensor<kKey, kCopy>(a); },
+        [&](uint32_t tiles) { adam_tensors_kernel<G, kState, kCopy, kNt><<<dim3(tiles), kThreads, 0, stream>>>(t); });
 }
 
 template <State kFrom, State kTo>
@@ -478,7 +536,7 @@ hipError_t convert(const std::vector<StateCopy>& list, hipStream_t stream) {
     CopyTable t{};
     return in_launches(
         list, kTile<State::k8Bit>, t,
-        [&](int i, const StateCopy& a, uint32_t bias) { t.e[i] = {a.m, a.v, a.m_to, a.v_to, a.n, bias, a.key}; },
+        [&](int i, const StateCopy& a) { t.e[i] = {a.m, a.v, a.m_to, a.v_to, a.n, a.key, 0}; },
         [&](uint32_t tiles) { adam_convert_kernel<kFrom, kTo><<<dim3(tiles), kThreads, 0, stream>>>(t); });
 }
 
@@ -499,17 +557,26 @@ uint32_t adam_key(uint64_t seed, int64_t step, int64_t tensor) {
 hipError_t launch_adam_tensors(const std::vector<AdamTensor>& list, const AdamScalars* groups, int n_groups,
                                bool state8, bool grad_bf16, const float* grad_scale, const float* skip,
                                hipStream_t stream) {
-    Table t{};
-    std::copy(groups, groups + n_groups, t.sc);
-    t.grad_scale = grad_scale;
-    t.skip = skip;
     // bytes of the whole list: the launches of a step follow one another
     int64_t bytes = 0;
-    for (const AdamTensor& a : list) bytes += a.n * ((state8 ? 12 : 24) + (grad_bf16 ? 2 : 4) + (a.pb ? 2 : 0));
+    bool copy = false;
+    for (const AdamTensor& a : list) {
+        bytes += a.n * ((state8 ? 12 : 24) + (grad_bf16 ? 2 : 4) + (a.pb ? 2 : 0));
+        copy |= a.pb != nullptr;
+        // what an entry can hold
+        for (const void* p : {static_cast<const void*>(a.p), a.g, static_cast<const void*>(a.m), static_cast<const void*>(a.v),
+                              static_cast<const void*>(a.pb)})
+            if (reinterpret_cast<uint64_t>(p) >> 48) return hipErrorInvalidDevicePointer;
+    }
     const auto go = [&](auto grad, auto state) {
         using G = decltype(grad);
         constexpr State kState = decltype(state)::value;
-        return bytes >= kNtBytes ? step<G, kState, true>(list, t, stream) : step<G, kState, false>(list, t, stream);
+        const auto with = [&](auto c) {
+            constexpr bool kCopy = decltype(c)::value;
+            return bytes >= kNtBytes ? step<G, kState, kCopy, true>(list, groups, n_groups, grad_scale, skip, stream)
+                                     : step<G, kState, kCopy, false>(list, groups, n_groups, grad_scale, skip, stream);
+        };
+        return copy ? with(std::true_type{}) : with(std::false_type{});
     };
     using Small = std::integral_constant<State, State::k8Bit>;
     using Full = std::integral_constant<State, State::kF32>;

@@ -356,3 +356,35 @@ def test_refusals():
         F.fsdp_adam_tensors(b, CFG)
     with pytest.raises(F.FsdpError, match="8BIT"):
         F.fsdp_adam_convert(a, b)
+
+
+@pytest.mark.parametrize("copy", [False, True])
+@pytest.mark.parametrize("states", ["f32", "8bit"])
+@pytest.mark.parametrize("n", [64, 65, 79, 80, 87, 88, 97, 98, 250])
+def test_lists_about_as_long_as_a_launch(n, states, copy):
+    g = np.random.Generator(np.random.PCG64(n))
+    sizes = [int(x) for x in g.integers(1, 70, n)]
+    sizes[n // 2] = 5000
+    c = Case(sizes, states, "f32", copy, groups=[int(x) for x in g.integers(0, 2, n)])
+    cfgs = [CFG, dict(lr=1e-2, step=3)]
+    F.fsdp_adam_tensors(c.list, cfgs, seed=8)
+    c.reference(cfgs, seed=8)
+    c.check()
+    if states == "8bit":
+        out = [[torch.empty(k, device=dev()) for k in sizes] for _ in range(2)]
+        F.fsdp_adam_convert(c.list, F.AdamTensors(None, None, *out))
+        for k, x, o in (("m", c.m, out[0]), ("v", c.v, out[1])):
+            for i, size in enumerate(sizes):
+                same(f32(o[i]), R.read_state(x[i], size, k).astype(np.float32), "%s %d" % (k, i))
+
+
+def test_a_long_tensor_goes_on_in_the_next_launch():
+    """Two short tensors, one of more tiles than a launch takes, and one behind it: every element steps once."""
+    sizes = [3000, 7, (1 << 30) + 3000, 50]
+    p, g, m, v = ([torch.full((n,), x, device=dev()) for n in sizes] for x in (0.5, 0.25, 0.0, 0.0))
+    F.fsdp_adam_tensors(F.AdamTensors(p, g, m, v, groups=[0, 1, 0, 1]), [CFG, dict(CFG, lr=0.5)])
+    for i, cfg in enumerate([CFG, dict(CFG, lr=0.5)] * 2):
+        one = lambda x: np.full(1, x, np.float32)  # noqa: E731
+        want = R.adam_f32(one(0.5), one(0.25), one(0), one(0), cfg)
+        for got, w in zip((p[i], m[i], v[i]), want):
+            assert float(got.min()) == float(got.max()) == float(w[0]), i
