@@ -30,6 +30,7 @@ from __future__ import annotations
 import argparse
 import hashlib
 import json
+import math
 import os
 import sys
 import time
@@ -114,6 +115,11 @@ def parse_args():
                          "from the checkpoint and from the input, the MLP activation with "
                          "checkpoint and its backward pass, pack and unpack; 10 launches each "
                          "after a 1 GiB read")
+    ap.add_argument("--train-ops", type=int, default=0, metavar="TOKENS",
+                    help="also time a training step's other operators for this many tokens (bf16): "
+                         "rotary positions at the unit's width, log probabilities of GPT-2's 50257 "
+                         "tokens and their gradient, and AdamW over the unit's parameters sharded "
+                         "over its ranks, in 32 and 8 bits; 10 launches each after a 1 GiB read")
     return ap.parse_args()
 
 
@@ -663,6 +669,63 @@ def layer_ops(shapes, tokens, stream, dev, gen, reps=10):
     return out
 
 
+def train_ops(shapes, ranks, tokens, stream, dev, gen, reps=10):
+    """A training step's other operators, timed as layer_ops' are."""
+    import torch
+    import sharded_fsdp_flatten_amd as F
+    d, _ = layer_widths(shapes)
+    dim = 128 if d >= 4096 else 64
+    heads, vocab = max(1, d // dim), 50257
+    fb = torch.zeros(1 << 28, device=dev)
+    fs = torch.zeros((), device=dev)
+
+    def flush():
+        torch.sum(fb, dim=0, out=fs)
+
+    def n(*shape, std=1.0):
+        return torch.randn(*shape, device=dev, generator=gen).mul_(std).bfloat16()
+
+    qkv = n(tokens, 3, heads, dim)
+    out = torch.empty_like(qkv)
+    freqs = F.fsdp_rotary_freqs(dim).to(dev)
+    logits, grad = n(tokens, vocab, std=3.0), torch.empty(tokens, vocab, dtype=torch.bfloat16, device=dev)
+    labels = torch.randint(0, vocab, (tokens,), device=dev, generator=gen)
+    logprob, mx, logsum, entropy = (torch.empty(tokens, device=dev) for _ in range(4))
+    dl = torch.full((tokens,), -1.0 / tokens, device=dev)
+    top, top_token = torch.empty(tokens, 20, device=dev), torch.empty(tokens, 20, dtype=torch.int64, device=dev)
+    ws = torch.empty(max(F.fsdp_logprob_workspace(tokens, vocab, k) for k in (0, 20)), device=dev)
+    sizes = [-(-math.prod(s) // ranks) for s in shapes]
+    total = sum(sizes)
+
+    def tensors(states, dtype):
+        held = [F.fsdp_adam_state_bytes(k) for k in sizes] if states == "8bit" else sizes
+        kind = torch.uint8 if states == "8bit" else torch.float32
+        m, v = ([torch.zeros(k, dtype=kind, device=dev) for k in held] for _ in range(2))
+        return F.AdamTensors([torch.zeros(k, device=dev) for k in sizes], [n(k, std=1e-3).to(dtype) for k in sizes], m, v, states=states,
+                             param_bf16=[torch.empty(k, dtype=torch.bfloat16, device=dev) for k in sizes])
+
+    full, small = tensors("f32", torch.float32), tensors("8bit", torch.bfloat16)
+    step = dict(lr=1e-4, step=10, weight_decay=0.1)
+    wide = 2 * tokens * vocab
+    rows = [
+        ("rotary q, k", 8 * tokens * heads * dim, lambda: F.fsdp_rotary_forward(
+            qkv[:, 0], out[:, 0], freqs, k=qkv[:, 1], k_out=out[:, 1])),
+        ("logprob_forward", wide, lambda: F.fsdp_logprob_forward(logits, labels, logprob, mx, logsum, ws)),
+        ("logprob_forward+entropy+20 alternatives", wide, lambda: F.fsdp_logprob_forward(
+            logits, labels, logprob, mx, logsum, ws, entropy=entropy, top_logprob=top, top_token=top_token)),
+        ("logprob_backward", 2 * wide, lambda: F.fsdp_logprob_backward(logits, labels, dl, mx, logsum, grad)),
+        ("adam_tensors f32+copy", 30 * total, lambda: F.fsdp_adam_tensors(full, step)),
+        ("adam_tensors 8 bit+copy", int(16.125 * total), lambda: F.fsdp_adam_tensors(small, step, seed=1)),
+    ]
+    result = {"tokens": tokens, "heads": heads, "head_dim": dim, "vocab": vocab, "adam_elements": total, "dtype": "bf16", "ops": {}}
+    for name, nbytes, call in rows:
+        call()
+        ms = _event_median(call, stream, reps, before=flush)
+        result["ops"][name] = {"bytes": nbytes, "event_ms_median": round(ms, 4), "GB/s": round(nbytes / (ms * 1e-3) / 1e9, 1)}
+        print("train ops: %s done" % name, file=sys.stderr, flush=True)
+    return result
+
+
 def contention_probe(B, u, N, contrib_rows, pre, post, grad, stream, dev, reps=10):
     """The reduction on the tile kernel and on the row-major sweep, alone and overlapped with a
     stream of bf16 GEMMs on a second stream of the same priority (the backward compute that the
@@ -982,6 +1045,8 @@ def main():
         result["reduce_shapes"] = reduce_shapes(B, stream, dev, gen)
     if args.layer_ops > 0:
         result["layer_ops"] = layer_ops(unit.shapes, args.layer_ops, stream, dev, gen)
+    if args.train_ops > 0:
+        result["train_ops"] = train_ops(unit.shapes, N, args.train_ops, stream, dev, gen)
     if args.floor_probe:
         fb = torch.zeros(1 << 28, device=dev)
         fs = torch.zeros((), device=dev)

@@ -899,12 +899,12 @@ FSDP_API fsdp_status fsdp_adam_state_bytes(int64_t numel, int64_t* bytes);
  *   tensors : host array of n_tensors, groups : host array of n_groups; both are read during
  *             the call.
  * No two tensors may overlap.  The list is cut into as many launches as its tables need (about 80 tensors
- * a launch; addresses of 48 bits).  A captured call keeps its step numbers, on which bias corrections and random numbers
+ * a launch).  A captured call keeps its step numbers, on which bias corrections and random numbers
  * rest, so that only a replay of the same step repeats it rightly.
  * Errors: FSDP_E_ARG (NULL list or groups; NULL tensors with n_tensors; a NULL buffer of a tensor
  * with elements), FSDP_E_RANGE (n_tensors negative, n_groups outside
- * 1..FSDP_ADAM_MAX_GROUPS, state_format, grad_dtype, a numel negative, a tensor's group, a group's
- * values as for fsdp_adam_shard), FSDP_E_ALIGN, FSDP_E_OVERFLOW (numel > 2^40), FSDP_E_HIP.
+ * 1..FSDP_ADAM_MAX_GROUPS, state_format, grad_dtype, a numel negative, a tensor's group, an address of more
+ * than 48 bits, a group's values as for fsdp_adam_shard), FSDP_E_ALIGN, FSDP_E_OVERFLOW (numel > 2^40), FSDP_E_HIP.
  */
 FSDP_API fsdp_status fsdp_adam_tensors(const fsdp_adam_list* list, const fsdp_adam_tensor* tensors,
                                        const fsdp_adamw_cfg* groups, void* stream);

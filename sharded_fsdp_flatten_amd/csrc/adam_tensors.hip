@@ -563,10 +563,6 @@ hipError_t launch_adam_tensors(const std::vector<AdamTensor>& list, const AdamSc
     for (const AdamTensor& a : list) {
         bytes += a.n * ((state8 ? 12 : 24) + (grad_bf16 ? 2 : 4) + (a.pb ? 2 : 0));
         copy |= a.pb != nullptr;
-        // what an entry can hold
-        for (const void* p : {static_cast<const void*>(a.p), a.g, static_cast<const void*>(a.m), static_cast<const void*>(a.v),
-                              static_cast<const void*>(a.pb)})
-            if (reinterpret_cast<uint64_t>(p) >> 48) return hipErrorInvalidDevicePointer;
     }
     const auto go = [&](auto grad, auto state) {
         using G = decltype(grad);

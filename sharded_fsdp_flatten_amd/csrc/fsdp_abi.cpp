@@ -1146,6 +1146,10 @@ fsdp_status fsdp_adam_tensors(const fsdp_adam_list* list, const fsdp_adam_tensor
                 (s = check_buf(x.param_bf16, x.param_bf16 != nullptr, sizeof(uint16_t), "a tensor's param_bf16")) != FSDP_OK)
                 return s;
             if (x.numel == 0) continue;
+            for (const void* p : {static_cast<const void*>(x.param), x.grad, static_cast<const void*>(x.exp_avg),
+                                  static_cast<const void*>(x.exp_avg_sq), static_cast<const void*>(x.param_bf16)})
+                if (reinterpret_cast<uintptr_t>(p) >> 48)  // what a table's entry holds
+                    return fail(FSDP_E_RANGE, "a tensor's address has more than 48 bits");
             t.push_back({x.numel, x.param, x.grad, x.exp_avg, x.exp_avg_sq, x.param_bf16,
                          state8 ? fsdp::adam_key(list->seed, groups[x.group].step, i) : 0, x.group});
         }

@@ -351,3 +351,23 @@ def test_many_long_rows(rows, cols, dtype, top, start):
     again = forward(m, tok, 1.0, top)
     for k in got:
         assert torch.equal(got[k].nan_to_num(9), again[k].nan_to_num(9)), k
+
+
+@pytest.mark.parametrize("rows,cols,dtype,start,in_place", [(2051, 33001, "bf16", 5, False), (1500, 20003, "f32", 1, False), (2049, 40007, "bf16", 1, True)])
+def test_gradient_of_many_long_rows(rows, cols, dtype, start, in_place):
+    """Loads past the cache: rows at any element, what lies between the rows stays."""
+    m = Matrix(rows, cols, T[dtype], cols + 3, start)
+    g = torch.Generator(device=dev()).manual_seed(rows)
+    m.t.copy_((torch.randn(rows, cols, generator=g, device=dev()) * 3).to(T[dtype]))
+    tok = torch.randint(-1, cols, (rows,))
+    some = [*range(20), rows // 2, rows - 1]
+    tok[:4] = torch.tensor([0, cols - 1, 1, cols - 2])
+    x = f64(m.t[some])
+    o = forward(m, tok, 0.8, 0)
+    dl, dh = torch.randn(rows, generator=torch.Generator().manual_seed(1)), torch.randn(rows, generator=torch.Generator().manual_seed(2))
+    y = m if in_place else Matrix(rows, cols, T[dtype], cols + 6, start + 2)
+    F.fsdp_logprob_backward(m.t, tok.to(dev()), dl.to(dev()), o["max"], o["logsum"], y.t, scale=0.8, dentropy=dh.to(dev()), entropy=o["entropy"])
+    want, bound = R.logprob_grad(x, tok[some].numpy(), f64(dl[some]), f64(dh[some]), *(f64(o[k][some]) for k in ("max", "logsum", "entropy")),
+                                 float(np.float32(0.8)), dtype)
+    close(y.t[some], want, bound, "gradient")
+    assert y.around_is_untouched() and m.around_is_untouched()

@@ -361,3 +361,8 @@ def test_an_empty_list_of_tensors_is_checked(lib):
         T.fsdp_adam_tensors(t, [])
     with pytest.raises(TypeError, match="positional|unexpected|missing"):
         T.fsdp_adam_tensors(t, dict(lr=1e-3))
+
+
+@pytest.mark.parametrize("name", ["param", "grad", "exp_avg", "exp_avg_sq", "param_bf16"])
+def test_adam_addresses_have_48_bits(lib, name):
+    assert adam(lib, [tensor(**{name: 1 << 48})]) == RANGE
