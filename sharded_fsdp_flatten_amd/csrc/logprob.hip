@@ -169,15 +169,25 @@ __device__ __forceinline__ uint64_t wave_key(uint64_t key, int want) {
     const uint64_t has = __ballot(rank == want && key != 0);
     return has ? lane_key(key, __builtin_ctzll(has)) : 0;
 }
-// How many of the first n keys are larger; read in pairs, 16 bytes at a time.
+// How many of the first n keys are larger; kL neighbouring lanes, which hold the same key, share the counting.
+template <int kL>
 __device__ __forceinline__ int larger(const uint64_t* keys, uint32_t n, uint64_t key) {
+    const uint32_t l = threadIdx.x % kL;
     int place = 0;
     uint32_t j = 0;
-    for (; j + 8 <= n; j += 8) {
+    for (; j + 8 * kL <= n; j += 8 * kL) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) place += keys[j + q] > key ? 1 : 0;
+        for (int q = 0; q < 8; ++q) place += keys[j + q * kL + l] > key ? 1 : 0;
     }
-    for (; j < n; ++j) place += keys[j] > key ? 1 : 0;
+    for (; j + l < n; j += kL) place += keys[j + l] > key ? 1 : 0;
+    if constexpr (kL >= 4) {
+        place += dpp<kQuadXor1>(place);
+        place += dpp<kQuadXor2>(place);
+    }
+    if constexpr (kL == 16) {
+        place += dpp<kHalfMirror>(place);
+        place += dpp<kMirror>(place);
+    }
     return place;
 }
 
@@ -205,19 +215,21 @@ __device__ __forceinline__ float* part_at(const LogprobFwd& a, const Split& sp, 
     return a.workspace + (row * sp.parts + part) * (kPartFloats + 2 * a.top);
 }
 
-// Statistics, and the given token's log probability, of a whole row.
+// The row's given token (-1: none), and its logit.
+__device__ __forceinline__ int64_t given(const LogprobFwd& a, int64_t row) {
+    const int64_t tok = a.tokens ? a.tokens[row] : -1;
+    return tok < a.cols ? tok : -1;
+}
 template <typename T>
-__device__ __forceinline__ void put_row(const LogprobFwd& a, int64_t row, const Row& r) {
+__device__ __forceinline__ float logit(const LogprobFwd& a, int64_t row, int64_t tok) {
+    return tok >= 0 ? value(static_cast<const T*>(a.x.p) + row * a.x.pitch + tok) : 0.0f;
+}
+// Statistics, and the given token's log probability, of a whole row.
+__device__ __forceinline__ void put_row(const LogprobFwd& a, int64_t row, const Row& r, int64_t tok, float x) {
     a.max[row] = r.max;
     a.logsum[row] = r.logsum;
     if (a.entropy) a.entropy[row] = r.entropy;
-    if (a.tokens) {
-        const int64_t tok = a.tokens[row];
-        float lp = 0.0f;
-        if (tok >= 0 && tok < a.cols)
-            lp = r.logprob(value(static_cast<const T*>(a.x.p) + row * a.x.pitch + tok), a.scale);
-        a.logprob[row] = lp;
-    }
+    if (a.tokens) a.logprob[row] = tok >= 0 ? r.logprob(x, a.scale) : 0.0f;
 }
 __device__ __forceinline__ void put_top(const LogprobFwd& a, int64_t row, int i, uint64_t key, const Row& r) {
     a.top_token[row * a.top + i] = static_cast<uint32_t>(~static_cast<uint32_t>(key));
@@ -296,7 +308,13 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
     constexpr int kW = kT / 64, kV = kE<T>, kU = 32 / kV;
     constexpr uint32_t kSeg = kT == 64 ? 1 : 8, kAll = kSegments<T, kT>;
     constexpr int kMost = kCandidates<kT>;
-    __shared__ Part parts[kW];
+    // Few rows: the last wave alone joins the waves' sums and writes the row, and it asks for the given token ahead, for all
+    // instructions of the other fifteen share four SIMDs (16 x 50257 bf16 with 8 / 64 alternatives 11.0 / 14.8 -> 10.2 / 13.6
+    // us).  Where rows fill the chip a wave's wait for the token costs more (16384 x 10001 with 5: 93.8 and 98.8).
+    constexpr bool kLone = kT == 1024;
+    __shared__ Part parts[kW], sums;
+    __shared__ Row stats;
+    __shared__ bool far;
     __shared__ uint64_t bound[kTop ? kW : 1];
     __shared__ alignas(16) uint64_t keys[kTop ? kMost : 2];
     __shared__ uint32_t segs[kTop ? kAll : 1];      // rank_bits of the segments' largest
@@ -315,6 +333,9 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
     const uint32_t nv = static_cast<uint32_t>((n - head) / kV);
     const int tail = static_cast<int>(n - head - static_cast<int64_t>(nv) * kV);
     const T* body = x + head;
+
+    const bool last = t >> 6 == kW - 1, whole = sp.parts == 1;
+    int64_t tok = kLone && last && whole ? given(a, row) : -1;
 
     Part p = {-INFINITY, 0.0f, 0.0f};
     // segments of kSeg << wide vectors
@@ -412,43 +433,67 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
     if (edge >= 0) one(value(x + edge));
 
     // the lanes' sums, then the waves'
+    float* ws = whole ? nullptr : part_at(a, sp, row, part);
+    float x_tok = logit<T>(a, row, tok);
+    const auto put_sums = [&](const Part& q, const Row& r) {
+        if (whole) {
+            put_row(a, row, r, tok, x_tok);
+        } else {
+            ws[0] = q.m;
+            ws[1] = q.s;
+            ws[2] = q.t;
+        }
+    };
     const auto meet = [&](Part q) {
         q = wave_join(q, k);
         if constexpr (kW > 1) {
             if ((t & 63) == 0) parts[t >> 6] = q;
-            __syncthreads();
-            q = wave_join((t & 63) < kW ? parts[t & 63] : Part{-INFINITY, 0.0f, 0.0f}, k);
-        } else {
-            __syncthreads();
+        }
+        __syncthreads();
+        if constexpr (kW > 1) {
+            if (!kLone || last) q = wave_join((t & 63) < kW ? parts[t & 63] : Part{-INFINITY, 0.0f, 0.0f}, k);
         }
         return q;
     };
-    p = meet(p);
-    if (p.m > -INFINITY && p.m < INFINITY && overflows(anchor(p.m, k))) {
-        Part q = {p.m, 0.0f, 0.0f};
+    const auto beyond = [&](const Part& q) { return q.m > -INFINITY && q.m < INFINITY && overflows(anchor(q.m, k)); };
+    const auto again = [&](float m) {
+        Part q = {m, 0.0f, 0.0f};
         for (int64_t c = t; c < n; c += kT) {
-            const float u = (value(x + c) - p.m) * k, e = __builtin_amdgcn_exp2f(u);
+            const float u = (value(x + c) - m) * k, e = __builtin_amdgcn_exp2f(u);
             q.s += e;
             q.t += weighted(e, u);
         }
-        __syncthreads();
-        p = meet(q);
-    }
-    const bool whole = sp.parts == 1;
-    float* ws = whole ? nullptr : part_at(a, sp, row, part);
-    const Row r = finish(p, a.scale, k);
-    if (t == 0) {
-        if (whole) {
-            put_row<T>(a, row, r);
-        } else {
-            ws[0] = p.m;
-            ws[1] = p.s;
-            ws[2] = p.t;
+        return meet(q);
+    };
+    p = meet(p);
+    Row r;
+    if constexpr (kLone) {
+        if (last) {
+            r = finish(p, a.scale, k);
+            if ((t & 63) == 0) {
+                far = beyond(p);
+                sums = p;
+                stats = r;
+                if (!beyond(p)) put_sums(p, r);
+            }
+        }
+    } else {
+        if (beyond(p)) {
+            __syncthreads();
+            p = again(p.m);
+        }
+        r = finish(p, a.scale, k);
+        if (t == 0) {
+            if (whole) {
+                tok = given(a, row);
+                x_tok = logit<T>(a, row, tok);
+            }
+            put_sums(p, r);
         }
     }
+    const uint32_t n_segs = kTop && nv ? ((all - 1) >> wide) + 1 : 0;
     if constexpr (kTop) {
         // (the sums' meeting was a barrier: the segments are complete)
-        const uint32_t n_segs = nv ? ((all - 1) >> wide) + 1 : 0;
         uint64_t best = 0;
         for (uint32_t i = t; i < n_segs; i += kT) best = max(best, key_of(segs[i], i));
         // the first waves have a segment in each of their lanes
@@ -459,7 +504,21 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
         if ((t >> 6) < full)
             low = 4 * a.top <= 16 * full ? wave_key<4>(quad_key(best), share) : wave_key<1>(best, share);
         if ((t & 63) == 0) bound[t >> 6] = low;
-        __syncthreads();
+    }
+    if constexpr (kTop || kLone) __syncthreads();
+    if constexpr (kLone) {
+        if (far) {
+            p = again(sums.m);
+            if (last) {
+                r = finish(p, a.scale, k);
+                if ((t & 63) == 0) {
+                    stats = r;
+                    put_sums(p, r);
+                }
+            }
+        }
+    }
+    if constexpr (kTop) {
         uint64_t reach = bound[0];
 #pragma unroll
         for (int i = 1; i < kW; ++i) reach = min(reach, bound[i]);
@@ -470,7 +529,7 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
         }
         __syncthreads();
         const auto put = [&](int i, uint64_t key) {
-            if (whole) put_top(a, row, i, key, r);
+            if (whole) put_top(a, row, i, key, kLone ? stats : r);
             else reinterpret_cast<uint64_t*>(ws + kPartFloats)[i] = key;
         };
         // against the bound a logit counts as if it had its segment's place
@@ -504,10 +563,11 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
             __syncthreads();
             got = select<T, kT>(x, n, c0, a.top, keys, &count);
         }
-        for (uint32_t i = t; i < got; i += kT) {
+        constexpr int kL = kLone ? 16 : 1;   // lanes a key
+        for (uint32_t i = t / kL; i < got; i += kT / kL) {
             const uint64_t key = keys[i];
-            const int place_of = larger(keys, got, key);
-            if (place_of < a.top) put(place_of, key);
+            const int place_of = larger<kL>(keys, got, key);
+            if (t % kL == 0 && place_of < a.top) put(place_of, key);
         }
         // a run shorter than the alternatives wanted
         for (uint32_t i = got + t; i < static_cast<uint32_t>(a.top); i += kT) put(static_cast<int>(i), 0);
@@ -524,6 +584,8 @@ __global__ void __launch_bounds__(kThreads) logprob_join_kernel(LogprobFwd a, Sp
     const int t = threadIdx.x;
     const float k = static_cast<float>(a.scale * kLog2e);
     if (t == 0) count = 0;
+    const int64_t tok = given(a, row);
+    const float x_tok = logit<T>(a, row, tok);
     // every wave joins all of them
     const int l = t & 63;
     Part p = {-INFINITY, 0.0f, 0.0f};
@@ -537,7 +599,7 @@ __global__ void __launch_bounds__(kThreads) logprob_join_kernel(LogprobFwd a, Sp
     }
     p = wave_join(p, k);
     const Row r = finish(p, a.scale, k);
-    if (t == 0) put_row<T>(a, row, r);
+    if (t == 0) put_row(a, row, r, tok, x_tok);
     if (!a.top) return;
     for (int d = 1; d < 64; d <<= 1)
         least = min(least, static_cast<uint64_t>(__shfl_xor(static_cast<unsigned long long>(least), d)));
@@ -549,10 +611,11 @@ __global__ void __launch_bounds__(kThreads) logprob_join_kernel(LogprobFwd a, Sp
     }
     __syncthreads();
     const uint32_t got = count;
-    for (uint32_t i = t; i < got; i += kThreads) {
+    constexpr int kL = 4;
+    for (uint32_t i = t / kL; i < got; i += kThreads / kL) {
         const uint64_t key = keys[i];
-        const int place = larger(keys, got, key);
-        if (place < a.top) put_top(a, row, place, key, r);
+        const int place = larger<kL>(keys, got, key);
+        if (t % kL == 0 && place < a.top) put_top(a, row, place, key, r);
     }
 }
 
