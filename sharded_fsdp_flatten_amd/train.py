@@ -327,25 +327,30 @@ class AdamTensors:
         self.numels = [t.numel() for t in lists[sized]]
         dev = self.device
         table = (fsdp_adam_tensor * max(1, n))()
+        spans, width = [], {"f32": 4, "bf16": 2, "8bit": 1}[states]
         for i in range(n):
             e, k = table[i], self.numels[i]
             e.numel = k
             e.group = self.groups[i]
-            held = fsdp_adam_state_bytes(k) if states == "8bit" else k
+            held = k if states != "8bit" else fsdp_adam_state_bytes(k)
             e.exp_avg = L._vector(exp_avgs[i], "exp_avgs[%d]" % i, held, dev, sdtype)
             e.exp_avg_sq = L._vector(exp_avg_sqs[i], "exp_avg_sqs[%d]" % i, held, dev, sdtype)
             if self.steps:
                 e.param = L._vector(lists["params"][i], "params[%d]" % i, k, dev, torch.float32)
                 e.grad = L._vector(lists["grads"][i], "grads[%d]" % i, k, dev, gdtype)
+                spans.append((e.param, 4 * k, "params", i))
             if param_bf16 is not None and lists["param_bf16"][i] is not None:
                 e.param_bf16 = L._vector(lists["param_bf16"][i], "param_bf16[%d]" % i, k, dev, torch.bfloat16)
-        spans = sorted((t.data_ptr(), t.numel() * t.element_size(), "%s[%d]" % (name, i))
-                       for name, v in lists.items() if name not in ("grads", "groups")
-                       for i, t in enumerate(v) if t is not None and t.numel())
-        self._overlap = next(("%s and %s overlap" % (first, second)
-                              for (a, size, first), (b, _, second) in zip(spans, spans[1:]) if a + size > b), None)
-        # aliases keep the memory where the caller's tensors are given other storage
-        self._keep = [t.detach() for name, v in lists.items() if name != "groups" for t in v if t is not None]
+                spans.append((e.param_bf16, 2 * k, "param_bf16", i))
+            spans += (e.exp_avg, width * held, "exp_avgs", i), (e.exp_avg_sq, width * held, "exp_avg_sqs", i)
+        self._overlap = None
+        spans = sorted(x for x in spans if x[0] and x[1])
+        for (a, size, first, i), (b, _, second, j) in zip(spans, spans[1:]):
+            if a + size > b:
+                self._overlap = "%s[%d] and %s[%d] overlap" % (first, i, second, j)
+                break
+        # the memory stays where the caller's tensors are given other storage
+        self._keep = [t.untyped_storage() for name, v in lists.items() if name != "groups" for t in v if t is not None]
         self._table = table
         self._address = ctypes.addressof(table)
 
