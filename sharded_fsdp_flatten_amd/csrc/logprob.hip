@@ -302,7 +302,7 @@ __device__ uint32_t select(const T* x, int64_t n, int64_t c0, int k, uint64_t* k
 // how many are larger.  Where too many reach it (rows that allow fewer than k tokens, rows whose largest
 // logits meet in a few segments) the k-th largest key itself is found, eight bits a pass over the row.
 // Measured, top 20 with entropy of 2048 x 50257 fp32: lanes that read all of their own logits again 107 us (they
-// are 16 bytes in every 4 KB: as many lines as the row has), segments 78.
+// are 16 bytes in every 4 KB: as many lines as the row has), segments 78 (73 with what came after).
 template <typename T, int kT, bool kEntropy, bool kTop, bool kNt>
 __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp, int64_t row0) {
     constexpr int kW = kT / 64, kV = kE<T>, kU = 32 / kV;
@@ -731,8 +731,8 @@ template <typename T>
 hipError_t forward_rows(const LogprobFwd& a, hipStream_t stream) {
     const Split sp = plan_split(a.rows, a.cols);
     const int64_t most = kMaxBlocks / 4 / sp.parts;   // of up to 1024 threads
-    // Past the cache where a call's logits outgrow it, rows at any element: 4096 x 50257 bf16 (412 MB) cached 75.0,
-    // nt 68.4 us; 2048 x 50257 fp32 72.1 and 66.7.
+    // Past the cache where a call's logits outgrow it, rows at any element: 4096 x 50257 bf16 (412 MB), 256 threads, cached 75.0,
+    // nt 68.4 us (64 with 512 threads and whole lines); 2048 x 50257 fp32 72.1 and 66.7 (62).
     const bool nt = a.rows * a.cols * static_cast<int64_t>(sizeof(T)) >= kNtBytes;
     // Threads of a workgroup.  A wave a row, against 256 threads: 16384 x 3000 bf16 19.6 and 32 us; 16384 x 6000 37.8 and 40.5, but
     // 99 and 85 with 20 alternatives.  1024, against 256, where workgroups are few: 200 x 262144 21 and 33.7, 200 x 50257 7.1 and

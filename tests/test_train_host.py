@@ -366,3 +366,15 @@ def test_an_empty_list_of_tensors_is_checked(lib):
 @pytest.mark.parametrize("name", ["param", "grad", "exp_avg", "exp_avg_sq", "param_bf16"])
 def test_adam_addresses_have_48_bits(lib, name):
     assert adam(lib, [tensor(**{name: 1 << 48})]) == RANGE
+
+
+def test_the_profile_was_taken_on_the_current_sources():
+    import hashlib
+    import re
+    from conftest import ROOT
+    with open(os.path.join(ROOT, "profiles", "train_ops_gpt2l_block.md")) as f:
+        given = dict(re.findall(r"^(\S+\.hip) sha256: `([0-9a-f]{64})`", f.read(), re.M))
+    assert set(given) >= {"rotary.hip", "logprob.hip", "adam_tensors.hip"}
+    for name, h in given.items():
+        with open(os.path.join(ROOT, "sharded_fsdp_flatten_amd", "csrc", name), "rb") as f:
+            assert hashlib.sha256(f.read()).hexdigest() == h, name
