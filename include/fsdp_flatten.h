@@ -803,7 +803,8 @@ FSDP_API fsdp_status fsdp_logprob_workspace(int64_t rows, int64_t cols, int32_t 
  *   top_token, top_logprob: the `top` largest logits' columns and log probabilities, in falling
  *             order, equal logits by rising column
  * max is rounded, and logsum is of the rounded one: their sum is the logarithm of the sum of
- * e^z_j.  Sums are binary32.
+ * e^z_j.  Sums are binary32; their order depends on rows, cols, dtype, the logits' alignment and whether top is 0, and on nothing
+ * else: the same call gives the same bits.
  * A token outside [0, cols) is none (a padded position): its logprob is 0.
  * Logits of -infinity are masked: their probability is 0, and their logprob -infinity.  A row that holds
  * nothing else (or only logits whose product with scale is -infinity in binary32) has max -infinity,

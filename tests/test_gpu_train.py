@@ -424,3 +424,54 @@ def test_logprob_at_the_ends_of_the_scale(scale):
     want = R.logprob(x.double().cpu().numpy(), tok.cpu().numpy(), scale)
     for got, k, e in ((o[0], "logprob", "elogprob"), (o[2], "logsum", "elogsum"), (o[3], "entropy", "eentropy")):
         assert (np.abs(got.double().cpu().numpy() - want[k]) <= want[e]).all(), k
+
+
+# ---------------------------------------------------------------------------
+# arguments that may be left out, shapes of several dimensions
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("batch,tokens,cols", [(2, 3, 50257), (2, 3, 200000), (64, 33, 50257), (5, 7, 300), (3, 70, 9000)])
+def test_logprob_of_a_batch_with_and_without_tokens(batch, tokens, cols):
+    """[batch, tokens, cols] logits; statistics are the same bits with tokens and without."""
+    x = normal(1, batch, tokens, cols, scale=3.0, dtype=torch.bfloat16)
+    tok = torch.randint(-1, cols, (batch, tokens), device=dev())
+    n, top = (batch, tokens), 5
+    ws = torch.empty(F.fsdp_logprob_workspace(batch * tokens, cols, top), device=dev())
+    lp, m1, s1, m2, s2, m3, s3, h = (torch.full(n, 7.0, device=dev()) for _ in range(8))
+    tl, tt = torch.empty(*n, top, device=dev()), torch.empty(*n, top, dtype=torch.int64, device=dev())
+    F.fsdp_logprob_forward(x, tok, lp, m1, s1, ws, entropy=h)
+    F.fsdp_logprob_forward(x, None, None, m2, s2, ws)
+    F.fsdp_logprob_forward(x, None, None, m3, s3, ws, top_logprob=tl, top_token=tt)
+    assert torch.equal(m1, m2) and torch.equal(s1, s2) and torch.equal(m1, m3)
+    rows = slice(0, 50)
+    want = R.logprob(x.view(-1, cols)[rows].double().cpu().numpy(), tok.view(-1)[rows].cpu().numpy(), 1.0)
+    # with alternatives a row's sum may be taken by another number of lanes, in another order: each of the two is within the
+    # bound of the exact one
+    for s in (s1, s3):
+        assert (np.abs(s.view(-1)[rows].double().cpu().numpy() - want["logsum"]) <= want["elogsum"]).all()
+    assert (np.abs(lp.view(-1)[rows].double().cpu().numpy() - want["logprob"]) <= want["elogprob"]).all()
+    assert np.array_equal(tt.view(-1, top)[rows].cpu().numpy(), R.top(x.view(-1, cols)[rows].double().cpu().numpy(), top))
+    # the gradient of the entropies alone, and of both as the sum of the parts
+    dl, dh, zero = normal(2, *n), normal(3, *n), torch.zeros(n, device=dev())
+    both, only, with_zero = (torch.empty_like(x) for _ in range(3))
+    F.fsdp_logprob_backward(x, None, None, m1, s1, only, dentropy=dh, entropy=h)
+    F.fsdp_logprob_backward(x, tok, zero, m1, s1, with_zero, dentropy=dh, entropy=h)
+    assert torch.equal(only, with_zero)
+    F.fsdp_logprob_backward(x, tok, dl, m1, s1, both, dentropy=dh, entropy=h)
+    F.fsdp_logprob_backward(x, tok, dl, m1, s1, x)
+    f = lambda t: t.view(-1, cols)[rows].double()  # noqa: E731
+    # three roundings to bf16, of each part and of the sum
+    assert ((f(both) - f(x) - f(only)).abs() <= 2.0 ** -8 * (f(both).abs() + f(x).abs() + f(only).abs()) * 1.01 + 1e-6).all()
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rotary_without_queries_or_batch(layout):
+    k = normal(1, 9, 3, 24)
+    f = F.fsdp_rotary_freqs(16).to(dev())
+    want = torch.empty_like(k)
+    F.fsdp_rotary_forward(k, want, f, start=5, layout=layout)
+    got, q = torch.empty_like(k), torch.empty(9, 0, 24, device=dev())
+    F.fsdp_rotary_forward(q, q, f, k=k, k_out=got, start=5, layout=layout)
+    assert torch.equal(got, want)
+    batched = torch.empty(1, 9, 3, 24, device=dev())
+    F.fsdp_rotary_forward(k[None], batched, f, positions=torch.arange(5, 14, device=dev())[None], layout=layout)
+    assert torch.equal(batched[0], want)
