@@ -716,15 +716,15 @@ Split plan_split(int64_t rows, int64_t cols) {
     return {static_cast<uint32_t>((cols + per - 1) / per), per};
 }
 
+template <typename T, int kT, bool kTop, bool kNt>
+void launch(const LogprobFwd& a, const Split& sp, int64_t r0, uint32_t blocks, hipStream_t stream) {
+    if (a.entropy) logprob_fwd_kernel<T, kT, true, kTop, kNt><<<blocks, kT, 0, stream>>>(a, sp, r0);
+    else logprob_fwd_kernel<T, kT, false, kTop, kNt><<<blocks, kT, 0, stream>>>(a, sp, r0);
+}
 template <typename T, int kT, bool kNt>
 void forward(const LogprobFwd& a, const Split& sp, int64_t r0, uint32_t blocks, hipStream_t stream) {
-    if (a.entropy) {
-        if (a.top) logprob_fwd_kernel<T, kT, true, true, kNt><<<blocks, kT, 0, stream>>>(a, sp, r0);
-        else logprob_fwd_kernel<T, kT, true, false, kNt><<<blocks, kT, 0, stream>>>(a, sp, r0);
-    } else {
-        if (a.top) logprob_fwd_kernel<T, kT, false, true, kNt><<<blocks, kT, 0, stream>>>(a, sp, r0);
-        else logprob_fwd_kernel<T, kT, false, false, kNt><<<blocks, kT, 0, stream>>>(a, sp, r0);
-    }
+    if (a.top) launch<T, kT, true, kNt>(a, sp, r0, blocks, stream);
+    else launch<T, kT, false, kNt>(a, sp, r0, blocks, stream);
 }
 
 template <typename T>
@@ -740,13 +740,18 @@ hipError_t forward_rows(const LogprobFwd& a, hipStream_t stream) {
     // 512, against 256, where many long rows keep the chip full: 4096 x 50257 bf16 64.8 and 67.2, 8192 x 33000 84.1 and 88.1, fp32 2048 x 50257
     // with 20 alternatives 76.8 and 80.7; not of 16384 x 20000 bf16, 119 and 103, 1024 x 131072, 47.0 and 43.7, nor of 4096 x 50257
     // with 20 alternatives, 91.5 and 86.7.
+    // 128, against 256, for short bf16 rows without alternatives: 16384 x 5001 34.8 and 41.7, x 10001 55.9 and 66.2, x 16001 86.8 and 89.3;
+    // not x 20001, 103.2 and 102.7, with alternatives (x 6001, 20: 93.0 and 84.5), or in fp32 (x 8001 87.7 and 82.6).
     const int64_t long_row = int64_t{a.top ? 128 : 64} << 10;
+    const bool short_row = sizeof(T) == 2 && !a.top && sp.per <= 16384;
     for (int64_t r0 = 0; r0 < a.rows; r0 += most) {
         const int64_t rows = std::min(a.rows - r0, most);
         const uint32_t blocks = static_cast<uint32_t>(rows * sp.parts);
         if (sp.per <= kShort) forward<T, 64, false>(a, sp, r0, blocks, stream);
         else if (nt && blocks >= 2048 && sp.per * static_cast<int64_t>(sizeof(T)) >= long_row)
             forward<T, 512, true>(a, sp, r0, blocks, stream);
+        else if (blocks >= 512 && short_row)
+            nt ? launch<uint16_t, 128, false, true>(a, sp, r0, blocks, stream) : launch<uint16_t, 128, false, false>(a, sp, r0, blocks, stream);
         else if (blocks >= 512 || sp.per < 16384)
             nt ? forward<T, 256, true>(a, sp, r0, blocks, stream) : forward<T, 256, false>(a, sp, r0, blocks, stream);
         else forward<T, 1024, false>(a, sp, r0, blocks, stream);

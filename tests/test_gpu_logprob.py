@@ -321,7 +321,8 @@ def test_refusals():
 
 
 @pytest.mark.parametrize("rows,cols,dtype,top,start", [(2048, 50257, "f32", 20, 1), (2051, 50257, "bf16", 0, 3), (2050, 66001, "bf16", 64, 7),
-                                                       (2048, 32768, "f32", 7, 0)])
+                                                       (2048, 32768, "f32", 7, 0), (700, 5003, "bf16", 0, 1), (12000, 9001, "bf16", 0, 3),
+                                                       (600, 16384, "bf16", 0, 0), (513, 4097, "bf16", 0, 7)])
 def test_many_long_rows(rows, cols, dtype, top, start):
     """Rows that fill the chip; a few of them hold masks, infinities, NaN, one value throughout and rising values."""
     m = Matrix(rows, cols, T[dtype], cols + 2, start)
