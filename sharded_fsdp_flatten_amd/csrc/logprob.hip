@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
     constexpr int kMost = kCandidates<kT>;
     // Few rows: the last wave alone joins the waves' sums and writes the row, and it asks for the given token ahead, for all
     // instructions of the other fifteen share four SIMDs (16 x 50257 bf16 with 8 / 64 alternatives 11.0 / 14.8 -> 10.2 / 13.6
-    // us).  Where rows fill the chip a wave's wait for the token costs more (16384 x 10001 with 5: 93.8 and 98.8).
+    // us).  Where rows fill the chip a wave's wait for the token costs more (16384 x 3001: 20.9 without and 22.0 with it).
     constexpr bool kLone = kT == 1024;
     __shared__ Part parts[kW], sums;
     __shared__ Row stats;
