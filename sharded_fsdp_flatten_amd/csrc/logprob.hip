@@ -23,18 +23,28 @@ struct Part {
     float m, s, t;
 };
 // k m, rounded, held within 2^24: against it -infinity gives e = 0 instead of NaN.  What its rounding
-// lacks, at most a half, is made up once for a row (finish).  Rows whose k m lies beyond (masks of the
-// type's lowest value and nothing else) are summed again, of differences from the maximum.
+// lacks, at most a half, is made up once for a row (finish).  A run of a row whose own k m lies beyond (masks of the
+// type's lowest value and nothing else, or logits as large as a scale's 2^24) is summed again, of differences from the
+// maximum: its r is k m itself.
 constexpr float kFar = 0x1p24f;
 __device__ __forceinline__ float anchor(float m, float k) { return __builtin_amdgcn_fmed3f(m * k, -kFar, kFar); }
-__device__ __forceinline__ bool overflows(float r) { return fabsf(r) == kFar; }
+__device__ __forceinline__ bool beyond(float m, float k) {
+    return m > -INFINITY && m < INFINITY && fabsf(anchor(m, k)) == kFar;
+}
+// k m less the r of a run's sums.
+__device__ __forceinline__ float lacking(float m, float k) { return beyond(m, k) ? 0.0f : fmaf(m, k, -anchor(m, k)); }
 
 // How far the exponents of sums against `from`'s anchor move when they are taken against that of `to`, the
-// larger one; never so far that 2^shift times a sum's weight could be infinity times 0.
+// larger one; never so far that 2^shift times a sum's weight could be infinity times 0.  The anchors are what the sums
+// of lanes and waves stand against, held or not: where their run's maximum lies beyond, the sums go.
 __device__ __forceinline__ float shift(float from, float to, float k) {
-    if (from == to) return 0.0f;
-    const float r = anchor(to, k);
-    return fmaxf(overflows(r) ? (from - to) * k : anchor(from, k) - r, -1000.0f);
+    return fmaxf(anchor(from, k) - anchor(to, k), -1000.0f);
+}
+// The same between runs, where either may stand against its k m instead: (from - to) k is exact but for one rounding
+// where the two are near each other.
+__device__ __forceinline__ float run_shift(float from, float to, float k) {
+    if (from == -INFINITY || !(beyond(from, k) || beyond(to, k))) return shift(from, to, k);
+    return fmaxf((from - to) * k - lacking(from, k) + lacking(to, k), -1000.0f);
 }
 __device__ __forceinline__ Part join(Part a, Part b, float k) {
     const float m = fmaxf(a.m, b.m);
@@ -59,8 +69,7 @@ __device__ __forceinline__ Row finish(const Part& p, float scale, float k) {
     r.max = p.m * scale;
     if (r.max == -INFINITY && p.s == p.s) return Row{-INFINITY, 0.0f, 0.0f};  // nothing above -infinity
     if (r.max == INFINITY) return Row{INFINITY, NAN, NAN};
-    const float ls = logf(p.s), a = anchor(p.m, k);
-    const float lacks = overflows(a) ? 0.0f : fmaf(p.m, k, -a);
+    const float ls = logf(p.s), lacks = lacking(p.m, k);
     // against the exact k m, and then of the rounded maximum, so that the two add up
     r.logsum = ls - static_cast<float>(kLn2) * lacks + fmaf(p.m, scale, -r.max);
     r.entropy = ls - static_cast<float>(kLn2) * (p.t / p.s);
@@ -142,9 +151,10 @@ __device__ __forceinline__ float wave_max(float x) {
 }
 // Join of the wave's lanes, the same in each: moved to the common maximum, then added.  (A product fused
 // into the first addition would round differently in the two lanes that exchange it.)
+template <bool kRuns = false>
 __device__ __forceinline__ Part wave_join(Part p, float k) {
 #pragma clang fp contract(off)
-    const float m = wave_max(p.m), d = shift(p.m, m, k), f = __builtin_amdgcn_exp2f(d);
+    const float m = wave_max(p.m), d = kRuns ? run_shift(p.m, m, k) : shift(p.m, m, k), f = __builtin_amdgcn_exp2f(d);
     return Part{m, wave_sum(p.s * f), wave_sum(f * (p.t + d * p.s))};
 }
 // The largest key of the lane's quad.
@@ -455,7 +465,6 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
         }
         return q;
     };
-    const auto beyond = [&](const Part& q) { return q.m > -INFINITY && q.m < INFINITY && overflows(anchor(q.m, k)); };
     const auto again = [&](float m) {
         Part q = {m, 0.0f, 0.0f};
         for (int64_t c = t; c < n; c += kT) {
@@ -471,14 +480,14 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
         if (last) {
             r = finish(p, a.scale, k);
             if ((t & 63) == 0) {
-                far = beyond(p);
+                far = beyond(p.m, k);
                 sums = p;
                 stats = r;
-                if (!beyond(p)) put_sums(p, r);
+                if (!beyond(p.m, k)) put_sums(p, r);
             }
         }
     } else {
-        if (beyond(p)) {
+        if (beyond(p.m, k)) {
             __syncthreads();
             p = again(p.m);
         }
@@ -597,7 +606,7 @@ __global__ void __launch_bounds__(kThreads) logprob_join_kernel(LogprobFwd a, Sp
         // lowest of these
         if (a.top) least = reinterpret_cast<const uint64_t*>(ws + kPartFloats)[(a.top + sp.parts - 1) / sp.parts - 1];
     }
-    p = wave_join(p, k);
+    p = wave_join<true>(p, k);
     const Row r = finish(p, a.scale, k);
     if (t == 0) put_row(a, row, r, tok, x_tok);
     if (!a.top) return;
