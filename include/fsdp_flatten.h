@@ -854,7 +854,8 @@ FSDP_API fsdp_status fsdp_logprob_backward(const fsdp_logprob_cfg* cfg, const fs
  * the largest code.  Every value a code stands for is a bf16 number.
  * Codes are rounded at random: the code below a magnitude or the one above it, with the odds
  * of its place between them, so that a state's expected value is the exact one (to nearest, v would
- * not move while a step changes it by less than half a code, as beta2 = 0.999 does).  The random
+ * not move while a step changes it by less than half a code, as beta2 = 0.999 does).  But a v above 0
+ * takes the smallest code at least: at 0 it would leave the next update m / eps.  The random
  * number of element j of the list's tensor i in step t is a hash of (seed, t, i, j): the same
  * call gives the same bits. */
 typedef enum {
