@@ -897,7 +897,8 @@ FSDP_API fsdp_status fsdp_adam_state_bytes(int64_t numel, int64_t* bytes);
  * computes with its group's cfg, with states in 32 bits bit for bit (after the rounded multiply by
  * *grad_scale, where given).  With 8-bit states param is updated from the new m and v before
  * their rounding, and its update's square root and quotients are the hardware's: within 14 x 2^-24
- * of fsdp_adam_shard's update.
+ * of fsdp_adam_shard's update, or 2^-126, whatever v and eps are (where v is subnormal and eps does
+ * not hide its root, or eps is subnormal or above 2^96, they are as exact as the shard's).
  *   tensors : host array of n_tensors, groups : host array of n_groups; both are read during
  *             the call.
  * No two tensors may overlap.  The list is cut into as many launches as its tables need (about 80 tensors

@@ -342,22 +342,37 @@ Entry<kKey, kCopy> entry_of_tensor(const AdamTensor& a) {
     return e;
 }
 
-// kExact: the single shard's step, bit for bit.  Else (8-bit states) its square root and quotients are the
-// hardware's, to one unit in the last place each, and the update stays within 14 x 2^-24 of itself: 29.5 M elements 97 ->
-// 86 us, where the exact ones' 45 more instruction slots an element bind the kernel.
-template <bool kExact>
-__device__ __forceinline__ void adam1(float& p, float g, float& m, float& v, const AdamScalars& s, float inv_bc2s) {
+// The moments, and the parameter's decay, as the single shard's step has them, bit for bit.
+__device__ __forceinline__ void moments(float& p, float g, float& m, float& v, const AdamScalars& s) {
     p = p * s.decay;
     m = s.b1 * m + s.omb1 * g;
     const float gg = g * g;
     v = s.b2 * v + s.omb2 * gg;
+}
+// The update.  kExact: the single shard's, bit for bit.  Else (8-bit states) its square root and quotients are the
+// hardware's, to one unit in the last place each, and it stays within 14 x 2^-24 of itself: 29.5 M elements 97 ->
+// 86 us, where the exact ones' 45 more instruction slots an element bind the kernel.
+template <bool kExact>
+__device__ __forceinline__ float updated(float p, float m, float v, const AdamScalars& s, float inv_bc2s) {
     if constexpr (kExact) {
         const float den = sqrtf(v) / s.bc2s + s.eps;
-        p = p - s.step_size * (m / den);
+        return p - s.step_size * (m / den);
     } else {
         const float den = __builtin_amdgcn_sqrtf(v) * inv_bc2s + s.eps;
-        p = p - s.step_size * (m * __builtin_amdgcn_rcpf(den));
+        return p - s.step_size * (m * __builtin_amdgcn_rcpf(den));
     }
+}
+// The hardware's root takes a subnormal v as 0; its reciprocal takes a subnormal denominator as 0, and gives 0 for
+// a subnormal result.  Where either can matter the exact path is taken: groups with such an eps (but for eps a denominator
+// above 0 lies between 2^-75 and 2^91), and four elements with such a v where eps does not hide its root (at most 2^-63).
+// With v = 0 and no eps both paths give an infinity or NaN.
+__device__ __forceinline__ bool far_eps(float eps) { return eps != 0.0f && !(eps >= 0x1p-126f && eps <= 0x1p96f); }
+__device__ __forceinline__ bool hides_roots(const AdamScalars& s) { return s.eps * s.bc2s >= 0x1p-38f; }
+__device__ __forceinline__ bool any_subnormal(const float* v) {
+    uint32_t low = 0xFFFFFFFFu;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) low = min(low, __builtin_bit_cast(uint32_t, v[j]) - 1u);   // (0 comes last)
+    return low < 0x7FFFFFu;
 }
 
 // The workgroup's entry, and which of the entry's tiles of this launch it takes.  Each XCD takes runs of 64
@@ -380,6 +395,7 @@ template <typename G, State kState, bool kWhole, bool kNt>
 __device__ __forceinline__ void adam_tile(const AdamScalars& s, const float* grad_scale, const Tensor& e, int64_t base) {
     constexpr int kN = kTile<kState> / kThreads / 4;
     const float inv_bc2s = 1.0f / s.bc2s;
+    const bool rare = kState != State::kF32 && far_eps(s.eps), hidden = hides_roots(s);
     const float gs = grad_scale ? *grad_scale : 1.0f;
     const int64_t scales = (e.n + 15) / 16 * 16;
     f4 p[kN];
@@ -409,7 +425,14 @@ __device__ __forceinline__ void adam_tile(const AdamScalars& s, const float* gra
         m[h].get(mm);
         v[h].get(vv);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) adam1<kState == State::kF32>(pp[j], grad_scale ? gg[j] * gs : gg[j], mm[j], vv[j], s, inv_bc2s);
+        for (int j = 0; j < 4; ++j) moments(pp[j], grad_scale ? gg[j] * gs : gg[j], mm[j], vv[j], s);
+        if (kState == State::kF32 || rare || (!hidden && any_subnormal(vv))) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) pp[j] = updated<true>(pp[j], mm[j], vv[j], s, inv_bc2s);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) pp[j] = updated<false>(pp[j], mm[j], vv[j], s, inv_bc2s);
+        }
         put4<kWhole>(e.p + at, n, pp);
         if (e.pb) put4<kWhole>(e.pb + at, n, pp);
         uint32_t r[4];

@@ -1,5 +1,6 @@
 """AdamW with 8-bit states on the GPU where values are small: an exp_avg_sq above 0 is held as the smallest code at
-least, so that the next update stays about as large as fp32 states allow."""
+least, so that the next update stays about as large as fp32 states allow; subnormal exp_avg_sq; eps of 0, subnormal,
+tiny and huge."""
 import numpy as np
 import pytest
 import torch
@@ -98,3 +99,33 @@ def test_conversion_keeps_small_values():
     for got, which, u in zip(to, "mv", r):
         assert np.array_equal(got.cpu().numpy(), kept_state(x, u, which)), which
     assert np.array_equal(R.read_state(to[1].cpu().numpy(), n, "v") > 0, x > 0)
+
+
+@pytest.mark.parametrize("grad", ["f32", "bf16"])
+@pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-40, 1e-30, 1e-20, 2.0 ** 95, 2.0 ** 100, 2.0 ** 127])
+@pytest.mark.parametrize("size", [1e-22, 1e-20, 1e-19, 1e-17, 1.0])
+def test_subnormal_squares_and_any_eps(size, eps, grad):
+    """exp_avg_sq of 1e-45 to 1e-37 among others, where eps does not hide its root; eps whose reciprocal is
+    subnormal or infinite."""
+    c = Case([4000, 45], "8bit", grad, scale=size)
+    for step in (1, 2):
+        cfg = dict(lr=1e-2, betas=(0.9, 0.999), eps=eps, step=step)
+        F.fsdp_adam_tensors(c.list, cfg, seed=step)
+        c.reference([cfg], seed=step)
+        c.check()
+
+
+@pytest.mark.parametrize("size", [1e-21, 1e-20, 3e-19])
+def test_a_first_step_of_tiny_gradients_without_eps(size):
+    """From states of 0, as fsdp_adam_shard takes it: by about lr."""
+    n = 100
+    g = torch.full((n,), size, device=dev())
+    p = torch.ones(n, device=dev())
+    m, v = (torch.zeros(F.fsdp_adam_state_bytes(n), dtype=torch.uint8, device=dev()) for _ in range(2))
+    F.fsdp_adam_tensors(F.AdamTensors([p], [g], [m], [v], states="8bit"), dict(lr=0.25, step=1, eps=0.0))
+    q, qm, qv = torch.ones(n, device=dev()), torch.zeros(n, device=dev()), torch.zeros(n, device=dev())
+    unit = F.fsdp_unit_create(F.FSDP_FLAT, [(n,)], 1)
+    F.fsdp_adam_shard(unit, q, g, qm, qv, lr=0.25, betas=(0.9, 0.999), eps=0.0, weight_decay=0.0, step=1)
+    # the update, within 14 x 2^-24 of itself, and both results' rounding
+    assert float((p - q).abs().max()) <= (14 * 0.3 + 2) * R.U
+    assert 0.2 < float(1 - q.max()) < 0.3
