@@ -62,7 +62,8 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
 // Four values, scaled by inv = 1 / 2^s and rounded at random to codes' values: n = floor(|y| / q + r / 2^16) of
 // steps q, an eighth of the power of two below y, but no less than 2^(kMinExp - 3).  Above 2^kMinExp that is
 // adding r below the three mantissa bits that stay and cutting off what is left of them (20 bits; the sum is
-// exact either way); smaller values, and zeros, take the sum itself.
+// exact either way); smaller values, and zeros, take the sum itself.  16 bits of odds, so that one hash gives both states'
+// numbers: a rounding is low by 2^-17 of a step on average.
 // A v above 0 takes the smallest code at least.  At 0 beside an m that is not, the next update would be m / eps: of
 // gradients of 1 and 31 of 5e-6 in a group, as of an embedding's row that is seen once, those moved their parameters by 452 lr
 // in the step after; now by 0.69, with fp32 states by 0.67.  The smallest codes' m / sqrt(v) is at most 2^-9 / 224 /
