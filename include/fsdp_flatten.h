@@ -903,7 +903,7 @@ FSDP_API fsdp_status fsdp_adam_state_bytes(int64_t numel, int64_t* bytes);
  * not hide its root, or eps is subnormal or above 2^96, they are as exact as the shard's).
  *   tensors : host array of n_tensors, groups : host array of n_groups; both are read during
  *             the call.
- * No two tensors may overlap.  The list is cut into as many launches as its tables need (about 80 tensors
+ * No two tensors may overlap (not checked).  The list is cut into as many launches as its tables need (about 80 tensors
  * a launch).  A captured call keeps its step numbers, on which bias corrections and random numbers
  * rest, so that only a replay of the same step repeats it rightly.
  * Errors: FSDP_E_ARG (NULL list or groups; NULL tensors with n_tensors; a NULL buffer of a tensor
@@ -919,8 +919,9 @@ FSDP_API fsdp_status fsdp_adam_tensors(const fsdp_adam_list* list, const fsdp_ad
  * FSDP_STATE_8BIT: to save 8-bit states, or to start from others.  From 8 bits the values are exact
  * (in bf16 as well); to 8 bits they are rounded as by a step of the number `step` with the
  * same seed.  Only numel, exp_avg and exp_avg_sq of the tensors are read; exp_avg_sq must hold
- * no negative values.  numel has to be the same in both lists, and no buffer of one may overlap another.
- * Errors: FSDP_E_ARG (NULL arrays or buffers), FSDP_E_RANGE (n_tensors, the formats, numel, step < 1),
+ * no negative values.  numel has to be the same in both lists, and no buffer of `to` may overlap another of either list.
+ * Errors: FSDP_E_ARG (NULL arrays or buffers), FSDP_E_RANGE (n_tensors, the formats, numel, step < 1, buffers that
+ * overlap),
  * FSDP_E_ALIGN, FSDP_E_OVERFLOW, FSDP_E_HIP.
  */
 FSDP_API fsdp_status fsdp_adam_convert(int32_t n_tensors, const fsdp_adam_tensor* from,

@@ -8,6 +8,7 @@
 
 #include <hip/hip_runtime_api.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <memory>
@@ -399,6 +400,28 @@ fsdp_status check_state(const fsdp_adam_tensor& t, int32_t format) {
     const size_t e = format == FSDP_STATE_F32 ? 4 : format == FSDP_STATE_BF16 ? 2 : 1;
     const fsdp_status s = check_buf(t.exp_avg, t.numel, e, "a tensor's exp_avg");
     return s != FSDP_OK ? s : check_buf(t.exp_avg_sq, t.numel, e, "a tensor's exp_avg_sq");
+}
+
+// Bytes from `at` to `end`.
+struct Span {
+    uintptr_t at, end;
+};
+Span state_span(const void* p, int64_t n, int32_t format) {
+    const int64_t bytes = format == FSDP_STATE_8BIT ? fsdp::state_bytes(n) : n * (format == FSDP_STATE_F32 ? 4 : 2);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    return {at, at + static_cast<uintptr_t>(bytes)};
+}
+// Whether two of the written spans, or a written and a read one, have bytes in common.
+bool spans_meet(std::vector<Span>& written, const std::vector<Span>& read) {
+    const auto before = [](const Span& x, const Span& y) { return x.at < y.at; };
+    if (!std::is_sorted(written.begin(), written.end(), before)) std::sort(written.begin(), written.end(), before);
+    for (size_t i = 1; i < written.size(); ++i)
+        if (written[i - 1].end > written[i].at) return true;
+    for (const Span& r : read) {  // the last that begins before it ends: those before it end earlier still
+        const auto next = std::lower_bound(written.begin(), written.end(), Span{r.end, 0}, before);
+        if (next != written.begin() && (next - 1)->end > r.at) return true;
+    }
+    return false;
 }
 
 fsdp::RowsIn in(const fsdp_rows& r) { return {r.data, r.pitch}; }
@@ -1109,7 +1132,7 @@ fsdp_status fsdp_adam_state_bytes(int64_t numel, int64_t* bytes) {
         if (!bytes) return fail(FSDP_E_ARG, "bytes is NULL");
         const fsdp_status s = check_numel(numel);
         if (s != FSDP_OK) return s;
-        *bytes = fsdp::state_scales(numel) + (numel + fsdp::kStateGroup - 1) / fsdp::kStateGroup;
+        *bytes = fsdp::state_bytes(numel);
         return ok();
     });
 }
@@ -1184,6 +1207,19 @@ fsdp_status fsdp_adam_convert(int32_t n_tensors, const fsdp_adam_tensor* from, i
             t.push_back({from[i].numel, from[i].exp_avg, from[i].exp_avg_sq, to[i].exp_avg, to[i].exp_avg_sq,
                          to_format == FSDP_STATE_8BIT ? fsdp::adam_key(seed, step, i) : 0});
         }
+        std::vector<Span> written, read;
+        written.reserve(2 * t.size());
+        read.reserve(2 * t.size());
+        for (const auto& x : t) {
+            written.push_back(state_span(x.m_to, x.n, to_format));
+            read.push_back(state_span(x.m, x.n, from_format));
+        }
+        for (const auto& x : t) {
+            written.push_back(state_span(x.v_to, x.n, to_format));
+            read.push_back(state_span(x.v, x.n, from_format));
+        }
+        if (spans_meet(written, read))
+            return fail(FSDP_E_RANGE, "a buffer that is written overlaps another");
         const auto state = [](int32_t f) {
             return f == FSDP_STATE_F32 ? fsdp::State::kF32 : f == FSDP_STATE_BF16 ? fsdp::State::kBF16 : fsdp::State::k8Bit;
         };

@@ -70,6 +70,7 @@ struct AdamTensor {
 };
 // Bytes from the start of an 8-bit state of n elements to its scales.
 inline int64_t state_scales(int64_t n) { return (n + 15) / 16 * 16; }
+inline int64_t state_bytes(int64_t n) { return state_scales(n) + (n + kStateGroup - 1) / kStateGroup; }
 hipError_t launch_adam_tensors(const std::vector<AdamTensor>& t, const AdamScalars* groups, int n_groups,
                                bool state8, bool grad_bf16, const float* grad_scale, const float* skip,
                                hipStream_t stream);

@@ -387,7 +387,8 @@ def _adam_cfg(lr, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0) -> bytes
 
 def fsdp_adam_convert(src: AdamTensors, dst: AdamTensors, *, seed: int = 0, step: int = 1,
                       stream=None) -> None:
-    """Copy the states of one list to another of another format; one of the two is "8bit"."""
+    """Copy the states of one list to another of another format; one of the two is "8bit".  No state of dst may
+    overlap another of either list."""
     for t, name in ((src, "src"), (dst, "dst")):
         if not isinstance(t, AdamTensors):
             raise TypeError("%s must be an AdamTensors, got %r" % (name, type(t)))
