@@ -572,6 +572,7 @@ hipError_t convert(const std::vector<StateCopy>& list, hipStream_t stream) {
         [&](uint32_t tiles) { adam_convert_kernel<kFrom, kTo><<<dim3(tiles), kThreads, 0, stream>>>(t); });
 }
 
+// The output function of SplitMix64 (Steele, Lea and Flood, 2014), with its published multipliers.
 uint64_t mix64(uint64_t k) {
     k = (k ^ (k >> 30)) * 0xBF58476D1CE4E5B9ull;
     k = (k ^ (k >> 27)) * 0x94D049BB133111EBull;

@@ -1043,9 +1043,7 @@ fsdp_status fsdp_logprob_workspace(int64_t rows, int64_t cols, int32_t top, int6
         if (!n_floats) return fail(FSDP_E_ARG, "n_floats is NULL");
         fsdp_status s;
         if ((s = check_extent(rows, cols)) != FSDP_OK || (s = check_top(cols, top)) != FSDP_OK) return s;
-        const int64_t n = fsdp::logprob_workspace_floats(rows, cols, top);
-        if (n < 0) return fail(FSDP_E_OVERFLOW, "the workspace's size overflows int64");
-        *n_floats = n;
+        *n_floats = fsdp::logprob_workspace_floats(rows, cols, top);
         return ok();
     });
 }

@@ -46,13 +46,6 @@ __device__ __forceinline__ float run_shift(float from, float to, float k) {
     if (from == -INFINITY || !(beyond(from, k) || beyond(to, k))) return shift(from, to, k);
     return fmaxf((from - to) * k - lacking(from, k) + lacking(to, k), -1000.0f);
 }
-__device__ __forceinline__ Part join(Part a, Part b, float k) {
-    const float m = fmaxf(a.m, b.m);
-    const float da = shift(a.m, m, k), db = shift(b.m, m, k);
-    const float fa = __builtin_amdgcn_exp2f(da), fb = __builtin_amdgcn_exp2f(db);
-    return Part{m, a.s * fa + b.s * fb, fa * (a.t + da * a.s) + fb * (b.t + db * b.s)};
-}
-
 // e u without 0 x infinity: far below -149 e is 0; a NaN stays one
 __device__ __forceinline__ float weighted(float e, float u) { return e * fmaxf(u, -200.0f); }
 
@@ -218,7 +211,7 @@ struct Split {
     uint32_t parts;
     int64_t per;
 };
-// What a run leaves in the workspace (then its `top` keys in falling order, 0 where it has fewer).
+// What a run leaves in the workspace (then its `top` keys in falling order; a run is longer than that).
 constexpr int kPartFloats = 4;
 
 __device__ __forceinline__ float* part_at(const LogprobFwd& a, const Split& sp, int64_t row, uint32_t part) {
@@ -578,8 +571,6 @@ __global__ void __launch_bounds__(kT) logprob_fwd_kernel(LogprobFwd a, Split sp,
             const int place_of = larger<kL>(keys, got, key);
             if (t % kL == 0 && place_of < a.top) put(place_of, key);
         }
-        // a run shorter than the alternatives wanted
-        for (uint32_t i = got + t; i < static_cast<uint32_t>(a.top); i += kT) put(static_cast<int>(i), 0);
     }
 }
 
@@ -615,7 +606,7 @@ __global__ void __launch_bounds__(kThreads) logprob_join_kernel(LogprobFwd a, Sp
     __syncthreads();
     for (uint32_t i = t; i < sp.parts * a.top; i += kThreads) {
         const uint64_t key = reinterpret_cast<const uint64_t*>(part_at(a, sp, row, i / a.top) + kPartFloats)[i % a.top];
-        if (key == 0 || key < least) continue;
+        if (key < least) continue;
         keys[atomicAdd(&count, 1u)] = key;
     }
     __syncthreads();
@@ -722,6 +713,8 @@ Split plan_split(int64_t rows, int64_t cols) {
     int64_t parts = std::min<int64_t>({cols / kRun, kFill / std::max<int64_t>(rows, 1), kMaxParts});
     parts = std::max<int64_t>(parts, 1);
     const int64_t per = ((cols + parts - 1) / parts + kV - 1) / kV * kV;
+    // runs differ by the last one's lack of up to 8 (parts - 1) columns: none is shorter than the alternatives wanted
+    static_assert(kRun - 8 * (kMaxParts - 1) >= kMaxTop);
     return {static_cast<uint32_t>((cols + per - 1) / per), per};
 }
 
@@ -743,14 +736,16 @@ hipError_t forward_rows(const LogprobFwd& a, hipStream_t stream) {
     // Past the cache where a call's logits outgrow it, rows at any element: 4096 x 50257 bf16 (412 MB), 256 threads, cached 75.0,
     // nt 68.4 us (64 with 512 threads and whole lines); 2048 x 50257 fp32 72.1 and 66.7 (62).
     const bool nt = a.rows * a.cols * static_cast<int64_t>(sizeof(T)) >= kNtBytes;
-    // Threads of a workgroup.  A wave a row, against 256 threads: 16384 x 3000 bf16 19.6 and 32 us; 16384 x 6000 37.8 and 40.5, but
-    // 99 and 85 with 20 alternatives.  1024, against 256, where workgroups are few: 200 x 262144 21 and 33.7, 200 x 50257 7.1 and
-    // 8.2; not of 600 x 50257, 14.6 and 13.4 (27.6 and 22.6 with alternatives), nor of 200 x 12000 with alternatives, 9.5 and 8.8.
-    // 512, against 256, where many long rows keep the chip full: 4096 x 50257 bf16 64.8 and 67.2, 8192 x 33000 84.1 and 88.1, fp32 2048 x 50257
-    // with 20 alternatives 76.8 and 80.7; not of 16384 x 20000 bf16, 119 and 103, 1024 x 131072, 47.0 and 43.7, nor of 4096 x 50257
-    // with 20 alternatives, 91.5 and 86.7.
-    // 128, against 256, for short bf16 rows without alternatives: 16384 x 5001 34.8 and 41.7, x 10001 55.9 and 66.2, x 16001 86.8 and 89.3;
-    // not x 20001, 103.2 and 102.7, with alternatives (x 6001, 20: 93.0 and 84.5), or in fp32 (x 8001 87.7 and 82.6).
+    // Threads of a workgroup, each choice against 256 (us, its own time first; bf16 but where said):
+    //   64, a wave a row, up to kShort columns: 16384 x 3000 19.6 / 32; x 6000 37.8 / 40.5, but 99 / 85 with 20 alternatives.
+    //   512, from 2048 long rows past the cache: 4096 x 50257 64.2 / 65.0, 2560 x 50257 41.7 / 43.9, 8192 x 33000 84.1 / 88.1.  Not
+    //     16384 x 20000, 119 / 103, 1024 x 131072, 47.0 / 43.7, or 4096 x 50257 with 20 alternatives, 91.5 / 86.7.  In fp32 at
+    //     50257 columns it makes little difference on either side of the border: 1536 rows 47.5 / 47.7, 2048 61.8 / 62.0, 2560
+    //     76.7 / 76.4; with 20 alternatives 57.2 / 55.7, 73.1 / 74.7, 87.8 / 87.2.
+    //   128, short rows without alternatives: 16384 x 5001 34.8 / 41.7, x 10001 55.9 / 66.2, x 16001 86.8 / 89.3.  Not x 20001,
+    //     103.2 / 102.7, x 6001 with 20 alternatives, 93.0 / 84.5, or fp32, x 8001 87.7 / 82.6.
+    //   1024, under 512 workgroups of 16384 columns and more: 200 x 262144 21 / 33.7, 200 x 50257 7.1 / 8.2.  Not 600 x 50257, 14.6 /
+    //     13.4 (27.6 / 22.6 with alternatives), or 200 x 12000 with alternatives, 9.5 / 8.8.
     const int64_t long_row = int64_t{a.top ? 128 : 64} << 10;
     const bool short_row = sizeof(T) == 2 && !a.top && sp.per <= 16384;
     for (int64_t r0 = 0; r0 < a.rows; r0 += most) {

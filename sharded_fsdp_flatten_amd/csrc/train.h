@@ -52,7 +52,7 @@ struct LogprobBwd {
     const float *dl, *dh;        // either may be nullptr
     const float *max, *logsum, *entropy;
 };
-int64_t logprob_workspace_floats(int64_t rows, int64_t cols, int32_t top);  // -1: overflows int64
+int64_t logprob_workspace_floats(int64_t rows, int64_t cols, int32_t top);
 hipError_t launch_logprob_forward(const LogprobFwd& a, hipStream_t stream);
 hipError_t launch_logprob_backward(const LogprobBwd& a, hipStream_t stream);
 
@@ -83,8 +83,7 @@ struct StateCopy {
     uint32_t key;
 };
 hipError_t launch_adam_convert(const std::vector<StateCopy>& t, State from, State to, hipStream_t stream);
-// Key of a tensor's random numbers: a 64-bit mixing function (xor-shift-multiply) of seed, step and the
-// tensor's place in its list.
+// Key of a tensor's random numbers: a 64-bit hash of seed, step and the tensor's place in its list.
 uint32_t adam_key(uint64_t seed, int64_t step, int64_t tensor);
 
 }  // namespace fsdp
