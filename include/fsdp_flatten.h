@@ -731,15 +731,16 @@ FSDP_API fsdp_status fsdp_rotary_freqs(int64_t rot, double base, int32_t scaling
 /*
  * Rotate pair (a, b) of every head of q and k at position x by the angle w = x f_i:
  *   (a, b) -> scale (a cos w - b sin w, a sin w + b cos w)
- * w is computed and reduced to a turn in binary64 (within |w| 2^-51), its fraction of a turn rounded to
- * binary32 (2^-26 of a turn); cosine and sine are binary32, results rounded once.  Elements behind the
- * rotated ones are copied bit for bit (in place: left alone).  In place, no other operand may overlap.
- * An output's heads, tokens and sequences must not overlap: of the pitches with more than one
- * entry, each from the smallest up must pass the extent of those before it.
+ * w is computed and reduced to a turn in binary64 (within |w| 2^-51), its fraction of a
+ * turn rounded to binary32 (2^-26 of a turn); cosine and sine are binary32, results
+ * rounded once.  Elements behind the rotated ones are copied bit for bit (in place: left
+ * alone).  In place, no other operand may overlap. An output's heads, tokens and sequences
+ * must not overlap: of the pitches with more than one entry, each from the smallest up
+ * must pass the extent of those before it.
  * batch, tokens or heads + kv_heads == 0: nothing is done.
- * Errors: FSDP_E_ARG (NULL cfg or io; with elements, a NULL buffer or freqs),
- * FSDP_E_RANGE (sizes negative, rot, head_dim, dtype, layout, scale, pitches),
- * FSDP_E_ALIGN, FSDP_E_OVERFLOW (an extent, a position from start or the number of elements beyond
+ * Errors: FSDP_E_ARG (NULL cfg or io; with elements, a NULL buffer or freqs), FSDP_E_RANGE
+ * (sizes negative, rot, head_dim, dtype, layout, scale, pitches), FSDP_E_ALIGN,
+ * FSDP_E_OVERFLOW (an extent, a position from start or the number of elements beyond
  * int64), FSDP_E_HIP.
  */
 FSDP_API fsdp_status fsdp_rotary_forward(const fsdp_rotary_cfg* cfg, const fsdp_rotary_io* io,
@@ -802,22 +803,22 @@ FSDP_API fsdp_status fsdp_logprob_workspace(int64_t rows, int64_t cols, int32_t 
  *   entropy = -sum over j of p_j log p_j,  p_j = e^(z_j - max - logsum)
  *   top_token, top_logprob: the `top` largest logits' columns and log probabilities, in falling
  *             order, equal logits by rising column
- * max is rounded, and logsum is of the rounded one: their sum is the logarithm of the sum of
- * e^z_j.  Sums are binary32; their order depends on rows, cols, dtype, the logits' alignment and whether top is 0, and on nothing
- * else: the same call gives the same bits.
+ * max is rounded, and logsum is of the rounded one: their sum is the logarithm of the sum
+ * of e^z_j.  Sums are binary32; their order depends on rows, cols, dtype, the logits'
+ * alignment and whether top is 0, and on nothing else: the same call gives the same bits.
  * A token outside [0, cols) is none (a padded position): its logprob is 0.
- * Logits of -infinity are masked: their probability is 0, and their logprob -infinity.  A row that holds
- * nothing else (or only logits whose product with scale is -infinity in binary32) has max -infinity,
- * logsum 0, entropy 0 and every logprob -infinity.  A row that holds a NaN or +infinity (or a product that
- * is) has NaN for logsum, entropy and every logprob (tokens that are none apart); a NaN is ranked as
- * -infinity.
+ * Logits of -infinity are masked: their probability is 0, and their logprob -infinity.  A
+ * row that holds nothing else (or only logits whose product with scale is -infinity in
+ * binary32) has max -infinity, logsum 0, entropy 0 and every logprob -infinity.  A row
+ * that holds a NaN or +infinity (or a product that is) has NaN for logsum, entropy and
+ * every logprob (tokens that are none apart); a NaN is ranked as -infinity.
  * Every partial result read was written by the same call: the workspace needs no clearing,
  * and calls that share one must be ordered.
  * rows or cols == 0: nothing is written.
- * Errors: FSDP_E_ARG (NULL cfg or io; with elements, NULL logits, max or logsum, one of tokens
- * and logprob without the other, top without its buffers, a NULL workspace where one is needed),
- * FSDP_E_RANGE (sizes, dtype, top, scale, a pitch, workspace_len), FSDP_E_ALIGN,
- * FSDP_E_OVERFLOW, FSDP_E_HIP.
+ * Errors: FSDP_E_ARG (NULL cfg or io; with elements, NULL logits, max or logsum, one of
+ * tokens and logprob without the other, top without its buffers, a NULL workspace where
+ * one is needed), FSDP_E_RANGE (sizes, dtype, top, scale, a pitch, workspace_len),
+ * FSDP_E_ALIGN, FSDP_E_OVERFLOW, FSDP_E_HIP.
  */
 FSDP_API fsdp_status fsdp_logprob_forward(const fsdp_logprob_cfg* cfg, const fsdp_logprob_fwd* io,
                                           void* stream);
@@ -826,40 +827,41 @@ FSDP_API fsdp_status fsdp_logprob_forward(const fsdp_logprob_cfg* cfg, const fsd
  * Gradient of the logits from those of the log probabilities (dl) and entropies (dh):
  *   dlogits_j = scale (dl ([j = t] - p_j) - dh p_j (log p_j + entropy))
  * dl counts as 0 for a token that is none.  Where both dl and dh are 0 (or not given), and
- * where the forward pass found no logit above -infinity, the row's gradient is 0 whatever the
- * logits hold, and they are not read.
- * Errors: FSDP_E_ARG (NULL cfg or io; neither dlogprob nor dentropy; with elements, NULL logits,
- * dlogits, max or logsum, dlogprob without tokens, dentropy without entropy), FSDP_E_RANGE,
- * FSDP_E_ALIGN, FSDP_E_OVERFLOW, FSDP_E_HIP.
+ * where the forward pass found no logit above -infinity, the row's gradient is 0 whatever
+ * the logits hold, and they are not read.
+ * Errors: FSDP_E_ARG (NULL cfg or io; neither dlogprob nor dentropy; with elements, NULL
+ * logits, dlogits, max or logsum, dlogprob without tokens, dentropy without entropy),
+ * FSDP_E_RANGE, FSDP_E_ALIGN, FSDP_E_OVERFLOW, FSDP_E_HIP.
  */
 FSDP_API fsdp_status fsdp_logprob_backward(const fsdp_logprob_cfg* cfg, const fsdp_logprob_bwd* io,
                                            void* stream);
 
 /* ------------------------------------------------------------------------
- * AdamW over many tensors: the shards of a rank's units (or the row shards of
- * its parameters) in a few launches, each tensor with its group's hyper-parameters, states in
+ * AdamW over many tensors: the shards of a rank's units (or the row shards of its
+ * parameters) in a few launches, each tensor with its group's hyper-parameters, states in
  * 32 or 8 bits.
  * ------------------------------------------------------------------------ */
 
 /* How exp_avg (m) and exp_avg_sq (v) are held.  In 8 bits a state of n elements is one buffer:
- * n codes, filled up to a multiple of 16 bytes, then ceil(n / 32) scale bytes, one for every 32
- * elements in order (the last group may be shorter).  A scale byte b stands for 2^(b - 127); an
- * element is its code times that.  255: the group held an infinity or a NaN, and reads back as NaN
- * throughout.  All bytes 0 is a state of zeros.
+ * n codes, filled up to a multiple of 16 bytes, then ceil(n / 32) scale bytes, one for
+ * every 32 elements in order (the last group may be shorter).  A scale byte b stands for
+ * 2^(b - 127); an element is its code times that.  255: the group held an infinity or a
+ * NaN, and reads back as NaN throughout.  All bytes 0 is a state of zeros.
  *   m: 8-bit floats with a sign, 4 exponent bits of bias 7, 3 mantissa bits, largest 448;
  *      scales from 2^-124
  *   v: 8-bit floats without a sign, 5 exponent bits of bias 15, 3 mantissa bits, largest 61440
  *      (the 8 bits below the sign of a binary16 number); scales from 2^-116
- * The scale is the smallest power of two at which the group's largest magnitude is not above
- * the largest code.  Every value a code stands for is a bf16 number.
- * Codes are rounded at random: the code below a magnitude or the one above it, with the odds
- * of its place between them (to nearest, v would not move while a step changes it by less than half a
- * code, as beta2 = 0.999 does).  The odds have 16 bits, cut off: a state's expected value is the exact
- * one less 0 to 2^-16 of the distance of its codes, 2^-17 on average.  Over the 1 / (1 - beta2) steps
- * that v remembers this adds up to 0.05 to 0.1% of v at beta2 = 0.999, and to ten times that at 0.9999.
- * A v above 0 takes the smallest code at least: at 0 it would leave the next update m / eps.
- * The random number of element j of the list's tensor i in step t is a hash of (seed, t, i, j): the
- * same call gives the same bits. */
+ * The scale is the smallest power of two at which the group's largest magnitude is not
+ * above the largest code.  Every value a code stands for is a bf16 number.
+ * Codes are rounded at random: the code below a magnitude or the one above it, with the
+ * odds of its place between them (to nearest, v would not move while a step changes it by
+ * less than half a code, as beta2 = 0.999 does).  The odds have 16 bits, cut off: a
+ * state's expected value is the exact one less 0 to 2^-16 of the distance of its codes,
+ * 2^-17 on average.  Over the 1 / (1 - beta2) steps that v remembers this adds up to 0.05
+ * to 0.1% of v at beta2 = 0.999, and to ten times that at 0.9999. A v above 0 takes the
+ * smallest code at least: at 0 it would leave the next update m / eps. The random number
+ * of element j of the list's tensor i in step t is a hash of (seed, t, i, j): the same
+ * call gives the same bits. */
 typedef enum {
     FSDP_STATE_F32 = 1,
     FSDP_STATE_8BIT = 2,
@@ -895,34 +897,37 @@ typedef struct {
 FSDP_API fsdp_status fsdp_adam_state_bytes(int64_t numel, int64_t* bytes);
 
 /*
- * One AdamW step over a list of tensors: for each of them what fsdp_adam_shard
- * computes with its group's cfg, with states in 32 bits bit for bit (after the rounded multiply by
- * *grad_scale, where given).  With 8-bit states param is updated from the new m and v before
- * their rounding, and its update's square root and quotients are the hardware's: within 14 x 2^-24
- * of fsdp_adam_shard's update, or 2^-126, whatever v and eps are (where v is subnormal and eps does
- * not hide its root, or eps is subnormal or above 2^96, they are as exact as the shard's).
+ * One AdamW step over a list of tensors: for each of them what fsdp_adam_shard computes
+ * with its group's cfg, with states in 32 bits bit for bit (after the rounded multiply by
+ * *grad_scale, where given).  With 8-bit states param is updated from the new m and v
+ * before their rounding, and its update's square root and quotients are the hardware's:
+ * within 14 x 2^-24 of fsdp_adam_shard's update, or 2^-126, whatever v and eps are (where
+ * v is subnormal and eps does not hide its root, or eps is subnormal or above 2^96, they
+ * are as exact as the shard's).
  *   tensors : host array of n_tensors, groups : host array of n_groups; both are read during
  *             the call.
- * No two tensors may overlap (not checked).  The list is cut into as many launches as its tables need (about 80 tensors
- * a launch).  A captured call keeps its step numbers, on which bias corrections and random numbers
- * rest, so that only a replay of the same step repeats it rightly.
- * Errors: FSDP_E_ARG (NULL list or groups; NULL tensors with n_tensors; a NULL buffer of a tensor
- * with elements), FSDP_E_RANGE (n_tensors negative, n_groups outside
- * 1..FSDP_ADAM_MAX_GROUPS, state_format, grad_dtype, a numel negative, a tensor's group, an address of more
- * than 48 bits, a group's values as for fsdp_adam_shard), FSDP_E_ALIGN, FSDP_E_OVERFLOW (numel > 2^40), FSDP_E_HIP.
+ * No two tensors may overlap (not checked).  The list is cut into as many launches as its
+ * tables need (about 80 tensors a launch).  A captured call keeps its step numbers, on
+ * which bias corrections and random numbers rest, so that only a replay of the same step
+ * repeats it rightly.
+ * Errors: FSDP_E_ARG (NULL list or groups; NULL tensors with n_tensors; a NULL buffer of a
+ * tensor with elements), FSDP_E_RANGE (n_tensors negative, n_groups outside
+ * 1..FSDP_ADAM_MAX_GROUPS, state_format, grad_dtype, a numel negative, a tensor's group,
+ * an address of more than 48 bits, a group's values as for fsdp_adam_shard), FSDP_E_ALIGN,
+ * FSDP_E_OVERFLOW (numel > 2^40), FSDP_E_HIP.
  */
 FSDP_API fsdp_status fsdp_adam_tensors(const fsdp_adam_list* list, const fsdp_adam_tensor* tensors,
                                        const fsdp_adamw_cfg* groups, void* stream);
 
 /*
  * Copy the states of a list of tensors from one format to another, of which one has to be
- * FSDP_STATE_8BIT: to save 8-bit states, or to start from others.  From 8 bits the values are exact
- * (in bf16 as well); to 8 bits they are rounded as by a step of the number `step` with the
- * same seed.  Only numel, exp_avg and exp_avg_sq of the tensors are read; exp_avg_sq must hold
- * no negative values.  numel has to be the same in both lists, and no buffer of `to` may overlap another of either list.
- * Errors: FSDP_E_ARG (NULL arrays or buffers), FSDP_E_RANGE (n_tensors, the formats, numel, step < 1, buffers that
- * overlap),
- * FSDP_E_ALIGN, FSDP_E_OVERFLOW, FSDP_E_HIP.
+ * FSDP_STATE_8BIT: to save 8-bit states, or to start from others.  From 8 bits the values
+ * are exact (in bf16 as well); to 8 bits they are rounded as by a step of the number
+ * `step` with the same seed.  Only numel, exp_avg and exp_avg_sq of the tensors are read;
+ * exp_avg_sq must hold no negative values.  numel has to be the same in both lists, and no
+ * buffer of `to` may overlap another of either list.
+ * Errors: FSDP_E_ARG (NULL arrays or buffers), FSDP_E_RANGE (n_tensors, the formats,
+ * numel, step < 1, buffers that overlap), FSDP_E_ALIGN, FSDP_E_OVERFLOW, FSDP_E_HIP.
  */
 FSDP_API fsdp_status fsdp_adam_convert(int32_t n_tensors, const fsdp_adam_tensor* from,
                                        int32_t from_format, const fsdp_adam_tensor* to,
