@@ -287,7 +287,9 @@ class _Held:
             for i, t in enumerate(tensors):
                 if t is not None:
                     s = t.untyped_storage()
-                    storages.setdefault(s._cdata, (name, i, s))
+                    k = s._cdata
+                    if k not in storages:
+                        storages[k] = name, i, s
             self.upto[name] = len(storages)
         self.names = [x[:2] for x in storages.values()]
         self.probes = [f for _, _, s in storages.values() for f in (s.data_ptr, s.nbytes)]   # (which hold them)
